@@ -21,7 +21,9 @@ POOL_LIB_PATH = os.path.join(_PKG, "librssm_pool.so")
 RSSM_F32, RSSM_BF16, RSSM_F16, RSSM_I8, RSSM_F8E4M3 = 0, 1, 2, 3, 4
 RSSM_OK, RSSM_ERR_INVALID_ARGUMENT, RSSM_ERR_UNSUPPORTED, RSSM_ERR_HIP = 0, 1, 2, 3
 EXPORTS = ("rssm_materialize", "rssm_materialize_checkpoints", "rssm_last_error", "rssm_materialize_launch_config",
-           "rssm_debug_encode_rows", "rssm_debug_row_scales", "rssm_gdn_commit", "rssm_ssu_decode")
+           "rssm_debug_encode_rows", "rssm_debug_row_scales", "rssm_gdn_commit", "rssm_ssu_decode",
+           "rssm_linear_attention", "rssm_linear_attention_step", "rssm_linear_attention_workspace",
+           "rssm_paged_append", "rssm_paged_attention", "rssm_paged_attention_workspace", "rssm_block_norm")
 POOL_EXPORTS = ("rssm_pool_alloc", "rssm_pool_free", "rssm_torch_pool_alloc", "rssm_torch_pool_free")
 RSSM_MAX_CHECKPOINTS = 4
 RSSM_SSU_MAX_TOKENS = 8
@@ -80,6 +82,46 @@ class RssmSsuTables(ctypes.Structure):
         "slots", "ring_start", "num_buffered")]
 
 
+class RssmLinearDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_seqs", "num_tokens", "num_heads", "heads_per_group", "dim", "dstate", "num_slots", "pad_slot_id",
+        "max_seq_len", "state_dtype", "input_dtype", "dt_softplus")] + [
+        (n, ctypes.c_int64) for n in (
+            "state_slot_stride", "x_token_stride", "B_token_stride", "C_token_stride", "dt_token_stride",
+            "z_token_stride", "y_token_stride", "workspace_bytes")]
+
+
+class RssmLinearTables(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "state", "A", "D", "dt_bias", "x", "B", "C", "dt", "z", "y", "slots", "seq_start", "load_state", "workspace")]
+
+
+class RssmPagedDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_seqs", "num_tokens", "num_q_heads", "num_kv_heads", "head_dim", "page_size", "num_pages", "max_pages",
+        "max_seq_len", "max_kv_len", "window", "sinks", "dtype")] + [("scale", ctypes.c_float)] + [
+        (n, ctypes.c_int64) for n in (
+            "page_stride", "row_stride", "head_stride", "q_token_stride", "out_token_stride", "new_token_stride",
+            "table_stride", "workspace_bytes")]
+
+
+class RssmPagedTables(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "k_cache", "v_cache", "k_new", "v_new", "q", "out", "lse", "page_table", "seq_start", "kv_len", "workspace")]
+
+
+class RssmNormDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "channels", "groups", "input_dtype", "residual_dtype")] + [
+        ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float)] + [
+        (n, ctypes.c_int64) for n in (
+            "y_row_stride", "z_row_stride", "residual_row_stride", "residual_out_row_stride", "normed_row_stride")]
+
+
+class RssmNormTables(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "y", "z", "residual", "post_weight", "pre_weight", "channel_scale", "residual_out", "normed")]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -95,6 +137,19 @@ def _load():
     lib.rssm_gdn_commit.restype = ctypes.c_int
     lib.rssm_ssu_decode.argtypes = [ctypes.POINTER(RssmSsuDesc), ctypes.POINTER(RssmSsuTables), ctypes.c_void_p]
     lib.rssm_ssu_decode.restype = ctypes.c_int
+    for name, desc, tables in (("rssm_linear_attention", RssmLinearDesc, RssmLinearTables),
+                               ("rssm_linear_attention_step", RssmLinearDesc, RssmLinearTables),
+                               ("rssm_paged_append", RssmPagedDesc, RssmPagedTables),
+                               ("rssm_paged_attention", RssmPagedDesc, RssmPagedTables),
+                               ("rssm_block_norm", RssmNormDesc, RssmNormTables)):
+        fn = getattr(lib, name)
+        fn.argtypes = [ctypes.POINTER(desc), ctypes.POINTER(tables), ctypes.c_void_p]
+        fn.restype = ctypes.c_int
+    for name, desc in (("rssm_linear_attention_workspace", RssmLinearDesc),
+                       ("rssm_paged_attention_workspace", RssmPagedDesc)):
+        fn = getattr(lib, name)
+        fn.argtypes = [ctypes.POINTER(desc), ctypes.POINTER(ctypes.c_int64)]
+        fn.restype = ctypes.c_int
     lib.rssm_last_error.argtypes = []
     lib.rssm_last_error.restype = ctypes.c_char_p
     lib.rssm_materialize_launch_config.argtypes = [ctypes.POINTER(RssmDesc), ctypes.POINTER(ctypes.c_int32),
@@ -469,6 +524,288 @@ class SsuDecodeCall:
         st = _lib.rssm_ssu_decode(self._refs[0], self._refs[1], self._stream)
         if st != RSSM_OK:
             raise RssmError(st, rssm_last_error())
+
+
+def _rows(t, name: str, dtype, shape, device):
+    """(address, token stride) of a [tokens, ...] tensor whose rows are dense inside."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    want = 1
+    for n, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and stride != want:
+            raise ValueError(f"{name} must be dense inside a row (strides {t.stride()})")
+        want *= n
+    # one row: its stride says nothing, and an expanded row would be below the dense size
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else want)
+
+
+def _device_of(t, name: str):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor (got {t.device})")
+    return t.device
+
+
+def _same_device(device, tensors) -> None:
+    for name, t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device} (got {t.device})")
+
+
+def _aligned_stride(stride: int, elem: int) -> int:
+    """A dense row stride rounded up to 16 bytes (for a tensor of one row or
+    none, where any legal value does)."""
+    step = 16 // elem
+    return (stride + step - 1) // step * step
+
+
+def _workspace(nbytes: int, given, device, stream):
+    """The caller's workspace after a check, or a new one that lives on the call's stream."""
+    import torch
+    if given is not None:
+        if _device_of(given, "workspace") != device or not given.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        return given
+    if nbytes == 0:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(s):      # the allocator reuses it in that stream's order
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _launch(fn, desc, tab, device, stream) -> None:
+    """One library call on `stream` (default: torch's current stream of the tensors' device)."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        _check(fn(ctypes.byref(desc), ctypes.byref(tab), _stream_handle(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(ctypes.byref(desc), ctypes.byref(tab), _stream_handle(stream)))
+
+
+def _linear_marshal(state, A, x, B, C, dt, y, slots, seq_start=None, *, max_seq_len=None, load_state=None, D=None,
+                    dt_bias=None, z=None, dt_softplus: bool = True, pad_slot_id: int = -1):
+    import torch
+    dev = _device_of(state, "state")
+    if state.dim() != 4:
+        raise ValueError("state must be a pool [slots, H, dim, dstate]")
+    if x.dim() != 3 or B.dim() != 3:
+        raise ValueError("x must be [tokens, H, dim] and B [tokens, G, dstate]")
+    S, H, dim, dstate = state.shape
+    N, G = x.shape[0], B.shape[1]
+    if G < 1 or H % G != 0:
+        raise ValueError(f"the group count of B ({G}) must divide the head count ({H})")
+    if S and (state.stride(3) != 1 or state.stride(2) != dstate or (H > 1 and state.stride(1) != dim * dstate)):
+        raise ValueError("state must be dense inside a slot")
+    f32, i32, idt = torch.float32, torch.int32, x.dtype
+    R = slots.shape[0]
+    xp, xs = _rows(x, "x", idt, (N, H, dim), dev)
+    Bp, Bs = _rows(B, "B", idt, (N, G, dstate), dev)
+    Cp, Cs = _rows(C, "C", idt, (N, G, dstate), dev)
+    yp, ys = _rows(y, "y", idt, (N, H, dim), dev)
+    zp, zs = _rows(z, "z", idt, (N, H, dim), dev) if z is not None else (None, xs)
+    dp, ds = _rows(dt, "dt", f32, (N, H), dev) if dt is not None else (None, H)
+    _same_device(dev, (("A", A), ("D", D), ("dt_bias", dt_bias), ("slots", slots), ("seq_start", seq_start),
+                       ("load_state", load_state)))
+    prompt = seq_start is not None
+    desc = RssmLinearDesc(
+        num_seqs=_scalar("num_seqs", R), num_tokens=_scalar("num_tokens", N), num_heads=_scalar("num_heads", H),
+        heads_per_group=_scalar("hpg", H // G), dim=_scalar("dim", dim), dstate=_scalar("dstate", dstate),
+        num_slots=_scalar("num_slots", S), pad_slot_id=_scalar("pad_slot_id", pad_slot_id),
+        max_seq_len=_scalar("max_seq_len", max_seq_len) if prompt else 1, state_dtype=dtype_code(state.dtype),
+        input_dtype=dtype_code(idt), dt_softplus=1 if dt_softplus and dt is not None else 0,
+        state_slot_stride=state.stride(0) if S > 1 else H * dim * dstate, x_token_stride=xs, B_token_stride=Bs,
+        C_token_stride=Cs, dt_token_stride=ds, z_token_stride=zs, y_token_stride=ys, workspace_bytes=0)
+    tab = RssmLinearTables(
+        state=state.data_ptr(), A=_ptr(A, "A", f32, (H,)), D=_ptr(D, "D", f32, (H,)),
+        dt_bias=_ptr(dt_bias, "dt_bias", f32, (H,)), x=xp, B=Bp, C=Cp, dt=dp, z=zp, y=yp,
+        slots=_ptr(slots, "slots", i32, (R,)), seq_start=_ptr(seq_start, "seq_start", i32, (R + 1,)),
+        load_state=_ptr(load_state, "load_state", i32, (R,)), workspace=None)
+    return desc, tab, dev
+
+
+def _give_workspace(desc, tab, query, given, device, stream):
+    need = ctypes.c_int64()
+    _check(query(ctypes.byref(desc), ctypes.byref(need)))
+    ws = _workspace(need.value, given, device, stream)
+    if ws is not None:
+        tab.workspace = ws.data_ptr()
+        desc.workspace_bytes = ws.numel() * ws.element_size()
+    return ws
+
+
+def rssm_linear_attention(state, A, x, B, C, dt, y, slots, seq_start, *, max_seq_len: int, workspace=None,
+                          stream=None, **kw) -> None:
+    """Enqueue linear attention with a decay for each head over ragged prompts
+    (one layer): y and the slots' new states.  state pool [slots, H, dim,
+    dstate] (f32/bf16/f16, updated in place), A fp32 [H], x [N, H, dim], B / C [N, G,
+    dstate], dt fp32 [N, H] (raw) or None (dt = 1), y [N, H, dim] (dtype of x),
+    slots int32 [R], seq_start int32 [R + 1] (sequence r owns rows
+    seq_start[r] .. seq_start[r+1] - 1).  Rows of x, B, C, dt, z and y may be views of a
+    wider row.  Keywords: max_seq_len (required, the longest sequence),
+    load_state int32 [R] (0: start from a zero state), D, dt_bias fp32 [H], z,
+    dt_softplus=True, pad_slot_id=-1, workspace (uint8 tensor of
+    rssm_linear_attention_workspace's size; allocated when needed and not given)."""
+    desc, tab, dev = _linear_marshal(state, A, x, B, C, dt, y, slots, seq_start, max_seq_len=max_seq_len, **kw)
+    ws = _give_workspace(desc, tab, _lib.rssm_linear_attention_workspace, workspace, dev, stream)  # noqa: F841
+    _launch(_lib.rssm_linear_attention, desc, tab, dev, stream)
+
+
+def rssm_linear_attention_workspace(state, A, x, B, C, dt, y, slots, seq_start, *, max_seq_len: int, **kw) -> int:
+    """Workspace bytes of rssm_linear_attention for these arguments."""
+    desc, _, _ = _linear_marshal(state, A, x, B, C, dt, y, slots, seq_start, max_seq_len=max_seq_len, **kw)
+    need = ctypes.c_int64()
+    _check(_lib.rssm_linear_attention_workspace(ctypes.byref(desc), ctypes.byref(need)))
+    return need.value
+
+
+def rssm_linear_attention_step(state, A, x, B, C, dt, y, slots, *, stream=None, **kw) -> None:
+    """Enqueue the single-token form: row r of x, B, C, dt, z and y is request
+    r's token.  Arguments as rssm_linear_attention without seq_start,
+    max_seq_len, load_state and workspace."""
+    if "load_state" in kw or "max_seq_len" in kw:
+        raise TypeError("the single-token form takes no load_state and no max_seq_len")
+    desc, tab, dev = _linear_marshal(state, A, x, B, C, dt, y, slots, **kw)
+    _launch(_lib.rssm_linear_attention_step, desc, tab, dev, stream)
+
+
+def _paged_caches(k_cache, v_cache, page_table, seq_start, kv_len):
+    """Descriptor and table fields of the caches and their metadata."""
+    import torch
+    dev = _device_of(k_cache, "k_cache")
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, page_size, kv_heads, head_dim] (any strides with dense head_dim)")
+    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride() or v_cache.dtype != k_cache.dtype:
+        raise ValueError("v_cache must have k_cache's shape, strides and dtype")
+    if k_cache.shape[3] != 1 and k_cache.stride(3) != 1:
+        raise ValueError("head_dim of the caches must be dense")
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be int32 [seqs, pages] with dense rows")
+    S, M = page_table.shape
+    _same_device(dev, (("v_cache", v_cache), ("page_table", page_table), ("seq_start", seq_start), ("kv_len", kv_len)))
+    P, ps, Hkv, D = k_cache.shape
+    # a dimension of one entry is never stepped over: any legal stride will do
+    st = [t if n > 1 else _aligned_stride(D, k_cache.element_size()) for n, t in zip(k_cache.shape, k_cache.stride())]
+    desc = RssmPagedDesc(
+        num_seqs=_scalar("num_seqs", S), num_kv_heads=_scalar("kv_heads", Hkv), head_dim=_scalar("head_dim", D),
+        page_size=_scalar("page_size", ps), num_pages=_scalar("num_pages", P), max_pages=_scalar("max_pages", M),
+        dtype=dtype_code(k_cache.dtype), page_stride=st[0], row_stride=st[1], head_stride=st[2],
+        table_stride=page_table.stride(0) if S > 1 else M)
+    tab = RssmPagedTables(k_cache=k_cache.data_ptr(), v_cache=v_cache.data_ptr(), page_table=page_table.data_ptr(),
+                          seq_start=_ptr(seq_start, "seq_start", torch.int32, (S + 1,)),
+                          kv_len=_ptr(kv_len, "kv_len", torch.int32, (S,)))
+    return desc, tab, dev
+
+
+def rssm_paged_append(k_cache, v_cache, k_new, v_new, page_table, seq_start, kv_len, *, stream=None) -> None:
+    """Enqueue the append of new tokens to a paged cache: sequence s's rows
+    seq_start[s] .. seq_start[s+1] - 1 of k_new / v_new [N, kv_heads, head_dim] go to its
+    last positions before kv_len[s] (int32 [S], the new tokens counted).
+    Caches [pages, page_size, kv_heads, head_dim], any strides with dense
+    head_dim, both alike; page_table int32 [S, pages] (entries outside
+    [0, pages) are skipped)."""
+    desc, tab, dev = _paged_caches(k_cache, v_cache, page_table, seq_start, kv_len)
+    shape = (k_new.shape[0], k_cache.shape[2], k_cache.shape[3])
+    tab.k_new, ks = _rows(k_new, "k_new", k_cache.dtype, shape, dev)
+    tab.v_new, vs = _rows(v_new, "v_new", k_cache.dtype, shape, dev)
+    if ks != vs:
+        raise ValueError("k_new and v_new must have the same row stride")
+    desc.num_tokens = _scalar("num_tokens", shape[0])
+    desc.new_token_stride = ks
+    _launch(_lib.rssm_paged_append, desc, tab, dev, stream)
+
+
+def _paged_marshal(q, k_cache, v_cache, page_table, seq_start, kv_len, out, *, max_seq_len: int, max_kv_len: int,
+                   scale=None, window: int = 0, sinks: int = 0, lse=None):
+    import torch
+    desc, tab, dev = _paged_caches(k_cache, v_cache, page_table, seq_start, kv_len)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, q_heads, head_dim]")
+    N, Hq, D = q.shape[0], q.shape[1], k_cache.shape[3]
+    tab.q, desc.q_token_stride = _rows(q, "q", k_cache.dtype, (N, Hq, D), dev)
+    tab.out, desc.out_token_stride = _rows(out, "out", k_cache.dtype, (N, Hq, D), dev)
+    if lse is not None:
+        _same_device(dev, (("lse", lse),))
+        tab.lse = _ptr(lse, "lse", torch.float32, (N, Hq))
+    desc.num_tokens = _scalar("num_tokens", N)
+    desc.num_q_heads = _scalar("q_heads", Hq)
+    desc.max_seq_len = _scalar("max_seq_len", max_seq_len)
+    desc.max_kv_len = _scalar("max_kv_len", max_kv_len)
+    desc.window = _scalar("window", window)
+    desc.sinks = _scalar("sinks", sinks)
+    desc.scale = D ** -0.5 if scale is None else float(scale)
+    return desc, tab, dev
+
+
+def rssm_paged_attention(q, k_cache, v_cache, page_table, seq_start, kv_len, out, *, workspace=None, stream=None,
+                         **kw) -> None:
+    """Enqueue causal attention of each sequence's new tokens (the last
+    seq_start[s+1] - seq_start[s] of its kv_len[s] cached tokens) over a paged
+    cache.  q, out [N, q_heads, head_dim] (rows may be views of wider ones);
+    caches and tables as rssm_paged_append, which comes first.  Keywords:
+    max_seq_len, max_kv_len (required: the longest of the call), scale
+    (default head_dim ** -0.5), window=0 (tokens seen up to and including the query's; 0: all), sinks=0 (first
+    tokens seen beside the window), lse fp32 [N, q_heads] (optional output),
+    workspace (uint8 tensor of rssm_paged_attention_workspace's size;
+    allocated when needed and not given)."""
+    desc, tab, dev = _paged_marshal(q, k_cache, v_cache, page_table, seq_start, kv_len, out, **kw)
+    ws = _give_workspace(desc, tab, _lib.rssm_paged_attention_workspace, workspace, dev, stream)  # noqa: F841
+    _launch(_lib.rssm_paged_attention, desc, tab, dev, stream)
+
+
+def rssm_paged_attention_workspace(q, k_cache, v_cache, page_table, seq_start, kv_len, out, **kw) -> int:
+    """Workspace bytes of rssm_paged_attention for these arguments."""
+    desc, _, _ = _paged_marshal(q, k_cache, v_cache, page_table, seq_start, kv_len, out, **kw)
+    need = ctypes.c_int64()
+    _check(_lib.rssm_paged_attention_workspace(ctypes.byref(desc), ctypes.byref(need)))
+    return need.value
+
+
+def rssm_block_norm(y, residual, residual_out, normed=None, *, z=None, post_weight=None, pre_weight=None,
+                    channel_scale=None, residual_scale: float = 1.0, groups: int = 1, eps: float = 1e-5,
+                    stream=None) -> None:
+    """Enqueue the norms around a block, row by row of [rows, channels]:
+    u = y silu(z); v = u post_weight / rms of its group; residual_out =
+    residual + residual_scale channel_scale v; normed = residual_out
+    pre_weight / rms of the row (from the unrounded sum).  y, z and normed share one
+    dtype, residual and residual_out another; post_weight, pre_weight and
+    channel_scale are fp32 [channels].  post_weight=None: no norm of the block's
+    output; z, channel_scale, pre_weight and normed are optional.  residual_out may be
+    residual, normed may be y."""
+    import torch
+    dev = _device_of(y, "y")
+    if y.dim() != 2:
+        raise ValueError("y must be [rows, channels]")
+    R, C = y.shape
+    idt, rdt, f32 = y.dtype, residual.dtype, torch.float32
+    desc = RssmNormDesc(rows=_scalar("rows", R), channels=_scalar("channels", C), groups=_scalar("groups", groups),
+                        input_dtype=dtype_code(idt), residual_dtype=dtype_code(rdt), eps=float(eps),
+                        residual_scale=float(residual_scale))
+    tab = RssmNormTables()
+    tab.y, desc.y_row_stride = _rows(y, "y", idt, (R, C), dev)
+    tab.residual, desc.residual_row_stride = _rows(residual, "residual", rdt, (R, C), dev)
+    tab.residual_out, desc.residual_out_row_stride = _rows(residual_out, "residual_out", rdt, (R, C), dev)
+    desc.z_row_stride = desc.normed_row_stride = desc.y_row_stride
+    if z is not None:
+        tab.z, desc.z_row_stride = _rows(z, "z", idt, (R, C), dev)
+    if normed is not None:
+        tab.normed, desc.normed_row_stride = _rows(normed, "normed", idt, (R, C), dev)
+    _same_device(dev, (("post_weight", post_weight), ("pre_weight", pre_weight), ("channel_scale", channel_scale)))
+    tab.post_weight = _ptr(post_weight, "post_weight", f32, (C,))
+    tab.pre_weight = _ptr(pre_weight, "pre_weight", f32, (C,))
+    tab.channel_scale = _ptr(channel_scale, "channel_scale", f32, (C,))
+    _launch(_lib.rssm_block_norm, desc, tab, dev, stream)
 
 
 def rssm_pool_alloc(nbytes: int):

@@ -24,7 +24,11 @@ POOL_LIB_PATH = os.path.join(PKG, "librssm_pool.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["rssm_inst_f32.hip", "rssm_inst_bf16.hip", "rssm_inst_f16.hip", "rssm_inst_i8.hip",
-           "rssm_inst_f8.hip", "rssm_inst_gdn.hip", "rssm_inst_ssu.hip", "rssm_materialize.hip"]
+           "rssm_inst_f8.hip", "rssm_inst_gdn.hip", "rssm_inst_ssu.hip", "rssm_materialize.hip",
+           "rssm_inst_linattn_f32.hip", "rssm_inst_linattn_bf16.hip", "rssm_inst_linattn_f16.hip",
+           "rssm_inst_paged_f32.hip", "rssm_inst_paged_bf16.hip", "rssm_inst_paged_f16.hip",
+           "rssm_inst_norm_f32.hip", "rssm_inst_norm_bf16.hip", "rssm_inst_norm_f16.hip",
+           "rssm_linear_attention.hip", "rssm_paged_attention.hip", "rssm_block_norm.hip"]
 POOL_SOURCES = ["rssm_pool.hip"]
 ARCH = os.environ.get("RSSM_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,0 +1,534 @@
+// linattn_kernel.h -- gfx950 kernels of linear attention with a decay for each
+// head: the chunked prompt form and the single-token form.
+//
+// A chunk of Q = 64 tokens with l_i = sum_{u <= i} dt_u A inside it and starting
+// state S0 gives
+//     y_i = exp(l_i) S0 C_i + sum_{j <= i} exp(l_i - l_j) dt_j (C_i . B_j) x_j + D x_i
+//     S'  = exp(l_Q) S0 + sum_j w_j x_j B_j^T,    w_j = exp(l_Q - l_j) dt_j.
+// One workgroup of 4 wavefronts holds one 64-row tile of one head's state in
+// registers and walks the chunks of one stretch of one sequence.  Everything
+// is laid out transposed, so that each product's D tiles are the next one's operand
+// (mma_device.h):
+//   scores  G^T[j][i] = B_j . C_i          A = B rows (LDS), Bm = C rows (global -> registers)
+//   y^T[p][i] = S0[p] . C_i                A = S0 rows (LDS, rounded), Bm = the same C rows
+//       times exp(l_i), a scalar of the lane's column i
+//   y^T += x^T M^T                         A = x columns (LDS), Bm = masked weighted scores
+//   S'^T[n][p] = B^T (w x)                 A = B columns (LDS), Bm = w_j x_j, split so that no
+//                                          product loses more than 2^-22 (bf16: three parts,
+//                                          fp16: two parts scaled by a power of two, fp32: none)
+// Wavefront w owns tokens 16w .. 16w+15 of y and state rows 16w .. 16w+15 of the
+// update.  The next chunk's inputs are loaded into registers while the current
+// one is computed.
+//
+// When sequences x heads are too few to fill the chip, the token axis is split into
+// stretches: one launch folds each stretch from a zero state (kStateOnly), a second scans the
+// stretches' states and decays, a third computes the outputs from the
+// scanned starting states.
+#pragma once
+
+#include "mma_device.h"
+#include "ssu_kernel.h"
+
+namespace rssm {
+
+struct LinArgs {
+  char* state;
+  const float* A;
+  const float* D;         // [H] or null
+  const float* dt_bias;   // [H] or null
+  const char* x;
+  const char* B;
+  const char* C;
+  const float* dt;        // or null
+  const char* z;          // or null
+  char* y;
+  const int32_t* slots;
+  const int32_t* seq_start;
+  const int32_t* load_state;   // or null
+  float* ws_state;        // [seqs][nseg][H][dim][dstate] (nseg > 1)
+  float* ws_decay;        // [seqs][nseg][H] log decay of each stretch
+  int64_t state_stride, x_stride, B_stride, C_stride, dt_stride, z_stride, y_stride;   // elements
+  int32_t num_seqs, num_tokens, H, hpg, dim, num_slots, pad, max_seq_len, dt_softplus;
+  int32_t nseg, seg_len;  // stretches of the token axis and their length (a multiple of 64)
+};
+
+constexpr int kLinQ = 64;       // tokens a chunk
+constexpr int kLinP = 64;       // state rows a workgroup
+constexpr int kLinBlock = 256;
+
+// Sequence s of the call: slot, first row and length, after the guards.
+struct LinSeq {
+  int slot, start, len;
+  bool live;
+};
+
+__device__ __forceinline__ LinSeq lin_seq(const LinArgs& a, int s) {
+  LinSeq q;
+  q.slot = sload(a.slots + s);
+  q.live = q.slot != a.pad && q.slot >= 0 && q.slot < a.num_slots;
+  int b = sload(a.seq_start + s), e = sload(a.seq_start + s + 1);
+  b = b < 0 ? 0 : (b > a.num_tokens ? a.num_tokens : b);
+  e = e < b ? b : (e > a.num_tokens ? a.num_tokens : e);
+  q.start = b;
+  q.len = e - b < a.max_seq_len ? e - b : a.max_seq_len;
+  return q;
+}
+
+template <int ST>
+__device__ __forceinline__ f32x4 load_state4(const char* p) {
+  return widen4<ST>(reinterpret_cast<const typename Mma<ST>::elem*>(p));
+}
+template <int ST>
+__device__ __forceinline__ void store_state4(char* p, f32x4 v) {
+  narrow4<ST>(reinterpret_cast<typename Mma<ST>::elem*>(p), v);
+}
+
+// 2^k by exponent bits, k in [-126, 127].
+__device__ __forceinline__ float pow2i(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
+
+// Exponent k such that 2^k brings a magnitude m (finite, >= 0) to about
+// 2^12; 0 for m = 0 or non-finite m.  Within +-60 so that 2^k times the fp32 sums stays finite.
+__device__ __forceinline__ int scale_exp(float m) {
+  const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
+  if (!(m > 0.0f) || e == 128) return 0;
+  const int k = 12 - e;
+  return k > 60 ? 60 : (k < -60 ? -60 : k);
+}
+
+template <int IT, int N>
+struct LinLds {
+  typedef typename Mma<IT>::elem elem;
+  static constexpr int kPad = 16 / sizeof(elem);   // one 16-byte step: rows land 4 banks apart
+  static constexpr int kN = N + kPad;
+  static constexpr int kP = kLinP + kPad;
+  elem Bs[kLinQ * kN];
+  elem Ss[kLinP * kN];
+  elem Xs[kLinQ * kP];
+  float lh[kLinQ], ll[kLinQ], e[kLinQ], dt[kLinQ], w[kLinQ];   // l_i (high and low part), exp(l_i), dt_i, w_i
+  float sinv[kLinP];   // fp16: inverse scale of each state row in Ss
+  float decay, total;
+};
+
+// Stage `rows` x COLS elements at `base` (row stride `stride` elements) into
+// registers, rows past `rows` as zeros: the buffer size ends with the last row.
+template <int IT, int COLS>
+struct Stage {
+  typedef typename Mma<IT>::elem elem;
+  static constexpr int kVec = 16 / sizeof(elem);
+  static constexpr int kPerRow = COLS / kVec;
+  static constexpr int kN = kLinQ * kPerRow / kLinBlock;
+  u32x4 v[kN];
+  __device__ __forceinline__ void load(const char* base, int64_t stride, int rows, int tid) {
+    const uint32_t rb = static_cast<uint32_t>(stride * sizeof(elem));
+    const rsrc_t r = make_rsrc(base, rows > 0 ? (rows - 1) * rb + COLS * sizeof(elem) : 0);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int at = tid + i * kLinBlock;
+      v[i] = bload16<false>(r, (at / kPerRow) * rb + (at % kPerRow) * 16, 0);
+    }
+  }
+  __device__ __forceinline__ void store(elem* tile, int pitch, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int at = tid + i * kLinBlock;
+      *reinterpret_cast<u32x4*>(tile + (at / kPerRow) * pitch + (at % kPerRow) * kVec) = v[i];
+    }
+  }
+};
+
+template <int IT, int ST, int N, bool kStateOnly>
+__global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_kernel(LinArgs a) {
+  typedef typename Mma<IT>::elem elem;
+  typedef typename Mma<IT>::frag frag;
+  constexpr int NT = N / 16;
+  constexpr int KS = N / 32;
+  constexpr int es = sizeof(elem);
+  constexpr int ss = sizeof(typename Mma<ST>::elem);
+  __shared__ LinLds<IT, N> L;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
+  int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int ptiles = a.dim / kLinP;
+  const int item = xcd_order(blockIdx.x, gridDim.x);
+  const int pt0 = item % ptiles, h = (item / ptiles) % a.H;
+  const int rest = item / (ptiles * a.H);
+  const int seg = rest % a.nseg, s = rest / a.nseg;
+  const LinSeq q = lin_seq(a, s);
+  if (!q.live) return;
+  const int t0 = seg * a.seg_len;
+  const int t1 = q.len - t0 < a.seg_len ? q.len : t0 + a.seg_len;
+  if (kStateOnly ? (q.len - t0 <= a.seg_len) : (seg > 0 && t0 >= q.len)) return;
+  // wavefronts with later tokens have more causal products: alternate which SIMD gets them
+  const int wrow = (item & 1) ? 3 - wave : wave;
+
+  const float A = sload(a.A + h);
+  const float Dh = a.D != nullptr ? sload(a.D + h) : 0.0f;
+  const float bias = a.dt_bias != nullptr ? sload(a.dt_bias + h) : 0.0f;
+  const int grp = h / a.hpg;
+  const int64_t tile = (static_cast<int64_t>(h) * a.dim + pt0 * kLinP) * N;   // of this workgroup inside a slot
+  const int64_t wtile = static_cast<int64_t>(a.H) * a.dim * N;
+  // lane's place in the state: row p = 16 wave + li, columns 16 nt + 4g
+  const int64_t sat = static_cast<int64_t>(16 * wave + li) * N + 4 * g;
+  char* const slot_state = a.state + (q.slot * a.state_stride + tile) * ss;
+
+  f32x4 S[NT];
+  if constexpr (kStateOnly) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) S[n] = f32x4{0, 0, 0, 0};
+  } else if (a.nseg > 1) {
+    const float* p = a.ws_state + (static_cast<int64_t>(s) * a.nseg + seg) * wtile + tile + sat;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) S[n] = *reinterpret_cast<const f32x4*>(p + 16 * n);
+  } else if (a.load_state == nullptr || sload(a.load_state + s) != 0) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) S[n] = load_state4<ST>(slot_state + (sat + 16 * n) * ss);
+  } else {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) S[n] = f32x4{0, 0, 0, 0};
+  }
+
+  Stage<IT, kLinP> xr;
+  Stage<IT, N> br;
+  frag cr[KS];
+  float dtr = 0.0f;
+  const int64_t hx = static_cast<int64_t>(h) * a.dim + pt0 * kLinP;
+  auto fetch = [&](int t) {
+    const int rows = t1 - t < kLinQ ? t1 - t : kLinQ;
+    const int64_t row = q.start + t;
+    xr.load(a.x + (row * a.x_stride + hx) * es, a.x_stride, rows, tid);
+    br.load(a.B + (row * a.B_stride + static_cast<int64_t>(grp) * N) * es, a.B_stride, rows, tid);
+    if (wave == 0) {
+      dtr = 1.0f;
+      if (a.dt != nullptr) {
+        const rsrc_t r = make_rsrc(a.dt + row * a.dt_stride + h, ((rows - 1) * static_cast<uint32_t>(a.dt_stride) + 1) * 4);
+        dtr = new_token_dt(bload_f32(r, lane * static_cast<uint32_t>(a.dt_stride) * 4, 0), bias, a.dt_softplus);
+      }
+    }
+  };
+  auto fetch_out = [&](int t) {   // C rows and z of the wavefront's tokens: column i = 16 wrow + li
+    const int rows = t1 - t < kLinQ ? t1 - t : kLinQ;
+    const int64_t row = q.start + t;
+    const uint32_t cb = static_cast<uint32_t>(a.C_stride * es);
+    const rsrc_t rc = make_rsrc(a.C + (row * a.C_stride + static_cast<int64_t>(grp) * N) * es, (rows - 1) * cb + N * es);
+    const uint32_t i = 16 * wrow + li;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const uint32_t at = i * cb + (32 * k + 8 * g) * es;
+      if constexpr (IT == kF32) {
+        const u32x4 u = bload16<false>(rc, at, 0), v = bload16<false>(rc, at + 16, 0);
+        cr[k] = __builtin_bit_cast(frag, u32x8{u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w});
+      } else {
+        cr[k] = __builtin_bit_cast(frag, bload16<false>(rc, at, 0));
+      }
+    }
+  };
+
+  double seg_total = 0.0;
+  if (t0 < t1) {
+    fetch(t0);
+    if constexpr (!kStateOnly) fetch_out(t0);
+  }
+  for (int t = t0; t < t1; t += kLinQ) {
+    const int rows = t1 - t < kLinQ ? t1 - t : kLinQ;
+    if (t > t0) __syncthreads();   // every read of the previous chunk's tiles is done
+    xr.store(L.Xs, LinLds<IT, N>::kP, tid);
+    br.store(L.Bs, LinLds<IT, N>::kN, tid);
+    if constexpr (!kStateOnly) {
+      float sc = 1.0f;
+      if constexpr (IT == kF16) {   // bring each state row into the range of fp16
+        float m = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(S[n][r]));
+        const int k = scale_exp(max_groups(m));
+        sc = pow2i(k);
+        if (g == 0) L.sinv[16 * wave + li] = pow2i(-k);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        narrow4<IT>(L.Ss + (16 * wave + li) * LinLds<IT, N>::kN + 16 * n + 4 * g, IT == kF16 ? S[n] * sc : S[n]);
+    }
+    if (wave == 0) {
+      // sums of dt A in fp64: differences of far positions keep their relative accuracy
+      const float dtv = lane < rows ? dtr : 0.0f;
+      double l = static_cast<double>(dtv) * static_cast<double>(A);
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const double o = __shfl_up(l, d);
+        if (lane >= d) l += o;
+      }
+      const double end = __shfl(l, 63);
+      const float lh = static_cast<float>(l);
+      L.lh[lane] = lh;
+      L.ll[lane] = static_cast<float>(l - lh);
+      L.e[lane] = expf(lh);
+      L.dt[lane] = dtv;
+      L.w[lane] = lane < rows ? expf(static_cast<float>(end - l)) * dtv : 0.0f;
+      if (lane == 0) {
+        L.decay = expf(static_cast<float>(end));
+        L.total = static_cast<float>(end);
+      }
+    }
+    __syncthreads();
+    frag cc[KS];
+    if constexpr (!kStateOnly) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k) cc[k] = cr[k];
+    }
+    if (t + kLinQ < t1) {
+      fetch(t + kLinQ);
+      if constexpr (!kStateOnly) fetch_out(t + kLinQ);
+    }
+
+    if constexpr (!kStateOnly) {
+      const int i = 16 * wrow + li;
+      // masked, decay-weighted scores M^T[j][i], j = 16 jt + 4g + r
+      f32x4 M[4];
+      const float lhi = L.lh[i], lli = L.ll[i];
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt) {
+        M[jt] = f32x4{0, 0, 0, 0};
+        if (jt > wrow) continue;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          M[jt] = mma<IT>(frag_row<IT>(L.Bs + (16 * jt + li) * LinLds<IT, N>::kN + 32 * k + 8 * g), cc[k], M[jt]);
+        const f32x4 lj = *reinterpret_cast<const f32x4*>(L.lh + 16 * jt + 4 * g);
+        const f32x4 kj = *reinterpret_cast<const f32x4*>(L.ll + 16 * jt + 4 * g);
+        const f32x4 dj = *reinterpret_cast<const f32x4*>(L.dt + 16 * jt + 4 * g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float d = (lhi - lj[r]) + (lli - kj[r]);
+          const float v = M[jt][r] * ((IT == kF32 ? expf(d) : __expf(d)) * dj[r]);
+          M[jt][r] = 16 * jt + 4 * g + r <= i ? v : 0.0f;
+        }
+      }
+      int mk = 0;
+      if constexpr (IT == kF16) {   // one power of two for the lane's column of M
+        float m = 0.0f;
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(M[jt][r]));
+        mk = scale_exp(max_groups(m));
+        const float ms = pow2i(mk);
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt) M[jt] *= ms;
+      }
+      const float ei = L.e[i], mi = pow2i(-mk);
+      f32x4 Y[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        f32x4 acc = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          acc = mma<IT>(frag_row<IT>(L.Ss + (16 * p + li) * LinLds<IT, N>::kN + 32 * k + 8 * g), cc[k], acc);
+        if constexpr (IT == kF16) acc *= *reinterpret_cast<const f32x4*>(L.sinv + 16 * p + 4 * g);
+        Y[p] = acc * ei;
+      }
+      f32x4 X[4];
+      bool bad = false;
+      const frag m0 = to_frag<IT>(stack(M[0], M[1])), m1 = to_frag<IT>(stack(M[2], M[3]));
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        f32x4 acc = f32x4{0, 0, 0, 0};
+        acc = mma<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 0, 16 * p, lane), m0, acc);
+        if (wrow >= 2) acc = mma<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 32, 16 * p, lane), m1, acc);
+        X[p] = acc;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) bad |= !(fabsf(acc[r]) < __builtin_inff());
+      }
+      if (__builtin_expect(__ballot(bad) != 0, 0)) {
+        // a non-finite x times the zero weight of a later token is not zero:
+        // add the visible tokens one by one instead
+        for (int p = 0; p < 4; ++p) X[p] = f32x4{0, 0, 0, 0};
+        for (int jt = 0; jt < 4; ++jt)
+          for (int e = 0; e < 16; ++e) {
+            const f32x4 src = jt == 0 ? M[0] : jt == 1 ? M[1] : jt == 2 ? M[2] : M[3];
+            const int r = e & 3;
+            const float own = r == 0 ? src[0] : r == 1 ? src[1] : r == 2 ? src[2] : src[3];
+            const float m = __shfl(own, (e >> 2) * 16 + li);
+            const int j = 16 * jt + e;
+            if (j <= i)
+              for (int p = 0; p < 4; ++p)
+                X[p] += widen4<IT>(L.Xs + j * LinLds<IT, N>::kP + 16 * p + 4 * g) * m;
+          }
+      }
+      if (i < rows) {
+        const int64_t row = q.start + t + i;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const f32x4 xi = widen4<IT>(L.Xs + i * LinLds<IT, N>::kP + 16 * p + 4 * g);
+          f32x4 v = Y[p] + X[p] * mi + xi * Dh;
+          if (a.z != nullptr) {
+            const f32x4 zi = widen4<IT>(reinterpret_cast<const elem*>(a.z) + row * a.z_stride + hx + 16 * p + 4 * g);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] *= silu(zi[r]);
+          }
+          narrow4<IT>(reinterpret_cast<elem*>(a.y) + row * a.y_stride + hx + 16 * p + 4 * g, v);
+        }
+      }
+    }
+
+    // state: S^T[n][p] of the wavefront's 16 rows p = 16 wave + li
+    const float decay = L.decay;
+    if (wave == 0) seg_total += L.total;
+    frag u0[2], u1[2], u2[2];
+    f32x8 wx[2];
+    int sk = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const f32x4 w0 = *reinterpret_cast<const f32x4*>(L.w + 32 * k + 4 * g);
+      const f32x4 w1 = *reinterpret_cast<const f32x4*>(L.w + 32 * k + 16 + 4 * g);
+      wx[k] = from_frag<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 32 * k, 16 * wave, lane)) * stack(w0, w1);
+    }
+    if constexpr (IT == kF16) {
+      float m = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(wx[k][e]));
+      sk = scale_exp(max_groups(m));
+    }
+    const float up = pow2i(sk), down = pow2i(-sk);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const f32x8 v = IT == kF16 ? wx[k] * up : wx[k];
+      u0[k] = to_frag<IT>(v);
+      if constexpr (IT != kF32) {
+        const f32x8 v1 = v - from_frag<IT>(u0[k]);
+        u1[k] = to_frag<IT>(v1);
+        if constexpr (IT == kBF16) u2[k] = to_frag<IT>(v1 - from_frag<IT>(u1[k]));
+      }
+    }
+    const float dup = IT == kF16 ? decay * up : decay;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      f32x4 acc = S[n] * dup;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const frag b = frag_col<IT>(L.Bs, LinLds<IT, N>::kN, 32 * k, 16 * n, lane);
+        if constexpr (IT == kBF16) acc = mma<IT>(b, u2[k], acc);
+        if constexpr (IT != kF32) acc = mma<IT>(b, u1[k], acc);
+        acc = mma<IT>(b, u0[k], acc);
+      }
+      S[n] = IT == kF16 ? acc * down : acc;
+    }
+  }
+
+  if constexpr (kStateOnly) {
+    float* p = a.ws_state + (static_cast<int64_t>(s) * a.nseg + seg + 1) * wtile + tile + sat;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(p + 16 * n) = S[n];
+    if (tid == 0 && pt0 == 0)
+      a.ws_decay[(static_cast<int64_t>(s) * a.nseg + seg) * a.H + h] = static_cast<float>(seg_total);
+  } else if (t1 == q.len) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) store_state4<ST>(slot_state + (sat + 16 * n) * ss, S[n]);
+  }
+}
+
+// Scan over stretches: workspace entry k becomes the state at the start of stretch k
+// (entry k + 1 held stretch k's own state from zero).  One thread a quartet of
+// state elements of one (sequence, head).
+template <int ST>
+__global__ __launch_bounds__(kLinBlock) void linattn_scan_kernel(LinArgs a, int elems) {
+  constexpr int ss = sizeof(typename Mma<ST>::elem);
+  const int h = blockIdx.y, s = blockIdx.z;
+  const LinSeq q = lin_seq(a, s);
+  if (!q.live) return;
+  const int at = (blockIdx.x * kLinBlock + threadIdx.x) * 4;
+  if (at >= elems) return;
+  const int64_t hs = static_cast<int64_t>(h) * elems + at, wtile = static_cast<int64_t>(a.H) * elems;
+  f32x4 run = f32x4{0, 0, 0, 0};
+  if (a.load_state == nullptr || sload(a.load_state + s) != 0)
+    run = load_state4<ST>(a.state + (q.slot * a.state_stride + hs) * ss);
+  float* w = a.ws_state + static_cast<int64_t>(s) * a.nseg * wtile + hs;
+  *reinterpret_cast<f32x4*>(w) = run;
+  for (int k = 0; (k + 1) * static_cast<int64_t>(a.seg_len) < q.len; ++k) {
+    w += wtile;
+    const float d = expf(sload(a.ws_decay + (static_cast<int64_t>(s) * a.nseg + k) * a.H + h));
+    run = run * d + *reinterpret_cast<const f32x4*>(w);
+    *reinterpret_cast<f32x4*>(w) = run;
+  }
+}
+
+// Single-token form: one workgroup a (request, head, 64 state rows), 16 rows a
+// wavefront.  The state streams through registers once (16-byte loads and
+// stores, all of a wavefront's rows in flight); each lane folds its columns
+// and the row's readout is summed over the lanes that share it.
+template <int IT, int ST, int N>
+__global__ __launch_bounds__(kLinBlock) void linattn_step_kernel(LinArgs a) {
+  typedef typename Mma<IT>::elem elem;
+  constexpr int ss = sizeof(typename Mma<ST>::elem);
+  constexpr int EV = 16 / ss;            // columns a lane
+  constexpr int LPR = N / EV;            // lanes a row
+  constexpr int RPP = 64 / LPR;          // rows a pass
+  constexpr int PASSES = 16 / RPP;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int ptiles = a.dim / kLinP;
+  const int pt0 = blockIdx.x % ptiles, h = (blockIdx.x / ptiles) % a.H, b = blockIdx.x / (ptiles * a.H);
+  const int slot = sload(a.slots + b);
+  if (slot == a.pad || slot < 0 || slot >= a.num_slots) return;
+  const int row0 = pt0 * kLinP + 16 * wave, cc = lane % LPR, rr = lane / LPR;
+  char* const st0 = a.state + (slot * a.state_stride + (static_cast<int64_t>(h) * a.dim + row0 + rr) * N + cc * EV) * ss;
+  u32x4 raw[PASSES];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) raw[p] = ld<true, u32x4>(st0 + p * (RPP * N * ss));
+  const int grp = h / a.hpg;
+  const elem* Bp = reinterpret_cast<const elem*>(a.B) + b * a.B_stride + static_cast<int64_t>(grp) * N + cc * EV;
+  const elem* Cp = reinterpret_cast<const elem*>(a.C) + b * a.C_stride + static_cast<int64_t>(grp) * N + cc * EV;
+  f32x4 Bv[EV / 4], Cv[EV / 4];
+#pragma unroll
+  for (int k = 0; k < EV / 4; ++k) {
+    Bv[k] = widen4<IT>(Bp + 4 * k);
+    Cv[k] = widen4<IT>(Cp + 4 * k);
+  }
+  float dt = 1.0f;
+  if (a.dt != nullptr)
+    dt = new_token_dt(sload(a.dt + b * a.dt_stride + h), a.dt_bias != nullptr ? sload(a.dt_bias + h) : 0.0f, a.dt_softplus);
+  const float decay = expf(dt * sload(a.A + h));
+  const float Dh = a.D != nullptr ? sload(a.D + h) : 0.0f;
+  const int64_t hx = static_cast<int64_t>(h) * a.dim + row0 + rr;
+  const elem* xp = reinterpret_cast<const elem*>(a.x) + b * a.x_stride + hx;
+  const elem* zp = a.z != nullptr ? reinterpret_cast<const elem*>(a.z) + b * a.z_stride + hx : nullptr;
+  elem* yp = reinterpret_cast<elem*>(a.y) + b * a.y_stride + hx;
+  float xv[PASSES], zv[PASSES];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    xv[p] = elem_to_float<IT>(xp[p * RPP]);
+    zv[p] = zp != nullptr ? elem_to_float<IT>(zp[p * RPP]) : 0.0f;
+  }
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const float dx = dt * xv[p];
+    float sum = 0.0f;
+    u32x4 o;
+    if constexpr (ST == kF32) {
+      const f32x4 v = __builtin_bit_cast(f32x4, raw[p]) * decay + Bv[0] * dx;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum = fmaf(v[e], Cv[0][e], sum);
+      o = __builtin_bit_cast(u32x4, v);
+    } else {
+      const f32x8 old = from_frag<ST>(__builtin_bit_cast(typename Mma<ST>::frag, raw[p]));
+      const f32x8 v = old * decay + stack(Bv[0], Bv[EV / 4 - 1]) * dx;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum = fmaf(v[e], Cv[0][e], sum);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum = fmaf(v[4 + e], Cv[EV / 4 - 1][e], sum);
+      o = __builtin_bit_cast(u32x4, to_frag<ST>(v));
+    }
+    st<true>(st0 + p * (RPP * N * ss), o);
+#pragma unroll
+    for (int d = 1; d < LPR; d <<= 1) sum += __shfl_xor(sum, d);
+    if (cc == 0) {
+      float v = fmaf(Dh, xv[p], sum);
+      if (zp != nullptr) v *= silu(zv[p]);
+      if constexpr (IT == kF32) yp[p * RPP] = v;
+      else if constexpr (IT == kBF16) yp[p * RPP] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+      else yp[p * RPP] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+    }
+  }
+}
+
+}  // namespace rssm

@@ -1,0 +1,609 @@
+// paged_kernel.h -- gfx950 kernels of the append to a paged key/value cache
+// and of causal attention over it.
+//
+// Rows of a tile are (new token, query head of the group) pairs of one
+// key/value head: row R is token R / group, head R % group.  Per tile of keys,
+// transposed like the linear-attention kernel (mma_device.h):
+//   S^T[j][i] = K_j . Q_i        A = K rows, Bm = Q rows (registers)
+//   P = exp2(c S - m)            column i is the lane's: maximum and sum need two
+//                                exchanges between the four lane groups
+//   O^T[d][i] += V^T P           A = V columns (transposing LDS read), Bm = P
+// with the running maximum m and sum l of each row (one pass over K and V).
+//  * paged_tile_kernel: many rows.  4 wavefronts x 16 RB rows share the K and
+//    V tiles of 64 tokens, double-buffered in LDS; the next tile is loaded
+//    into registers while the current one is computed.
+//  * paged_row_kernel: at most 16 rows (single-token decoding).  Bound by
+//    reading the cache, so every wavefront streams its own tiles of 32
+//    tokens, K straight into operand registers and V through its own part of LDS,
+//    without barriers; the four partial results are joined in LDS.
+// When there are few row tiles, the tiles of keys are split over workgroups and
+// paged_join_kernel joins the partial outputs in a fixed order.
+#pragma once
+
+#include "mma_device.h"
+
+namespace rssm {
+
+struct PagedArgs {
+  char* k;
+  char* v;
+  const char* k_new;
+  const char* v_new;
+  const char* q;
+  char* out;
+  float* lse;                 // or null
+  const int32_t* table;
+  const int32_t* seq_start;
+  const int32_t* kv_len;
+  float* part_o;              // [num_tokens * Hq][nsplit][D] (nsplit > 1)
+  float* part_ml;             // [num_tokens * Hq][nsplit][2]
+  int64_t page_stride, row_stride, head_stride, q_stride, out_stride, new_stride, table_stride;   // elements
+  uint32_t page_magic, page_shift;   // j / page_size = j * magic >> shift for j < 2^31
+  int32_t num_seqs, num_tokens, Hq, Hkv, group, page_size, num_pages, max_pages, max_seq_len, max_kv_len;
+  int32_t window, sinks;
+  float scale_log2;           // scale / ln 2
+  int32_t row_tiles, nsplit, split_tiles;   // row tiles a sequence, splits, key tiles a split
+};
+
+constexpr int kPagedBlock = 256;
+constexpr float kLn2 = 0.693147180559945309f;
+
+struct PagedSeq {
+  int start, q_len, first_pos;   // position of the first new token (negative: the first ones see nothing)
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int s) {
+  PagedSeq q;
+  int b = sload(a.seq_start + s), e = sload(a.seq_start + s + 1);
+  b = b < 0 ? 0 : (b > a.num_tokens ? a.num_tokens : b);
+  e = e < b ? b : (e > a.num_tokens ? a.num_tokens : e);
+  q.start = b;
+  q.q_len = e - b < a.max_seq_len ? e - b : a.max_seq_len;
+  const int n = sload(a.kv_len + s);
+  q.first_pos = (n < 0 ? 0 : n) - (e - b);
+  return q;
+}
+
+__device__ __forceinline__ int page_of(const PagedArgs& a, int j) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(j)) * a.page_magic) >> a.page_shift);
+}
+
+// Cache row of token j of sequence s in elements (head 0), -1 when it lies on no page.
+__device__ __forceinline__ int64_t cache_row(const PagedArgs& a, int s, int j, int limit) {
+  if (j >= limit) return -1;
+  const int pi = page_of(a, j);
+  if (pi >= a.max_pages) return -1;
+  const int page = gload(a.table + s * a.table_stride + pi);
+  if (page < 0 || page >= a.num_pages) return -1;
+  return page * a.page_stride + (j - pi * a.page_size) * a.row_stride;
+}
+
+// Tiles of T keys that rows at positions [pmin, pmax] see: the first `sink`
+// ones and those from `lo` to `hi`.
+struct KeyTiles {
+  int sink, lo, hi, count, limit;   // limit: first token no row sees
+};
+
+template <int T>
+__device__ __forceinline__ KeyTiles key_tiles(const PagedArgs& a, int pmin, int pmax) {
+  KeyTiles k;
+  k.limit = pmax < a.max_kv_len ? pmax + 1 : a.max_kv_len;
+  if (k.limit < 0) k.limit = 0;
+  k.lo = 0;
+  k.sink = 0;
+  if (a.window > 0) {
+    if (pmin >= a.window) {
+      const int low = pmin - a.window + 1;
+      k.sink = ((a.sinks < low ? a.sinks : low) + T - 1) / T;
+      k.lo = low / T;
+      if (k.lo < k.sink) k.lo = k.sink;
+    }
+  }
+  k.hi = (k.limit + T - 1) / T;
+  if (k.sink > k.hi) k.sink = k.hi;
+  if (k.lo > k.hi) k.lo = k.hi;
+  k.count = k.sink + (k.hi - k.lo);
+  return k;
+}
+
+__device__ __forceinline__ int key_tile(const KeyTiles& k, int v) { return v < k.sink ? v : k.lo + (v - k.sink); }
+
+__device__ __forceinline__ bool visible(const PagedArgs& a, int j, int pos) {
+  return j <= pos && (a.window == 0 || j > pos - a.window || j < a.sinks);
+}
+
+// Whether any of 16 raw bytes' elements is infinite or NaN.
+template <int IT>
+__device__ __forceinline__ bool nonfinite16(u32x4 v) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (IT == kBF16) any |= ((v[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+    else if constexpr (IT == kF16) any |= ((v[i] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+    else any |= ((v[i] & 0x7f800000u) + 0x00800000u) & 0x80000000u;
+  }
+  return any != 0;
+}
+
+// Running softmax of one row block (column li of each lane).
+struct RowState {
+  float m, l;   // maximum (log2 units) and the lane's part of the sum
+};
+
+// One tile of JT x 16 scores of a row block: mask, weights, and the factor for
+// the output so far.  vis: bit j of the tile set where token j0 + j is on a page.
+template <int JT, bool kMask>
+__device__ __forceinline__ float softmax_tile(const PagedArgs& a, f32x4 (&S)[JT], RowState& st, int j0, int pos,
+                                              uint64_t on_page, int g) {
+  float mx = -__builtin_inff();
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if constexpr (kMask) {
+        const int jl = 16 * jt + 4 * g + r;
+        if (!(((on_page >> jl) & 1) && visible(a, j0 + jl, pos))) S[jt][r] = -__builtin_inff();
+      }
+      mx = fmaxf(mx, S[jt][r]);
+    }
+  mx = max_groups(mx) * a.scale_log2;
+  const float mn = fmaxf(st.m, mx);
+  const float base = mn == -__builtin_inff() ? 0.0f : mn;   // nothing visible yet: exp2(-inf - 0) = 0
+  const float alpha = __builtin_amdgcn_exp2f(st.m - base);
+  st.m = mn;
+  float sum = 0.0f;
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float p = __builtin_amdgcn_exp2f(fmaf(S[jt][r], a.scale_log2, -base));
+      S[jt][r] = p;
+      sum += p;
+    }
+  st.l = st.l * alpha + sum;
+  return alpha;
+}
+
+// O += V^T P token by token with a select, for a tile in which a value that
+// some rows may not see is infinite or NaN (0 times it is not 0).
+template <int IT, int JT, int DT>
+__device__ __forceinline__ void add_visible(const PagedArgs& a, const f32x4 (&P)[JT], f32x4 (&O)[DT],
+                                            const typename Mma<IT>::elem* V, int pitch, int j0, int pos,
+                                            uint64_t on_page, int g, int li) {
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt)
+#pragma unroll 1
+    for (int e = 0; e < 16; ++e) {
+      const int r = e & 3, jl = 16 * jt + e;
+      const float own = r == 0 ? P[jt][0] : r == 1 ? P[jt][1] : r == 2 ? P[jt][2] : P[jt][3];
+      const float p = __shfl(own, (e >> 2) * 16 + li);
+      if (((on_page >> jl) & 1) && visible(a, j0 + jl, pos)) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) O[d] += widen4<IT>(V + jl * pitch + 16 * d + 4 * g) * p;
+      }
+    }
+}
+
+// Store one row's results: the output, or this split's partial ones.
+template <int IT, int DT>
+__device__ __forceinline__ void store_row(const PagedArgs& a, const f32x4 (&O)[DT], float m, float l, int64_t token,
+                                          int head, int split, int g) {
+  typedef typename Mma<IT>::elem elem;
+  if (a.nsplit == 1) {
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // nothing visible: zeros; NaN stays
+    elem* o = reinterpret_cast<elem*>(a.out) + token * a.out_stride + head * (DT * 16) + 4 * g;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) narrow4<IT>(o + 16 * d, O[d] * inv);
+    if (a.lse != nullptr && g == 0) a.lse[token * a.Hq + head] = (m + log2f(l)) * kLn2;
+  } else {
+    const int64_t at = (token * a.Hq + head) * a.nsplit + split;
+    float* o = a.part_o + at * (DT * 16) + 4 * g;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(o + 16 * d) = O[d];
+    if (g == 0) {
+      a.part_ml[2 * at] = m;
+      a.part_ml[2 * at + 1] = l;
+    }
+  }
+}
+
+__device__ __forceinline__ int64_t shfl64(int64_t v, int from) {
+  const int lo = __shfl(static_cast<int>(v), from), hi = __shfl(static_cast<int>(v >> 32), from);
+  return (static_cast<int64_t>(hi) << 32) | static_cast<uint32_t>(lo);
+}
+
+template <int IT, int D, int RB>
+__global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_kernel(PagedArgs a) {
+  typedef typename Mma<IT>::elem elem;
+  typedef typename Mma<IT>::frag frag;
+  constexpr int T = 64, JT = T / 16, KS = D / 32, DT = D / 16;
+  constexpr int kVec = 16 / sizeof(elem), kPerRow = D / kVec, kRowsPass = kPagedBlock / kPerRow, kPasses = T / kRowsPass;
+  constexpr int kPitch = D + kVec;
+  constexpr int kRows = 64 * RB;
+  __shared__ __align__(16) elem lds[2][2][T * kPitch];   // [buffer][K, V]
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int item = xcd_order(blockIdx.x, gridDim.x);
+  const int split = item % a.nsplit;
+  item /= a.nsplit;
+  const int rt = a.row_tiles - 1 - item % a.row_tiles;   // later tokens see more keys: first
+  item /= a.row_tiles;
+  const int kvh = item % a.Hkv, s = item / a.Hkv;
+  const PagedSeq sq = paged_seq(a, s);
+  const int total_rows = sq.q_len * a.group, row0 = rt * kRows;
+  if (row0 >= total_rows) return;
+  const int row1 = row0 + kRows < total_rows ? row0 + kRows : total_rows;
+  const KeyTiles kt = key_tiles<T>(a, sq.first_pos + row0 / a.group, sq.first_pos + (row1 - 1) / a.group);
+  const int v0 = split * a.split_tiles;
+  const int v1 = split == a.nsplit - 1 || kt.count - v0 < a.split_tiles ? kt.count : v0 + a.split_tiles;
+
+  frag Q[RB][KS];
+  int pos[RB], head[RB];
+  int64_t tok[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const int R = row0 + (wave * RB + b) * 16 + li;
+    const bool in = R < row1;
+    const int t = in ? R / a.group : 0;
+    tok[b] = in ? sq.start + t : -1;
+    head[b] = kvh * a.group + (in ? R - t * a.group : 0);
+    pos[b] = in && sq.first_pos + t >= 0 ? sq.first_pos + t : -1;
+    const elem* qp = reinterpret_cast<const elem*>(a.q) + (in ? tok[b] : sq.start) * a.q_stride + static_cast<int64_t>(head[b]) * D + 8 * g;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) Q[b][k] = frag_row<IT>(qp + 32 * k);
+  }
+  // positions of the wavefront's rows (uniform)
+  const int w0 = row0 + wave * RB * 16, w1 = w0 + RB * 16 < row1 ? w0 + RB * 16 : row1;
+  const int wmin = w1 == w0 + RB * 16 ? sq.first_pos + w0 / a.group : -1;   // -1: some rows see nothing
+  const int wmax = w0 < w1 ? sq.first_pos + (w1 - 1) / a.group : -1;
+
+  f32x4 O[RB][DT];
+  RowState rs[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    rs[b].m = -__builtin_inff();
+    rs[b].l = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) O[b][d] = f32x4{0, 0, 0, 0};
+  }
+
+  const int64_t hoff = static_cast<int64_t>(kvh) * a.head_stride;
+  u32x4 kr[kPasses], vr[kPasses];
+  const int vec = tid % kPerRow, srow = tid / kPerRow;
+  auto fetch = [&](int64_t row_off) {   // row_off: the lane's token's cache row (-1: none)
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int64_t off = shfl64(row_off, srow + i * kRowsPass);
+      kr[i] = vr[i] = u32x4{0, 0, 0, 0};
+      if (off >= 0) {
+        const int64_t at = (off + hoff + vec * kVec) * static_cast<int64_t>(sizeof(elem));
+        kr[i] = ld<false, u32x4>(a.k + at);
+        vr[i] = ld<false, u32x4>(a.v + at);
+      }
+    }
+  };
+  auto put = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int at = (srow + i * kRowsPass) * kPitch + vec * kVec;
+      *reinterpret_cast<u32x4*>(&lds[buf][0][at]) = kr[i];
+      *reinterpret_cast<u32x4*>(&lds[buf][1][at]) = vr[i];
+    }
+  };
+  int64_t off = -1, off_next = -1;
+  if (v0 < v1) {
+    off = cache_row(a, s, key_tile(kt, v0) * T + lane, kt.limit);
+    fetch(off);
+    if (v0 + 1 < v1) off_next = cache_row(a, s, key_tile(kt, v0 + 1) * T + lane, kt.limit);
+    put(0);
+  }
+  __syncthreads();
+  for (int v = v0; v < v1; ++v) {
+    const int buf = (v - v0) & 1, j0 = key_tile(kt, v) * T;
+    const uint64_t on_page = __ballot(off >= 0);
+    if (v + 1 < v1) {
+      off = off_next;
+      fetch(off);
+      if (v + 2 < v1) off_next = cache_row(a, s, key_tile(kt, v + 2) * T + lane, kt.limit);
+    }
+    if (j0 <= wmax) {
+      const elem* Kt = lds[buf][0];
+      const elem* Vt = lds[buf][1];
+      const bool full = on_page == ~0ull && j0 + T - 1 <= wmin &&
+                        (a.window == 0 || j0 > wmax - a.window || j0 + T <= a.sinks);
+      f32x4 S[RB][JT];
+#pragma unroll
+      for (int jt = 0; jt < JT; ++jt) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b) S[b][jt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const frag kf = frag_row<IT>(Kt + (16 * jt + li) * kPitch + 32 * k + 8 * g);
+#pragma unroll
+          for (int b = 0; b < RB; ++b) S[b][jt] = mma<IT>(kf, Q[b][k], S[b][jt]);
+        }
+      }
+      bool bad = false;
+      if (!full) {
+        for (int i = lane; i < T * kPerRow; i += 64)
+          bad |= nonfinite16<IT>(*reinterpret_cast<const u32x4*>(Vt + (i / kPerRow) * kPitch + (i % kPerRow) * kVec));
+        bad = __ballot(bad) != 0;
+      }
+      frag P[RB][JT / 2];
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        const float alpha = full ? softmax_tile<JT, false>(a, S[b], rs[b], j0, pos[b], on_page, g)
+                                 : softmax_tile<JT, true>(a, S[b], rs[b], j0, pos[b], on_page, g);
+        if (__ballot(alpha != 1.0f) != 0) {
+#pragma unroll
+          for (int d = 0; d < DT; ++d) O[b][d] *= alpha;
+        }
+#pragma unroll
+        for (int h = 0; h < JT / 2; ++h) P[b][h] = to_frag<IT>(stack(S[b][2 * h], S[b][2 * h + 1]));
+      }
+      if (__builtin_expect(bad, 0)) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+          add_visible<IT, JT, DT>(a, S[b], O[b], Vt, kPitch, j0, pos[b], on_page, g, li);
+      } else {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int h = 0; h < JT / 2; ++h) {
+            const frag vf = frag_col<IT>(Vt, kPitch, 32 * h, 16 * d, lane);
+#pragma unroll
+            for (int b = 0; b < RB; ++b) O[b][d] = mma<IT>(vf, P[b][h], O[b][d]);
+          }
+      }
+    }
+    if (v + 1 < v1) put(buf ^ 1);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const float l = sum_groups(rs[b].l);
+    if (tok[b] >= 0) store_row<IT, DT>(a, O[b], rs[b].m, l, tok[b], head[b], split, g);
+  }
+}
+
+template <int IT, int D>
+__global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_kernel(PagedArgs a) {
+  typedef typename Mma<IT>::elem elem;
+  typedef typename Mma<IT>::frag frag;
+  constexpr int T = 32, JT = 2, KS = D / 32, DT = D / 16, W = kPagedBlock / 64;
+  constexpr int kVec = 16 / sizeof(elem), kPerRow = D / kVec, kRowsPass = 64 / kPerRow, kPasses = T / kRowsPass;
+  constexpr int kPitch = D + kVec;
+  constexpr int kTileBytes = W * T * kPitch * sizeof(elem), kJoinBytes = W * 16 * (D + 4) * 4;
+  __shared__ __align__(16) char lds[kTileBytes > kJoinBytes ? kTileBytes : kJoinBytes];
+  __shared__ float jm[W][16], jl[W][16];
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int item = xcd_order(blockIdx.x, gridDim.x);
+  const int split = item % a.nsplit;
+  item /= a.nsplit;
+  const int kvh = item % a.Hkv, s = item / a.Hkv;
+  const PagedSeq sq = paged_seq(a, s);
+  const int rows = sq.q_len * a.group;
+  if (rows == 0) return;
+  const KeyTiles kt = key_tiles<T>(a, sq.first_pos, sq.first_pos + sq.q_len - 1);
+  const int v0 = split * a.split_tiles;
+  const int v1 = split == a.nsplit - 1 || kt.count - v0 < a.split_tiles ? kt.count : v0 + a.split_tiles;
+  const bool in = li < rows;
+  const int t = in ? li / a.group : 0;
+  const int64_t tok = sq.start + t;
+  const int head = kvh * a.group + (in ? li - t * a.group : 0);
+  const int pos = in && sq.first_pos + t >= 0 ? sq.first_pos + t : -1;
+  frag Q[KS];
+  {
+    const elem* qp = reinterpret_cast<const elem*>(a.q) + tok * a.q_stride + static_cast<int64_t>(head) * D + 8 * g;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) Q[k] = frag_row<IT>(qp + 32 * k);
+  }
+  f32x4 O[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) O[d] = f32x4{0, 0, 0, 0};
+  RowState rs{-__builtin_inff(), 0.0f};
+  elem* const Vt = reinterpret_cast<elem*>(lds) + wave * T * kPitch;
+  const int64_t hoff = static_cast<int64_t>(kvh) * a.head_stride;
+  const int vec = lane % kPerRow, srow = lane / kPerRow;
+  u32x4 kr[JT][KS * sizeof(elem) / 2], vr[kPasses];
+  auto fetch = [&](int64_t row_off) {   // lane l holds the cache row of token l % 32
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt) {
+      const int64_t off = shfl64(row_off, 16 * jt + li);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const int64_t at = (off + hoff + 32 * k + 8 * g) * static_cast<int64_t>(sizeof(elem));
+        if constexpr (IT == kF32) {
+          kr[jt][2 * k] = kr[jt][2 * k + 1] = u32x4{0, 0, 0, 0};
+          if (off >= 0) {
+            kr[jt][2 * k] = ld<true, u32x4>(a.k + at);
+            kr[jt][2 * k + 1] = ld<true, u32x4>(a.k + at + 16);
+          }
+        } else {
+          kr[jt][k] = u32x4{0, 0, 0, 0};
+          if (off >= 0) kr[jt][k] = ld<true, u32x4>(a.k + at);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int64_t off = shfl64(row_off, srow + i * kRowsPass);
+      vr[i] = u32x4{0, 0, 0, 0};
+      if (off >= 0) vr[i] = ld<true, u32x4>(a.v + (off + hoff + vec * kVec) * static_cast<int64_t>(sizeof(elem)));
+    }
+  };
+  const int first = v0 + wave;
+  int64_t off = -1, off_next = -1;
+  if (first < v1) {
+    off = cache_row(a, s, key_tile(kt, first) * T + (lane & 31), kt.limit);
+    fetch(off);
+    if (first + W < v1) off_next = cache_row(a, s, key_tile(kt, first + W) * T + (lane & 31), kt.limit);
+  }
+  for (int v = first; v < v1; v += W) {
+    const int j0 = key_tile(kt, v) * T;
+    const uint64_t on_page = __ballot(off >= 0) & 0xffffffffull;
+    bool bad = false;
+    frag K[JT][KS];
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt)
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        if constexpr (IT == kF32) {
+          const u32x4 u = kr[jt][2 * k], w = kr[jt][2 * k + 1];
+          K[jt][k] = __builtin_bit_cast(frag, u32x8{u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w});
+        } else {
+          K[jt][k] = __builtin_bit_cast(frag, kr[jt][k]);
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      bad |= nonfinite16<IT>(vr[i]);
+      *reinterpret_cast<u32x4*>(Vt + (srow + i * kRowsPass) * kPitch + vec * kVec) = vr[i];
+    }
+    bad = __ballot(bad) != 0;
+    f32x4 S[JT];
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt) {
+      S[jt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) S[jt] = mma<IT>(K[jt][k], Q[k], S[jt]);
+    }
+    if (v + W < v1) {
+      off = off_next;
+      fetch(off);
+      if (v + 2 * W < v1) off_next = cache_row(a, s, key_tile(kt, v + 2 * W) * T + (lane & 31), kt.limit);
+    }
+    const float alpha = softmax_tile<JT, true>(a, S, rs, j0, pos, on_page, g);
+    if (__ballot(alpha != 1.0f) != 0) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d) O[d] *= alpha;
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (__builtin_expect(bad, 0)) {
+      add_visible<IT, JT, DT>(a, S, O, Vt, kPitch, j0, pos, on_page, g, li);
+    } else {
+      const frag P = to_frag<IT>(stack(S[0], S[1]));
+#pragma unroll
+      for (int d = 0; d < DT; ++d) O[d] = mma<IT>(frag_col<IT>(Vt, kPitch, 0, 16 * d, lane), P, O[d]);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  // join the four wavefronts
+  __syncthreads();
+  float* const jo = reinterpret_cast<float*>(lds);   // [W][16][D + 4]
+  const float l = sum_groups(rs.l);
+  if (g == 0) {
+    jm[wave][li] = rs.m;
+    jl[wave][li] = l;
+  }
+#pragma unroll
+  for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(jo + (wave * 16 + li) * (D + 4) + 16 * d + 4 * g) = O[d];
+  __syncthreads();
+  if (wave == 0) {
+    float m = jm[0][li];
+#pragma unroll
+    for (int w = 1; w < W; ++w) m = fmaxf(m, jm[w][li]);
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+    float sum = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) O[d] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = __builtin_amdgcn_exp2f(jm[w][li] - base);
+      sum += jl[w][li] * f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) O[d] += *reinterpret_cast<const f32x4*>(jo + (w * 16 + li) * (D + 4) + 16 * d + 4 * g) * f;
+    }
+    if (in) store_row<IT, DT>(a, O, m, sum, tok, head, split, g);
+  }
+}
+
+// Joins the splits of one (token, head): one wavefront, lanes over head_dim.
+template <int IT, int D>
+__global__ __launch_bounds__(kPagedBlock) void paged_join_kernel(PagedArgs a) {
+  typedef typename Mma<IT>::elem elem;
+  constexpr int E = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kPagedBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t token = row / a.Hq;
+  if (token >= a.num_tokens) return;
+  // rows that belong to no sequence were not computed: leave them alone
+  int lo = 0, hi = a.num_seqs;
+  while (lo < hi) {   // first sequence whose end lies past the token
+    const int mid = (lo + hi) >> 1;
+    if (sload(a.seq_start + mid + 1) > token) hi = mid;
+    else lo = mid + 1;
+  }
+  if (lo >= a.num_seqs) return;
+  const PagedSeq sq = paged_seq(a, lo);
+  if (token < sq.start || token - sq.start >= sq.q_len) return;
+  const int head = static_cast<int>(row - token * a.Hq);
+  const float* ml = a.part_ml + row * a.nsplit * 2;
+  const float* po = a.part_o + row * a.nsplit * D + lane * E;
+  float m = -__builtin_inff();
+  for (int k = lane; k < a.nsplit; k += 64) m = fmaxf(m, ml[2 * k]);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float base = m == -__builtin_inff() ? 0.0f : m;
+  float l = 0.0f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  for (int k0 = 0; k0 < a.nsplit; k0 += 64) {
+    float f = 0.0f, lk = 0.0f;
+    if (k0 + lane < a.nsplit) {
+      f = __builtin_amdgcn_exp2f(ml[2 * (k0 + lane)] - base);
+      lk = ml[2 * (k0 + lane) + 1] * f;
+    }
+    l += lk;
+    const int n = a.nsplit - k0 < 64 ? a.nsplit - k0 : 64;
+    for (int k = 0; k < n; ++k) {
+      const float w = __shfl(f, k);
+      if (w != 0.0f) {   // an empty split wrote no output
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(po[static_cast<int64_t>(k0 + k) * D + e], w, o[e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+  elem* out = reinterpret_cast<elem*>(a.out) + token * a.out_stride + static_cast<int64_t>(head) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float v = o[e] * inv;
+    if constexpr (IT == kF32) out[e] = v;
+    else if constexpr (IT == kBF16) out[e] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+    else out[e] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+  }
+  if (a.lse != nullptr && lane == 0) a.lse[token * a.Hq + head] = (m + log2f(l)) * kLn2;
+}
+
+// Append: one thread a 16-byte vector of one new token's keys and values.
+template <int ES>
+__global__ __launch_bounds__(kPagedBlock) void paged_append_kernel(PagedArgs a, int head_vecs) {
+  const int per = a.Hkv * head_vecs;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * kPagedBlock + threadIdx.x;
+  const int64_t token = at / per;
+  if (token >= a.num_tokens) return;
+  const int v = static_cast<int>(at - token * per), h = v / head_vecs;
+  int lo = 0, hi = a.num_seqs;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (gload(a.seq_start + mid + 1) > token) hi = mid;
+    else lo = mid + 1;
+  }
+  if (lo >= a.num_seqs) return;
+  const int start = gload(a.seq_start + lo), end = gload(a.seq_start + lo + 1);
+  if (token < start) return;
+  const int64_t j = static_cast<int64_t>(gload(a.kv_len + lo)) - (end < a.num_tokens ? end : a.num_tokens) + token;
+  if (j < 0 || j > INT32_MAX - 1) return;
+  const int64_t row = cache_row(a, lo, static_cast<int>(j), INT32_MAX);
+  if (row < 0) return;
+  const int64_t src = (token * a.new_stride) * ES + v * 16;
+  const int64_t dst = (row + h * a.head_stride) * ES + (v - h * head_vecs) * 16;
+  st<false>(a.k + dst, ld<false, u32x4>(a.k_new + src));
+  st<false>(a.v + dst, ld<false, u32x4>(a.v_new + src));
+}
+
+}  // namespace rssm

@@ -23,6 +23,7 @@
 
 #include "gdn_kernel.h"
 #include "rssm_gdn_commit.h"
+#include "rssm_host.h"
 #include "rssm_kernel.h"
 #include "rssm_materialize.h"
 #include "rssm_ssu_decode.h"
@@ -43,9 +44,13 @@ const void* gdn_kernel_for(int window);
 const void* ssu_kernel_for(int state_dtype, int input_dtype, int tokens);
 }  // namespace rssm
 
-namespace {
+namespace rssm {
 
+namespace {
 thread_local char g_err[1024];
+}
+
+void clear_error() { g_err[0] = '\0'; }
 
 rssm_status fail(rssm_status st, const char* fmt, ...) {
   va_list ap;
@@ -74,12 +79,17 @@ const char* dtype_name(int d) {
   }
 }
 
-bool one_byte(int d) { return d == RSSM_I8 || d == RSSM_F8E4M3; }
+}  // namespace rssm
 
-template <typename T>
-bool aligned(const T* p, size_t a) {
-  return (reinterpret_cast<uintptr_t>(p) % a) == 0;
-}
+namespace {
+
+using rssm::aligned;
+using rssm::clear_error;
+using rssm::dtype_name;
+using rssm::fail;
+using rssm::verbose;
+
+bool one_byte(int d) { return d == RSSM_I8 || d == RSSM_F8E4M3; }
 
 // Compiled (dim, dstate) shapes.
 bool shape_supported(int state_dtype, int dim, int dstate) {
@@ -360,11 +370,11 @@ rssm_status launch(const rssm_materialize_desc* desc, const rssm_materialize_tab
 
 extern "C" {
 
-const char* rssm_last_error(void) { return g_err; }
+const char* rssm_last_error(void) { return rssm::g_err; }
 
 rssm_status rssm_materialize_launch_config(const rssm_materialize_desc* desc, int32_t* grid, int32_t* block,
                                            int32_t* lds_bytes) {
-  g_err[0] = '\0';
+  clear_error();
   rssm_status st = validate_desc(desc);
   if (st != RSSM_OK) return st;
   if (grid == nullptr || block == nullptr || lds_bytes == nullptr)
@@ -388,13 +398,13 @@ rssm_status rssm_materialize_launch_config(const rssm_materialize_desc* desc, in
 
 rssm_status rssm_materialize(const rssm_materialize_desc* desc, const rssm_materialize_tables* tables,
                              void* hip_stream) {
-  g_err[0] = '\0';
+  clear_error();
   return launch(desc, tables, 1, hip_stream);
 }
 
 rssm_status rssm_materialize_checkpoints(const rssm_materialize_desc* desc, const rssm_materialize_tables* tables,
                                          int32_t num_checkpoints, void* hip_stream) {
-  g_err[0] = '\0';
+  clear_error();
   if (num_checkpoints < 1 || num_checkpoints > RSSM_MAX_CHECKPOINTS)
     return fail(RSSM_ERR_INVALID_ARGUMENT, "num_checkpoints must be in [1, %d] (got %d)", RSSM_MAX_CHECKPOINTS,
                 num_checkpoints);
@@ -402,7 +412,7 @@ rssm_status rssm_materialize_checkpoints(const rssm_materialize_desc* desc, cons
 }
 
 rssm_status rssm_gdn_commit(const rssm_gdn_commit_desc* d, const rssm_gdn_commit_tables* t, void* hip_stream) {
-  g_err[0] = '\0';
+  clear_error();
   if (d == nullptr) return fail(RSSM_ERR_INVALID_ARGUMENT, "desc is NULL");
   if (d->num_layers < 1) return fail(RSSM_ERR_INVALID_ARGUMENT, "num_layers must be >= 1 (got %d)", d->num_layers);
   if (d->slots < 1) return fail(RSSM_ERR_INVALID_ARGUMENT, "slots must be >= 1 (got %d)", d->slots);
@@ -473,7 +483,7 @@ rssm_status rssm_gdn_commit(const rssm_gdn_commit_desc* d, const rssm_gdn_commit
 }
 
 rssm_status rssm_ssu_decode(const rssm_ssu_decode_desc* d, const rssm_ssu_decode_tables* t, void* hip_stream) {
-  g_err[0] = '\0';
+  clear_error();
   if (d == nullptr) return fail(RSSM_ERR_INVALID_ARGUMENT, "desc is NULL");
   if (d->batch < 0) return fail(RSSM_ERR_INVALID_ARGUMENT, "batch must be >= 0 (got %d)", d->batch);
   if (d->num_heads < 1) return fail(RSSM_ERR_INVALID_ARGUMENT, "num_heads must be >= 1 (got %d)", d->num_heads);
@@ -593,7 +603,7 @@ rssm_status rssm_ssu_decode(const rssm_ssu_decode_desc* d, const rssm_ssu_decode
 rssm_status rssm_debug_encode_rows(const rssm_materialize_desc* desc, const float* rows, const int32_t* coords,
                                    const int64_t* rand_seed, void* out_codes, float* out_scales, int32_t n,
                                    void* hip_stream) {
-  g_err[0] = '\0';
+  clear_error();
   if (desc == nullptr) return fail(RSSM_ERR_INVALID_ARGUMENT, "desc is NULL");
   if (desc->state_dtype < RSSM_F32 || desc->state_dtype > RSSM_F8E4M3)
     return fail(RSSM_ERR_INVALID_ARGUMENT, "unknown state_dtype %d", desc->state_dtype);
@@ -624,7 +634,7 @@ rssm_status rssm_debug_encode_rows(const rssm_materialize_desc* desc, const floa
 
 rssm_status rssm_debug_row_scales(int32_t state_dtype, const float* rowmax, float* scale, float* inv, int32_t n,
                                   void* hip_stream) {
-  g_err[0] = '\0';
+  clear_error();
   if (state_dtype != RSSM_I8 && state_dtype != RSSM_F8E4M3)
     return fail(RSSM_ERR_INVALID_ARGUMENT, "state_dtype must be a one-byte state (I8 or F8E4M3), got %d",
                 state_dtype);
