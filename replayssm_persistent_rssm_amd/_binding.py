@@ -526,13 +526,41 @@ class SsuDecodeCall:
             raise RssmError(st, rssm_last_error())
 
 
-def _rows(t, name: str, dtype, shape, device):
-    """(address, token stride) of a [tokens, ...] tensor whose rows are dense inside."""
+# --------------------------------------------------------------------------
+# Prompt-side operators.  These calls are a few microseconds of GPU work at
+# their smallest, so the common case (contiguous tensors of the right shape) is
+# checked with few attribute reads, and everything else, errors included, goes the
+# long way.
+# --------------------------------------------------------------------------
+_TORCH_CODES = {}
+
+
+def _code(dt) -> int:
+    c = _TORCH_CODES.get(dt)
+    if c is None:
+        c = _TORCH_CODES[dt] = dtype_code(dt)
+    return c
+
+
+def _device_index(t, name: str) -> int:
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor (got {t.device})")
+    return t.get_device()
+
+
+def _rows(t, name: str, dtype, shape, dense: int, index: int):
+    """(address, row stride) of a [rows, ...] tensor whose rows are dense inside
+    (`dense` elements a row)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr(), dense
+    except AttributeError:
+        pass
+    if _device_index(t, name) != index:
+        raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
     if t.dtype != dtype:
         raise ValueError(f"{name} must have dtype {dtype} (got {t.dtype})")
     if t.shape != shape:
@@ -542,186 +570,200 @@ def _rows(t, name: str, dtype, shape, device):
         if n != 1 and stride != want:
             raise ValueError(f"{name} must be dense inside a row (strides {t.stride()})")
         want *= n
-    # one row: its stride says nothing, and an expanded row would be below the dense size
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else want)
+    # the stride of a single row says nothing
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else dense)
 
 
-def _device_of(t, name: str):
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a device tensor (got {t.device})")
-    return t.device
+def _vec(t, name: str, dtype, n: int, index: int):
+    """Address of an optional contiguous vector of n elements."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.shape == (n,) and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if _device_index(t, name) != index:
+        raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
+    return _ptr(t, name, dtype, (n,))
 
 
-def _same_device(device, tensors) -> None:
-    for name, t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device} (got {t.device})")
+def _stride_of_one(elems: int, elem_size: int) -> int:
+    """A legal stride for a dimension that is never stepped over: `elems` rounded up to 16 bytes."""
+    step = 16 // elem_size
+    return (elems + step - 1) // step * step
 
 
-def _aligned_stride(stride: int, elem: int) -> int:
-    """A dense row stride rounded up to 16 bytes (for a tensor of one row or
-    none, where any legal value does)."""
-    step = 16 // elem
-    return (stride + step - 1) // step * step
+def _stream_of(index: int, stream) -> int:
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _workspace(nbytes: int, given, device, stream):
+def _workspace(nbytes: int, given, index: int, stream):
     """The caller's workspace after a check, or a new one that lives on the call's stream."""
     import torch
     if given is not None:
-        if _device_of(given, "workspace") != device or not given.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        if _device_index(given, "workspace") != index or not given.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
         return given
     if nbytes == 0:
         return None
+    dev = torch.device("cuda", index)
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
     with torch.cuda.stream(s):      # the allocator reuses it in that stream's order
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
-def _launch(fn, desc, tab, device, stream) -> None:
+def _launch(fn, desc, tab, index: int, stream) -> None:
     """One library call on `stream` (default: torch's current stream of the tensors' device)."""
     import torch
-    if device.index == torch.cuda.current_device():
-        _check(fn(ctypes.byref(desc), ctypes.byref(tab), _stream_handle(stream)))
+    if index == torch._C._cuda_getDevice():
+        st = fn(desc, tab, _stream_of(index, stream))
     else:
-        with torch.cuda.device(device):
-            _check(fn(ctypes.byref(desc), ctypes.byref(tab), _stream_handle(stream)))
+        with torch.cuda.device(index):
+            st = fn(desc, tab, _stream_of(index, stream))
+    if st != RSSM_OK:
+        raise RssmError(st, rssm_last_error())
 
 
-def _linear_marshal(state, A, x, B, C, dt, y, slots, seq_start=None, *, max_seq_len=None, load_state=None, D=None,
+def _give_workspace(desc, tab, query, given, index: int, stream):
+    need = ctypes.c_int64()
+    _check(query(desc, need))
+    if need.value == 0 and given is None:
+        return None
+    ws = _workspace(need.value, given, index, stream)
+    tab.workspace = ws.data_ptr()
+    desc.workspace_bytes = ws.numel() * ws.element_size()
+    return ws
+
+
+def _linear_marshal(state, A, x, B, C, dt, y, slots, seq_start=None, max_seq_len=1, load_state=None, D=None,
                     dt_bias=None, z=None, dt_softplus: bool = True, pad_slot_id: int = -1):
     import torch
-    dev = _device_of(state, "state")
+    dev = _device_index(state, "state")
     if state.dim() != 4:
         raise ValueError("state must be a pool [slots, H, dim, dstate]")
-    if x.dim() != 3 or B.dim() != 3:
-        raise ValueError("x must be [tokens, H, dim] and B [tokens, G, dstate]")
+    if x.dim() != 3 or B.dim() != 3 or slots.dim() != 1:
+        raise ValueError("x must be [tokens, H, dim], B [tokens, G, dstate] and slots [sequences]")
     S, H, dim, dstate = state.shape
     N, G = x.shape[0], B.shape[1]
     if G < 1 or H % G != 0:
         raise ValueError(f"the group count of B ({G}) must divide the head count ({H})")
-    if S and (state.stride(3) != 1 or state.stride(2) != dstate or (H > 1 and state.stride(1) != dim * dstate)):
-        raise ValueError("state must be dense inside a slot")
+    slot_stride = H * dim * dstate
+    if not state.is_contiguous():
+        if state.stride(3) != 1 or state.stride(2) != dstate or (H > 1 and state.stride(1) != dim * dstate):
+            raise ValueError("state must be dense inside a slot")
+        if S > 1:
+            slot_stride = state.stride(0)
     f32, i32, idt = torch.float32, torch.int32, x.dtype
     R = slots.shape[0]
-    xp, xs = _rows(x, "x", idt, (N, H, dim), dev)
-    Bp, Bs = _rows(B, "B", idt, (N, G, dstate), dev)
-    Cp, Cs = _rows(C, "C", idt, (N, G, dstate), dev)
-    yp, ys = _rows(y, "y", idt, (N, H, dim), dev)
-    zp, zs = _rows(z, "z", idt, (N, H, dim), dev) if z is not None else (None, xs)
-    dp, ds = _rows(dt, "dt", f32, (N, H), dev) if dt is not None else (None, H)
-    _same_device(dev, (("A", A), ("D", D), ("dt_bias", dt_bias), ("slots", slots), ("seq_start", seq_start),
-                       ("load_state", load_state)))
-    prompt = seq_start is not None
-    desc = RssmLinearDesc(
-        num_seqs=_scalar("num_seqs", R), num_tokens=_scalar("num_tokens", N), num_heads=_scalar("num_heads", H),
-        heads_per_group=_scalar("hpg", H // G), dim=_scalar("dim", dim), dstate=_scalar("dstate", dstate),
-        num_slots=_scalar("num_slots", S), pad_slot_id=_scalar("pad_slot_id", pad_slot_id),
-        max_seq_len=_scalar("max_seq_len", max_seq_len) if prompt else 1, state_dtype=dtype_code(state.dtype),
-        input_dtype=dtype_code(idt), dt_softplus=1 if dt_softplus and dt is not None else 0,
-        state_slot_stride=state.stride(0) if S > 1 else H * dim * dstate, x_token_stride=xs, B_token_stride=Bs,
-        C_token_stride=Cs, dt_token_stride=ds, z_token_stride=zs, y_token_stride=ys, workspace_bytes=0)
+    row, brow = H * dim, G * dstate
+    shape, bshape = (N, H, dim), (N, G, dstate)
+    xp, xs = _rows(x, "x", idt, shape, row, dev)
+    Bp, Bs = _rows(B, "B", idt, bshape, brow, dev)
+    Cp, Cs = _rows(C, "C", idt, bshape, brow, dev)
+    yp, ys = _rows(y, "y", idt, shape, row, dev)
+    zp, zs = _rows(z, "z", idt, shape, row, dev) if z is not None else (None, row)
+    dp, ds = _rows(dt, "dt", f32, (N, H), H, dev) if dt is not None else (None, H)
+    for name, v in (("num_tokens", N), ("num_seqs", R), ("num_slots", S), ("num_heads", H), ("pad_slot_id", pad_slot_id),
+                    ("max_seq_len", max_seq_len)):
+        if not -_INT32_MAX - 1 <= v <= _INT32_MAX:
+            raise ValueError(f"{name}={v} does not fit the library's int32 parameter")
+    desc = RssmLinearDesc(R, N, H, H // G, dim, dstate, S, pad_slot_id, max_seq_len, _code(state.dtype), _code(idt),
+                          1 if dt_softplus and dt is not None else 0, slot_stride, xs, Bs, Cs, ds, zs, ys, 0)
     tab = RssmLinearTables(
-        state=state.data_ptr(), A=_ptr(A, "A", f32, (H,)), D=_ptr(D, "D", f32, (H,)),
-        dt_bias=_ptr(dt_bias, "dt_bias", f32, (H,)), x=xp, B=Bp, C=Cp, dt=dp, z=zp, y=yp,
-        slots=_ptr(slots, "slots", i32, (R,)), seq_start=_ptr(seq_start, "seq_start", i32, (R + 1,)),
-        load_state=_ptr(load_state, "load_state", i32, (R,)), workspace=None)
+        state.data_ptr(), _vec(A, "A", f32, H, dev), _vec(D, "D", f32, H, dev), _vec(dt_bias, "dt_bias", f32, H, dev),
+        xp, Bp, Cp, dp, zp, yp, _vec(slots, "slots", i32, R, dev), _vec(seq_start, "seq_start", i32, R + 1, dev),
+        _vec(load_state, "load_state", i32, R, dev), None)
     return desc, tab, dev
 
 
-def _give_workspace(desc, tab, query, given, device, stream):
-    need = ctypes.c_int64()
-    _check(query(ctypes.byref(desc), ctypes.byref(need)))
-    ws = _workspace(need.value, given, device, stream)
-    if ws is not None:
-        tab.workspace = ws.data_ptr()
-        desc.workspace_bytes = ws.numel() * ws.element_size()
-    return ws
-
-
-def rssm_linear_attention(state, A, x, B, C, dt, y, slots, seq_start, *, max_seq_len: int, workspace=None,
-                          stream=None, **kw) -> None:
+def rssm_linear_attention(state, A, x, B, C, dt, y, slots, seq_start, *, max_seq_len: int, load_state=None, D=None,
+                          dt_bias=None, z=None, dt_softplus: bool = True, pad_slot_id: int = -1, workspace=None,
+                          stream=None) -> None:
     """Enqueue linear attention with a decay for each head over ragged prompts
     (one layer): y and the slots' new states.  state pool [slots, H, dim,
-    dstate] (f32/bf16/f16, updated in place), A fp32 [H], x [N, H, dim], B / C [N, G,
-    dstate], dt fp32 [N, H] (raw) or None (dt = 1), y [N, H, dim] (dtype of x),
-    slots int32 [R], seq_start int32 [R + 1] (sequence r owns rows
-    seq_start[r] .. seq_start[r+1] - 1).  Rows of x, B, C, dt, z and y may be views of a
-    wider row.  Keywords: max_seq_len (required, the longest sequence),
-    load_state int32 [R] (0: start from a zero state), D, dt_bias fp32 [H], z,
-    dt_softplus=True, pad_slot_id=-1, workspace (uint8 tensor of
+    dstate] (f32/bf16/f16, updated in place), A fp32 [H], x [N, H, dim], B / C
+    [N, G, dstate], dt fp32 [N, H] (raw) or None (dt = 1), y [N, H, dim] (dtype
+    of x), slots int32 [R], seq_start int32 [R + 1] (sequence r owns rows
+    seq_start[r] .. seq_start[r+1] - 1).  Rows of x, B, C, dt, z and y may be
+    views of a wider row.  Keywords: max_seq_len (required, the longest
+    sequence), load_state int32 [R] (0: start from a zero state), D, dt_bias fp32
+    [H], z, dt_softplus=True, pad_slot_id=-1, workspace (uint8 tensor of
     rssm_linear_attention_workspace's size; allocated when needed and not given)."""
-    desc, tab, dev = _linear_marshal(state, A, x, B, C, dt, y, slots, seq_start, max_seq_len=max_seq_len, **kw)
+    desc, tab, dev = _linear_marshal(state, A, x, B, C, dt, y, slots, seq_start, max_seq_len, load_state, D, dt_bias, z,
+                                     dt_softplus, pad_slot_id)
     ws = _give_workspace(desc, tab, _lib.rssm_linear_attention_workspace, workspace, dev, stream)  # noqa: F841
     _launch(_lib.rssm_linear_attention, desc, tab, dev, stream)
 
 
-def rssm_linear_attention_workspace(state, A, x, B, C, dt, y, slots, seq_start, *, max_seq_len: int, **kw) -> int:
+def rssm_linear_attention_workspace(state, A, x, B, C, dt, y, slots, seq_start, *, max_seq_len: int) -> int:
     """Workspace bytes of rssm_linear_attention for these arguments."""
-    desc, _, _ = _linear_marshal(state, A, x, B, C, dt, y, slots, seq_start, max_seq_len=max_seq_len, **kw)
+    desc, _, _ = _linear_marshal(state, A, x, B, C, dt, y, slots, seq_start, max_seq_len)
     need = ctypes.c_int64()
-    _check(_lib.rssm_linear_attention_workspace(ctypes.byref(desc), ctypes.byref(need)))
+    _check(_lib.rssm_linear_attention_workspace(desc, need))
     return need.value
 
 
-def rssm_linear_attention_step(state, A, x, B, C, dt, y, slots, *, stream=None, **kw) -> None:
+def rssm_linear_attention_step(state, A, x, B, C, dt, y, slots, *, D=None, dt_bias=None, z=None,
+                               dt_softplus: bool = True, pad_slot_id: int = -1, stream=None) -> None:
     """Enqueue the single-token form: row r of x, B, C, dt, z and y is request
     r's token.  Arguments as rssm_linear_attention without seq_start,
     max_seq_len, load_state and workspace."""
-    if "load_state" in kw or "max_seq_len" in kw:
-        raise TypeError("the single-token form takes no load_state and no max_seq_len")
-    desc, tab, dev = _linear_marshal(state, A, x, B, C, dt, y, slots, **kw)
+    desc, tab, dev = _linear_marshal(state, A, x, B, C, dt, y, slots, None, 1, None, D, dt_bias, z, dt_softplus,
+                                     pad_slot_id)
     _launch(_lib.rssm_linear_attention_step, desc, tab, dev, stream)
 
 
 def _paged_caches(k_cache, v_cache, page_table, seq_start, kv_len):
     """Descriptor and table fields of the caches and their metadata."""
     import torch
-    dev = _device_of(k_cache, "k_cache")
+    dev = _device_index(k_cache, "k_cache")
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [pages, page_size, kv_heads, head_dim] (any strides with dense head_dim)")
-    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride() or v_cache.dtype != k_cache.dtype:
-        raise ValueError("v_cache must have k_cache's shape, strides and dtype")
-    if k_cache.shape[3] != 1 and k_cache.stride(3) != 1:
-        raise ValueError("head_dim of the caches must be dense")
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be int32 [seqs, pages] with dense rows")
+    shape, strides, kdt = k_cache.shape, k_cache.stride(), k_cache.dtype
+    if v_cache.shape != shape or v_cache.stride() != strides or v_cache.dtype != kdt or v_cache.get_device() != dev:
+        raise ValueError("v_cache must have k_cache's shape, strides, dtype and device")
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.get_device() != dev or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be int32 [seqs, pages] on cuda:{dev} with dense rows")
     S, M = page_table.shape
-    _same_device(dev, (("v_cache", v_cache), ("page_table", page_table), ("seq_start", seq_start), ("kv_len", kv_len)))
-    P, ps, Hkv, D = k_cache.shape
-    # a dimension of one entry is never stepped over: any legal stride will do
-    st = [t if n > 1 else _aligned_stride(D, k_cache.element_size()) for n, t in zip(k_cache.shape, k_cache.stride())]
-    desc = RssmPagedDesc(
-        num_seqs=_scalar("num_seqs", S), num_kv_heads=_scalar("kv_heads", Hkv), head_dim=_scalar("head_dim", D),
-        page_size=_scalar("page_size", ps), num_pages=_scalar("num_pages", P), max_pages=_scalar("max_pages", M),
-        dtype=dtype_code(k_cache.dtype), page_stride=st[0], row_stride=st[1], head_stride=st[2],
-        table_stride=page_table.stride(0) if S > 1 else M)
-    tab = RssmPagedTables(k_cache=k_cache.data_ptr(), v_cache=v_cache.data_ptr(), page_table=page_table.data_ptr(),
-                          seq_start=_ptr(seq_start, "seq_start", torch.int32, (S + 1,)),
-                          kv_len=_ptr(kv_len, "kv_len", torch.int32, (S,)))
+    P, ps, Hkv, D = shape
+    if strides[3] != 1 and D != 1:
+        raise ValueError("head_dim of the caches must be dense")
+    if not k_cache.is_contiguous() or P < 2 or ps < 2 or Hkv < 2:
+        one = _stride_of_one(D, k_cache.element_size())
+        strides = [t if n > 1 else one for n, t in zip(shape, strides)]
+    for name, v in (("seqs", S), ("kv_heads", Hkv), ("page_size", ps), ("pages", P), ("page_table columns", M)):
+        if v > _INT32_MAX:
+            raise ValueError(f"{name}={v} does not fit the library's int32 parameter")
+    desc = RssmPagedDesc(S, 0, 0, Hkv, D, ps, P, M, 0, 0, 0, 0, _code(kdt), 0.0, strides[0], strides[1], strides[2],
+                         0, 0, 0, page_table.stride(0) if S > 1 else M, 0)
+    tab = RssmPagedTables(k_cache.data_ptr(), v_cache.data_ptr(), None, None, None, None, None, page_table.data_ptr(),
+                          _vec(seq_start, "seq_start", torch.int32, S + 1, dev), _vec(kv_len, "kv_len", torch.int32, S, dev),
+                          None)
     return desc, tab, dev
 
 
 def rssm_paged_append(k_cache, v_cache, k_new, v_new, page_table, seq_start, kv_len, *, stream=None) -> None:
     """Enqueue the append of new tokens to a paged cache: sequence s's rows
-    seq_start[s] .. seq_start[s+1] - 1 of k_new / v_new [N, kv_heads, head_dim] go to its
-    last positions before kv_len[s] (int32 [S], the new tokens counted).
-    Caches [pages, page_size, kv_heads, head_dim], any strides with dense
-    head_dim, both alike; page_table int32 [S, pages] (entries outside
+    seq_start[s] .. seq_start[s+1] - 1 of k_new / v_new [N, kv_heads, head_dim]
+    go to its last positions before kv_len[s] (int32 [S], the new tokens
+    counted).  Caches [pages, page_size, kv_heads, head_dim], any strides with
+    dense head_dim, both alike; page_table int32 [S, pages] (entries outside
     [0, pages) are skipped)."""
     desc, tab, dev = _paged_caches(k_cache, v_cache, page_table, seq_start, kv_len)
-    shape = (k_new.shape[0], k_cache.shape[2], k_cache.shape[3])
-    tab.k_new, ks = _rows(k_new, "k_new", k_cache.dtype, shape, dev)
-    tab.v_new, vs = _rows(v_new, "v_new", k_cache.dtype, shape, dev)
+    N, dense = k_new.shape[0], desc.num_kv_heads * desc.head_dim
+    shape = (N, desc.num_kv_heads, desc.head_dim)
+    tab.k_new, ks = _rows(k_new, "k_new", k_cache.dtype, shape, dense, dev)
+    tab.v_new, vs = _rows(v_new, "v_new", k_cache.dtype, shape, dense, dev)
     if ks != vs:
         raise ValueError("k_new and v_new must have the same row stride")
-    desc.num_tokens = _scalar("num_tokens", shape[0])
+    desc.num_tokens = _scalar("num_tokens", N)
     desc.new_token_stride = ks
     _launch(_lib.rssm_paged_append, desc, tab, dev, stream)
 
@@ -732,11 +774,12 @@ def _paged_marshal(q, k_cache, v_cache, page_table, seq_start, kv_len, out, *, m
     desc, tab, dev = _paged_caches(k_cache, v_cache, page_table, seq_start, kv_len)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, q_heads, head_dim]")
-    N, Hq, D = q.shape[0], q.shape[1], k_cache.shape[3]
-    tab.q, desc.q_token_stride = _rows(q, "q", k_cache.dtype, (N, Hq, D), dev)
-    tab.out, desc.out_token_stride = _rows(out, "out", k_cache.dtype, (N, Hq, D), dev)
+    N, Hq, D, kdt = q.shape[0], q.shape[1], desc.head_dim, k_cache.dtype
+    tab.q, desc.q_token_stride = _rows(q, "q", kdt, (N, Hq, D), Hq * D, dev)
+    tab.out, desc.out_token_stride = _rows(out, "out", kdt, (N, Hq, D), Hq * D, dev)
     if lse is not None:
-        _same_device(dev, (("lse", lse),))
+        if _device_index(lse, "lse") != dev:
+            raise ValueError(f"lse must be on cuda:{dev} (got {lse.device})")
         tab.lse = _ptr(lse, "lse", torch.float32, (N, Hq))
     desc.num_tokens = _scalar("num_tokens", N)
     desc.num_q_heads = _scalar("q_heads", Hq)
@@ -754,11 +797,11 @@ def rssm_paged_attention(q, k_cache, v_cache, page_table, seq_start, kv_len, out
     seq_start[s+1] - seq_start[s] of its kv_len[s] cached tokens) over a paged
     cache.  q, out [N, q_heads, head_dim] (rows may be views of wider ones);
     caches and tables as rssm_paged_append, which comes first.  Keywords:
-    max_seq_len, max_kv_len (required: the longest of the call), scale
-    (default head_dim ** -0.5), window=0 (tokens seen up to and including the query's; 0: all), sinks=0 (first
-    tokens seen beside the window), lse fp32 [N, q_heads] (optional output),
-    workspace (uint8 tensor of rssm_paged_attention_workspace's size;
-    allocated when needed and not given)."""
+    max_seq_len, max_kv_len (required: the longest of the call), scale (default
+    head_dim ** -0.5), window=0 (tokens seen up to and including the query's; 0:
+    all), sinks=0 (first tokens seen beside the window), lse fp32 [N, q_heads]
+    (optional output), workspace (uint8 tensor of
+    rssm_paged_attention_workspace's size; allocated when needed and not given)."""
     desc, tab, dev = _paged_marshal(q, k_cache, v_cache, page_table, seq_start, kv_len, out, **kw)
     ws = _give_workspace(desc, tab, _lib.rssm_paged_attention_workspace, workspace, dev, stream)  # noqa: F841
     _launch(_lib.rssm_paged_attention, desc, tab, dev, stream)
@@ -768,7 +811,7 @@ def rssm_paged_attention_workspace(q, k_cache, v_cache, page_table, seq_start, k
     """Workspace bytes of rssm_paged_attention for these arguments."""
     desc, _, _ = _paged_marshal(q, k_cache, v_cache, page_table, seq_start, kv_len, out, **kw)
     need = ctypes.c_int64()
-    _check(_lib.rssm_paged_attention_workspace(ctypes.byref(desc), ctypes.byref(need)))
+    _check(_lib.rssm_paged_attention_workspace(desc, need))
     return need.value
 
 
@@ -777,34 +820,29 @@ def rssm_block_norm(y, residual, residual_out, normed=None, *, z=None, post_weig
                     stream=None) -> None:
     """Enqueue the norms around a block, row by row of [rows, channels]:
     u = y silu(z); v = u post_weight / rms of its group; residual_out =
-    residual + residual_scale channel_scale v; normed = residual_out
-    pre_weight / rms of the row (from the unrounded sum).  y, z and normed share one
-    dtype, residual and residual_out another; post_weight, pre_weight and
-    channel_scale are fp32 [channels].  post_weight=None: no norm of the block's
-    output; z, channel_scale, pre_weight and normed are optional.  residual_out may be
-    residual, normed may be y."""
+    residual + residual_scale channel_scale v; normed = residual_out pre_weight
+    / rms of the row (from the unrounded sum).  y, z and normed share one dtype,
+    residual and residual_out another; post_weight, pre_weight and
+    channel_scale are fp32 [channels].  post_weight=None: no norm of the
+    block's output; z, channel_scale, pre_weight and normed are optional.
+    residual_out may be residual, normed may be y."""
     import torch
-    dev = _device_of(y, "y")
+    dev = _device_index(y, "y")
     if y.dim() != 2:
         raise ValueError("y must be [rows, channels]")
-    R, C = y.shape
+    shape = y.shape
+    R, C = shape
     idt, rdt, f32 = y.dtype, residual.dtype, torch.float32
-    desc = RssmNormDesc(rows=_scalar("rows", R), channels=_scalar("channels", C), groups=_scalar("groups", groups),
-                        input_dtype=dtype_code(idt), residual_dtype=dtype_code(rdt), eps=float(eps),
-                        residual_scale=float(residual_scale))
-    tab = RssmNormTables()
-    tab.y, desc.y_row_stride = _rows(y, "y", idt, (R, C), dev)
-    tab.residual, desc.residual_row_stride = _rows(residual, "residual", rdt, (R, C), dev)
-    tab.residual_out, desc.residual_out_row_stride = _rows(residual_out, "residual_out", rdt, (R, C), dev)
-    desc.z_row_stride = desc.normed_row_stride = desc.y_row_stride
-    if z is not None:
-        tab.z, desc.z_row_stride = _rows(z, "z", idt, (R, C), dev)
-    if normed is not None:
-        tab.normed, desc.normed_row_stride = _rows(normed, "normed", idt, (R, C), dev)
-    _same_device(dev, (("post_weight", post_weight), ("pre_weight", pre_weight), ("channel_scale", channel_scale)))
-    tab.post_weight = _ptr(post_weight, "post_weight", f32, (C,))
-    tab.pre_weight = _ptr(pre_weight, "pre_weight", f32, (C,))
-    tab.channel_scale = _ptr(channel_scale, "channel_scale", f32, (C,))
+    yp, ys = _rows(y, "y", idt, shape, C, dev)
+    rp, rs = _rows(residual, "residual", rdt, shape, C, dev)
+    op, os_ = _rows(residual_out, "residual_out", rdt, shape, C, dev)
+    zp, zs = _rows(z, "z", idt, shape, C, dev) if z is not None else (None, ys)
+    np_, ns = _rows(normed, "normed", idt, shape, C, dev) if normed is not None else (None, ys)
+    desc = RssmNormDesc(_scalar("rows", R), _scalar("channels", C), _scalar("groups", groups), _code(idt), _code(rdt),
+                        eps, residual_scale, ys, zs, rs, os_, ns)
+    tab = RssmNormTables(yp, zp, rp, _vec(post_weight, "post_weight", f32, C, dev),
+                         _vec(pre_weight, "pre_weight", f32, C, dev),
+                         _vec(channel_scale, "channel_scale", f32, C, dev), op, np_)
     _launch(_lib.rssm_block_norm, desc, tab, dev, stream)
 
 

@@ -338,20 +338,12 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
         for (int r = 0; r < 4; ++r) bad |= !(fabsf(acc[r]) < __builtin_inff());
       }
       if (__builtin_expect(__ballot(bad) != 0, 0)) {
-        // a non-finite x times the zero weight of a later token is not zero:
-        // add the visible tokens one by one instead
-        for (int p = 0; p < 4; ++p) X[p] = f32x4{0, 0, 0, 0};
-        for (int jt = 0; jt < 4; ++jt)
-          for (int e = 0; e < 16; ++e) {
-            const f32x4 src = jt == 0 ? M[0] : jt == 1 ? M[1] : jt == 2 ? M[2] : M[3];
-            const int r = e & 3;
-            const float own = r == 0 ? src[0] : r == 1 ? src[1] : r == 2 ? src[2] : src[3];
-            const float m = __shfl(own, (e >> 2) * 16 + li);
-            const int j = 16 * jt + e;
-            if (j <= i)
-              for (int p = 0; p < 4; ++p)
-                X[p] += widen4<IT>(L.Xs + j * LinLds<IT, N>::kP + 16 * p + 4 * g) * m;
-          }
+        // a non-finite x may have met the zero weight of a later token
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          X[p] = mma_seen<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 0, 16 * p, lane), m0, f32x4{0, 0, 0, 0});
+          X[p] = mma_seen<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 32, 16 * p, lane), m1, X[p]);
+        }
       }
       if (i < rows) {
         const int64_t row = q.start + t + i;

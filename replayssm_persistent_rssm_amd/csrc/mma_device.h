@@ -104,6 +104,36 @@ __device__ __forceinline__ typename Mma<IT>::frag frag_col(const typename Mma<IT
   }
 }
 
+// c + v p for a fragment v that holds infinities or NaN: a lane's column takes
+// them only from terms whose weight p is not zero (0 times infinity is not 0).  The
+// finite part goes through one product; the others count the +infinities and
+// -infinities among the terms that each column sees (a NaN counts as both).
+template <int IT>
+__device__ __forceinline__ f32x4 mma_seen(typename Mma<IT>::frag v, typename Mma<IT>::frag p, f32x4 c) {
+  const f32x8 x = from_frag<IT>(v), w = from_frag<IT>(p);
+  f32x8 fin, pos, neg, plus, minus;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const bool odd = !(fabsf(x[e]) < __builtin_inff());
+    fin[e] = odd ? 0.0f : x[e];
+    pos[e] = odd && x[e] != -__builtin_inff() ? 1.0f : 0.0f;
+    neg[e] = odd && x[e] != __builtin_inff() ? 1.0f : 0.0f;
+    plus[e] = w[e] >= 0.0f ? (w[e] > 0.0f ? 1.0f : 0.0f) : (w[e] < 0.0f ? 0.0f : 1.0f);
+    minus[e] = w[e] <= 0.0f ? (w[e] < 0.0f ? 1.0f : 0.0f) : (w[e] > 0.0f ? 0.0f : 1.0f);
+  }
+  typedef typename Mma<IT>::frag frag;
+  const f32x4 zero = f32x4{0, 0, 0, 0};
+  const frag fp = to_frag<IT>(pos), fn = to_frag<IT>(neg), sp = to_frag<IT>(plus), sm = to_frag<IT>(minus);
+  c = mma<IT>(to_frag<IT>(fin), p, c);
+  const f32x4 up = mma<IT>(fn, sm, mma<IT>(fp, sp, zero)), down = mma<IT>(fp, sm, mma<IT>(fn, sp, zero));
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (up[r] != 0.0f) c[r] += __builtin_inff();
+    if (down[r] != 0.0f) c[r] -= __builtin_inff();
+  }
+  return c;
+}
+
 // Split fragment of two stacked D tiles.
 __device__ __forceinline__ f32x8 stack(f32x4 a, f32x4 b) {
   return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};

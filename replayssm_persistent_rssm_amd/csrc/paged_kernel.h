@@ -68,14 +68,14 @@ __device__ __forceinline__ int page_of(const PagedArgs& a, int j) {
   return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(j)) * a.page_magic) >> a.page_shift);
 }
 
-// Cache row of token j of sequence s in elements (head 0), -1 when it lies on no page.
-__device__ __forceinline__ int64_t cache_row(const PagedArgs& a, int s, int j, int limit) {
-  if (j >= limit) return -1;
+// Cache row of token j of sequence s in elements (head 0); row 0 of the cache,
+// and ok = false, when the token lies on no page or at or past `limit`.
+__device__ __forceinline__ int64_t cache_row(const PagedArgs& a, int s, int j, int limit, bool& ok) {
   const int pi = page_of(a, j);
-  if (pi >= a.max_pages) return -1;
-  const int page = gload(a.table + s * a.table_stride + pi);
-  if (page < 0 || page >= a.num_pages) return -1;
-  return page * a.page_stride + (j - pi * a.page_size) * a.row_stride;
+  ok = (j < limit) & (pi < a.max_pages);
+  const int page = gload(a.table + s * a.table_stride + (ok ? pi : 0));
+  ok &= (page >= 0) & (page < a.num_pages);
+  return ok ? page * a.page_stride + (j - pi * a.page_size) * a.row_stride : 0;
 }
 
 // Tiles of T keys that rows at positions [pmin, pmax] see: the first `sink`
@@ -108,10 +108,6 @@ __device__ __forceinline__ KeyTiles key_tiles(const PagedArgs& a, int pmin, int 
 
 __device__ __forceinline__ int key_tile(const KeyTiles& k, int v) { return v < k.sink ? v : k.lo + (v - k.sink); }
 
-__device__ __forceinline__ bool visible(const PagedArgs& a, int j, int pos) {
-  return j <= pos && (a.window == 0 || j > pos - a.window || j < a.sinks);
-}
-
 // Whether any of 16 raw bytes' elements is infinite or NaN.
 template <int IT>
 __device__ __forceinline__ bool nonfinite16(u32x4 v) {
@@ -125,31 +121,44 @@ __device__ __forceinline__ bool nonfinite16(u32x4 v) {
   return any != 0;
 }
 
+// Scores of tokens a row may not see become -infinity.  bits: bit j where token
+// j0 + j of the tile is on a page.
+template <int JT>
+__device__ __forceinline__ void mask_tile(const PagedArgs& a, f32x4 (&S)[JT], int j0, int pos, uint64_t bits, int g) {
+  const int rel = pos - j0 - 4 * g;                       // o = j - j0 - 4g is visible up to here,
+  const int low = a.window > 0 ? rel - a.window : -1;     // past here (o >= 0 > -1 without a window)
+  const int sink = a.sinks - j0 - 4 * g;                  // or before here
+#pragma unroll
+  for (int jt = 0; jt < JT; ++jt) {
+    const uint32_t on = static_cast<uint32_t>(bits >> (32 * (jt / 2))) >> (4 * g);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int o = 16 * jt + r;
+      const bool see = (o <= rel) & ((o > low) | (o < sink)) & ((on & (1u << (o & 31))) != 0);
+      S[jt][r] = see ? S[jt][r] : -__builtin_inff();
+    }
+  }
+}
+
 // Running softmax of one row block (column li of each lane).
 struct RowState {
-  float m, l;   // maximum (log2 units) and the lane's part of the sum
+  float m, l;   // reference point of the exponents (log2 units) and the lane's part of the sum
 };
 
-// One tile of JT x 16 scores of a row block: mask, weights, and the factor for
-// the output so far.  vis: bit j of the tile set where token j0 + j is on a page.
-template <int JT, bool kMask>
-__device__ __forceinline__ float softmax_tile(const PagedArgs& a, f32x4 (&S)[JT], RowState& st, int j0, int pos,
-                                              uint64_t on_page, int g) {
+// Weights of one tile of scores, and the factor for the output so far.  The
+// reference point follows the maximum only when it lags by more than 2^8: sums and
+// products stay far from overflow, and most tiles need no rescaling.
+template <int JT>
+__device__ __forceinline__ float softmax_tile(const PagedArgs& a, f32x4 (&S)[JT], RowState& st) {
   float mx = -__builtin_inff();
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if constexpr (kMask) {
-        const int jl = 16 * jt + 4 * g + r;
-        if (!(((on_page >> jl) & 1) && visible(a, j0 + jl, pos))) S[jt][r] = -__builtin_inff();
-      }
-      mx = fmaxf(mx, S[jt][r]);
-    }
+    for (int r = 0; r < 4; ++r) mx = fmaxf(mx, S[jt][r]);
   mx = max_groups(mx) * a.scale_log2;
-  const float mn = fmaxf(st.m, mx);
+  const float mn = mx > st.m + 8.0f ? mx : st.m;
   const float base = mn == -__builtin_inff() ? 0.0f : mn;   // nothing visible yet: exp2(-inf - 0) = 0
-  const float alpha = __builtin_amdgcn_exp2f(st.m - base);
+  const float alpha = mn == st.m ? 1.0f : __builtin_amdgcn_exp2f(st.m - base);
   st.m = mn;
   float sum = 0.0f;
 #pragma unroll
@@ -162,26 +171,6 @@ __device__ __forceinline__ float softmax_tile(const PagedArgs& a, f32x4 (&S)[JT]
     }
   st.l = st.l * alpha + sum;
   return alpha;
-}
-
-// O += V^T P token by token with a select, for a tile in which a value that
-// some rows may not see is infinite or NaN (0 times it is not 0).
-template <int IT, int JT, int DT>
-__device__ __forceinline__ void add_visible(const PagedArgs& a, const f32x4 (&P)[JT], f32x4 (&O)[DT],
-                                            const typename Mma<IT>::elem* V, int pitch, int j0, int pos,
-                                            uint64_t on_page, int g, int li) {
-#pragma unroll
-  for (int jt = 0; jt < JT; ++jt)
-#pragma unroll 1
-    for (int e = 0; e < 16; ++e) {
-      const int r = e & 3, jl = 16 * jt + e;
-      const float own = r == 0 ? P[jt][0] : r == 1 ? P[jt][1] : r == 2 ? P[jt][2] : P[jt][3];
-      const float p = __shfl(own, (e >> 2) * 16 + li);
-      if (((on_page >> jl) & 1) && visible(a, j0 + jl, pos)) {
-#pragma unroll
-        for (int d = 0; d < DT; ++d) O[d] += widen4<IT>(V + jl * pitch + 16 * d + 4 * g) * p;
-      }
-    }
 }
 
 // Store one row's results: the output, or this split's partial ones.
@@ -268,47 +257,42 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
   }
 
   const int64_t hoff = static_cast<int64_t>(kvh) * a.head_stride;
-  u32x4 kr[kPasses], vr[kPasses];
   const int vec = tid % kPerRow, srow = tid / kPerRow;
-  auto fetch = [&](int64_t row_off) {   // row_off: the lane's token's cache row (-1: none)
+  // One staging register set serves K, then V: K of the next tile is in flight
+  // during the scores and the softmax, V during the second product.  row_off: cache row of
+  // the lane's token.  Tokens that no row may see are read from row 0: their weights are zero.
+  u32x4 stage[kPasses];
+  auto fetch = [&](const char* cache, int64_t row_off) {
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int64_t off = shfl64(row_off, srow + i * kRowsPass);
-      kr[i] = vr[i] = u32x4{0, 0, 0, 0};
-      if (off >= 0) {
-        const int64_t at = (off + hoff + vec * kVec) * static_cast<int64_t>(sizeof(elem));
-        kr[i] = ld<false, u32x4>(a.k + at);
-        vr[i] = ld<false, u32x4>(a.v + at);
-      }
-    }
+    for (int i = 0; i < kPasses; ++i)
+      stage[i] = ld<false, u32x4>(cache + (shfl64(row_off, srow + i * kRowsPass) + hoff + vec * kVec) * static_cast<int64_t>(sizeof(elem)));
   };
-  auto put = [&](int buf) {
+  auto put = [&](elem* tile) {
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int at = (srow + i * kRowsPass) * kPitch + vec * kVec;
-      *reinterpret_cast<u32x4*>(&lds[buf][0][at]) = kr[i];
-      *reinterpret_cast<u32x4*>(&lds[buf][1][at]) = vr[i];
-    }
+    for (int i = 0; i < kPasses; ++i)
+      *reinterpret_cast<u32x4*>(tile + (srow + i * kRowsPass) * kPitch + vec * kVec) = stage[i];
   };
-  int64_t off = -1, off_next = -1;
+  int64_t off = 0;
+  bool ok = false, ok_next = false;
   if (v0 < v1) {
-    off = cache_row(a, s, key_tile(kt, v0) * T + lane, kt.limit);
-    fetch(off);
-    if (v0 + 1 < v1) off_next = cache_row(a, s, key_tile(kt, v0 + 1) * T + lane, kt.limit);
-    put(0);
+    off = cache_row(a, s, key_tile(kt, v0) * T + lane, kt.limit, ok);
+    fetch(a.k, off);
+    put(lds[0][0]);
+    fetch(a.v, off);
+    if (v0 + 1 < v1) off = cache_row(a, s, key_tile(kt, v0 + 1) * T + lane, kt.limit, ok_next);
+    put(lds[0][1]);
   }
   __syncthreads();
   for (int v = v0; v < v1; ++v) {
     const int buf = (v - v0) & 1, j0 = key_tile(kt, v) * T;
-    const uint64_t on_page = __ballot(off >= 0);
-    if (v + 1 < v1) {
-      off = off_next;
-      fetch(off);
-      if (v + 2 < v1) off_next = cache_row(a, s, key_tile(kt, v + 2) * T + lane, kt.limit);
-    }
+    const uint64_t on_page = __ballot(ok);
+    const bool more = v + 1 < v1;
+    if (more) fetch(a.k, off);
+    const elem* Kt = lds[buf][0];
+    const elem* Vt = lds[buf][1];
+    frag P[RB][JT / 2];
+    bool bad = false;
     if (j0 <= wmax) {
-      const elem* Kt = lds[buf][0];
-      const elem* Vt = lds[buf][1];
       const bool full = on_page == ~0ull && j0 + T - 1 <= wmin &&
                         (a.window == 0 || j0 > wmax - a.window || j0 + T <= a.sinks);
       f32x4 S[RB][JT];
@@ -323,17 +307,16 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
           for (int b = 0; b < RB; ++b) S[b][jt] = mma<IT>(kf, Q[b][k], S[b][jt]);
         }
       }
-      bool bad = false;
       if (!full) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b) mask_tile<JT>(a, S[b], j0, pos[b], on_page, g);
         for (int i = lane; i < T * kPerRow; i += 64)
           bad |= nonfinite16<IT>(*reinterpret_cast<const u32x4*>(Vt + (i / kPerRow) * kPitch + (i % kPerRow) * kVec));
         bad = __ballot(bad) != 0;
       }
-      frag P[RB][JT / 2];
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
-        const float alpha = full ? softmax_tile<JT, false>(a, S[b], rs[b], j0, pos[b], on_page, g)
-                                 : softmax_tile<JT, true>(a, S[b], rs[b], j0, pos[b], on_page, g);
+        const float alpha = softmax_tile<JT>(a, S[b], rs[b]);
         if (__ballot(alpha != 1.0f) != 0) {
 #pragma unroll
           for (int d = 0; d < DT; ++d) O[b][d] *= alpha;
@@ -341,10 +324,23 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
 #pragma unroll
         for (int h = 0; h < JT / 2; ++h) P[b][h] = to_frag<IT>(stack(S[b][2 * h], S[b][2 * h + 1]));
       }
+    }
+    if (more) {
+      put(lds[buf ^ 1][0]);
+      fetch(a.v, off);
+      ok = ok_next;
+      if (v + 2 < v1) off = cache_row(a, s, key_tile(kt, v + 2) * T + lane, kt.limit, ok_next);
+    }
+    if (j0 <= wmax) {
       if (__builtin_expect(bad, 0)) {
 #pragma unroll
-        for (int b = 0; b < RB; ++b)
-          add_visible<IT, JT, DT>(a, S[b], O[b], Vt, kPitch, j0, pos[b], on_page, g, li);
+        for (int h = 0; h < JT / 2; ++h)
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            const frag vf = frag_col<IT>(Vt, kPitch, 32 * h, 16 * d, lane);
+#pragma unroll
+            for (int b = 0; b < RB; ++b) O[b][d] = mma_seen<IT>(vf, P[b][h], O[b][d]);
+          }
       } else {
 #pragma unroll
         for (int d = 0; d < DT; ++d)
@@ -356,7 +352,7 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
           }
       }
     }
-    if (v + 1 < v1) put(buf ^ 1);
+    if (more) put(lds[buf ^ 1][1]);
     __syncthreads();
   }
 #pragma unroll
@@ -410,39 +406,32 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
   auto fetch = [&](int64_t row_off) {   // lane l holds the cache row of token l % 32
 #pragma unroll
     for (int jt = 0; jt < JT; ++jt) {
-      const int64_t off = shfl64(row_off, 16 * jt + li);
+      const char* p = a.k + (shfl64(row_off, 16 * jt + li) + hoff + 8 * g) * static_cast<int64_t>(sizeof(elem));
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const int64_t at = (off + hoff + 32 * k + 8 * g) * static_cast<int64_t>(sizeof(elem));
         if constexpr (IT == kF32) {
-          kr[jt][2 * k] = kr[jt][2 * k + 1] = u32x4{0, 0, 0, 0};
-          if (off >= 0) {
-            kr[jt][2 * k] = ld<true, u32x4>(a.k + at);
-            kr[jt][2 * k + 1] = ld<true, u32x4>(a.k + at + 16);
-          }
+          kr[jt][2 * k] = ld<true, u32x4>(p + 128 * k);
+          kr[jt][2 * k + 1] = ld<true, u32x4>(p + 128 * k + 16);
         } else {
-          kr[jt][k] = u32x4{0, 0, 0, 0};
-          if (off >= 0) kr[jt][k] = ld<true, u32x4>(a.k + at);
+          kr[jt][k] = ld<true, u32x4>(p + 64 * k);
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int64_t off = shfl64(row_off, srow + i * kRowsPass);
-      vr[i] = u32x4{0, 0, 0, 0};
-      if (off >= 0) vr[i] = ld<true, u32x4>(a.v + (off + hoff + vec * kVec) * static_cast<int64_t>(sizeof(elem)));
-    }
+    for (int i = 0; i < kPasses; ++i)
+      vr[i] = ld<true, u32x4>(a.v + (shfl64(row_off, srow + i * kRowsPass) + hoff + vec * kVec) * static_cast<int64_t>(sizeof(elem)));
   };
   const int first = v0 + wave;
-  int64_t off = -1, off_next = -1;
+  int64_t off = 0;
+  bool ok = false, ok_next = false;
   if (first < v1) {
-    off = cache_row(a, s, key_tile(kt, first) * T + (lane & 31), kt.limit);
+    off = cache_row(a, s, key_tile(kt, first) * T + (lane & 31), kt.limit, ok);
     fetch(off);
-    if (first + W < v1) off_next = cache_row(a, s, key_tile(kt, first + W) * T + (lane & 31), kt.limit);
+    if (first + W < v1) off = cache_row(a, s, key_tile(kt, first + W) * T + (lane & 31), kt.limit, ok_next);
   }
   for (int v = first; v < v1; v += W) {
     const int j0 = key_tile(kt, v) * T;
-    const uint64_t on_page = __ballot(off >= 0) & 0xffffffffull;
+    const uint64_t on_page = __ballot(ok) & 0xffffffffull;
     bool bad = false;
     frag K[JT][KS];
 #pragma unroll
@@ -456,12 +445,6 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
           K[jt][k] = __builtin_bit_cast(frag, kr[jt][k]);
         }
       }
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      bad |= nonfinite16<IT>(vr[i]);
-      *reinterpret_cast<u32x4*>(Vt + (srow + i * kRowsPass) * kPitch + vec * kVec) = vr[i];
-    }
-    bad = __ballot(bad) != 0;
     f32x4 S[JT];
 #pragma unroll
     for (int jt = 0; jt < JT; ++jt) {
@@ -469,21 +452,29 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
 #pragma unroll
       for (int k = 0; k < KS; ++k) S[jt] = mma<IT>(K[jt][k], Q[k], S[jt]);
     }
-    if (v + W < v1) {
-      off = off_next;
-      fetch(off);
-      if (v + 2 * W < v1) off_next = cache_row(a, s, key_tile(kt, v + 2 * W) * T + (lane & 31), kt.limit);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      bad |= nonfinite16<IT>(vr[i]);
+      *reinterpret_cast<u32x4*>(Vt + (srow + i * kRowsPass) * kPitch + vec * kVec) = vr[i];
     }
-    const float alpha = softmax_tile<JT, true>(a, S, rs, j0, pos, on_page, g);
+    bad = __ballot(bad) != 0;
+    if (v + W < v1) {
+      fetch(off);
+      ok = ok_next;
+      if (v + 2 * W < v1) off = cache_row(a, s, key_tile(kt, v + 2 * W) * T + (lane & 31), kt.limit, ok_next);
+    }
+    mask_tile<JT>(a, S, j0, pos, on_page, g);
+    const float alpha = softmax_tile<JT>(a, S, rs);
     if (__ballot(alpha != 1.0f) != 0) {
 #pragma unroll
       for (int d = 0; d < DT; ++d) O[d] *= alpha;
     }
     __builtin_amdgcn_wave_barrier();
+    const frag P = to_frag<IT>(stack(S[0], S[1]));
     if (__builtin_expect(bad, 0)) {
-      add_visible<IT, JT, DT>(a, S, O, Vt, kPitch, j0, pos, on_page, g, li);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) O[d] = mma_seen<IT>(frag_col<IT>(Vt, kPitch, 0, 16 * d, lane), P, O[d]);
     } else {
-      const frag P = to_frag<IT>(stack(S[0], S[1]));
 #pragma unroll
       for (int d = 0; d < DT; ++d) O[d] = mma<IT>(frag_col<IT>(Vt, kPitch, 0, 16 * d, lane), P, O[d]);
     }
@@ -598,8 +589,9 @@ __global__ __launch_bounds__(kPagedBlock) void paged_append_kernel(PagedArgs a, 
   if (token < start) return;
   const int64_t j = static_cast<int64_t>(gload(a.kv_len + lo)) - (end < a.num_tokens ? end : a.num_tokens) + token;
   if (j < 0 || j > INT32_MAX - 1) return;
-  const int64_t row = cache_row(a, lo, static_cast<int>(j), INT32_MAX);
-  if (row < 0) return;
+  bool ok;
+  const int64_t row = cache_row(a, lo, static_cast<int>(j), INT32_MAX, ok);
+  if (!ok) return;
   const int64_t src = (token * a.new_stride) * ES + v * 16;
   const int64_t dst = (row + h * a.head_stride) * ES + (v - h * head_vecs) * 16;
   st<false>(a.k + dst, ld<false, u32x4>(a.k_new + src));

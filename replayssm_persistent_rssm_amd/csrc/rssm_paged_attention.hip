@@ -166,7 +166,7 @@ void fill_args(PagedArgs* a, const rssm_paged_attention_desc* d, const rssm_page
   a->max_pages = d->max_pages;
   a->max_seq_len = d->max_seq_len;
   a->max_kv_len = d->max_kv_len;
-  a->window = d->window;
+  a->window = std::min(d->window, 1 << 30);   // no cache is longer
   a->sinks = d->sinks;
   a->scale_log2 = d->scale * 1.4426950408889634f;
   a->row_tiles = 1;
