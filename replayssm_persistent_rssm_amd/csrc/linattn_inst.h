@@ -11,8 +11,7 @@ enum : int { kLinChunk = 0, kLinFold = 1, kLinStep = 2 };
 template <int IT, int ST, int N>
 const void* linattn_fn(int which) {
   if (which == kLinChunk) return reinterpret_cast<const void*>(&linattn_chunk_kernel<IT, ST, N, false>);
-  // the fold never touches the state pool: one instance serves every state dtype
-  if (which == kLinFold) return reinterpret_cast<const void*>(&linattn_chunk_kernel<IT, kF32, N, true>);
+  if (which == kLinFold) return reinterpret_cast<const void*>(&linattn_chunk_kernel<IT, ST, N, true>);
   return reinterpret_cast<const void*>(&linattn_step_kernel<IT, ST, N>);
 }
 

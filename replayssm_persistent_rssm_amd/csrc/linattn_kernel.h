@@ -13,9 +13,8 @@
 //   y^T[p][i] = S0[p] . C_i                A = S0 rows (LDS, rounded), Bm = the same C rows
 //       times exp(l_i), a scalar of the lane's column i
 //   y^T += x^T M^T                         A = x columns (LDS), Bm = masked weighted scores
-//   S'^T[n][p] = B^T (w x)                 A = B columns (LDS), Bm = w_j x_j, split so that no
-//                                          product loses more than 2^-22 (bf16: three parts,
-//                                          fp16: two parts scaled by a power of two, fp32: none)
+//   S'^T[n][p] = B^T (w x)                 A = B columns (LDS), Bm = w_j x_j in parts of the
+//                                          input type (fp16: scaled by a power of two)
 // Wavefront w owns tokens 16w .. 16w+15 of y and state rows 16w .. 16w+15 of the
 // update.  The next chunk's inputs are loaded into registers while the current
 // one is computed.
@@ -104,9 +103,11 @@ struct LinLds {
   elem Bs[kLinQ * kN];
   elem Ss[kLinP * kN];
   elem Xs[kLinQ * kP];
-  float lh[kLinQ], ll[kLinQ], e[kLinQ], dt[kLinQ], w[kLinQ];   // l_i (high and low part), exp(l_i), dt_i, w_i
+  // four chunks at a time: l_i in log2 units (and, for fp32, the part that its rounding
+  // dropped), exp(l_i), dt_i, w_i; the whole chunk's decay and its logarithm
+  float l2[4][kLinQ], l2lo[IT == kF32 ? 4 : 1][kLinQ], e[4][kLinQ], dt[4][kLinQ], w[4][kLinQ];
+  float decay[4], total[4];
   float sinv[kLinP];   // fp16: inverse scale of each state row in Ss
-  float decay, total;
 };
 
 // Stage `rows` x COLS elements at `base` (row stride `stride` elements) into
@@ -144,13 +145,27 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
   constexpr int KS = N / 32;
   constexpr int es = sizeof(elem);
   constexpr int ss = sizeof(typename Mma<ST>::elem);
+  // parts of w_j x_j in the update: enough bits for an fp32 state (bf16 8 a part, fp16
+  // 11), 16 and more for a state that is stored in 16 bits
+  constexpr int kParts = IT == kF32 ? 1 : (IT == kBF16 && ST == kF32 ? 3 : 2);
   __shared__ LinLds<IT, N> L;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int ptiles = a.dim / kLinP;
-  const int item = xcd_order(blockIdx.x, gridDim.x);
-  const int pt0 = item % ptiles, h = (item / ptiles) % a.H;
-  const int rest = item / (ptiles * a.H);
+  // Each XCD takes a range of heads of every stretch, so that the heads of a
+  // B/C group meet in its L2 and ragged lengths spread evenly; when the heads
+  // do not divide among the XCDs, a contiguous range of items.
+  const int ptiles = a.dim / kLinP, units = a.H * ptiles;
+  int unit, rest;
+  if (units % 8 == 0) {
+    const int per = units / 8, i = blockIdx.x / 8;
+    unit = blockIdx.x % 8 * per + i % per;
+    rest = i / per;
+  } else {
+    const int item = xcd_order(blockIdx.x, gridDim.x);
+    unit = item % units;
+    rest = item / units;
+  }
+  const int pt0 = unit % ptiles, h = unit / ptiles;
   const int seg = rest % a.nseg, s = rest / a.nseg;
   const LinSeq q = lin_seq(a, s);
   if (!q.live) return;
@@ -158,7 +173,7 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
   const int t1 = q.len - t0 < a.seg_len ? q.len : t0 + a.seg_len;
   if (kStateOnly ? (q.len - t0 <= a.seg_len) : (seg > 0 && t0 >= q.len)) return;
   // wavefronts with later tokens have more causal products: alternate which SIMD gets them
-  const int wrow = (item & 1) ? 3 - wave : wave;
+  const int wrow = (unit & 1) ? 3 - wave : wave;
 
   const float A = sload(a.A + h);
   const float Dh = a.D != nullptr ? sload(a.D + h) : 0.0f;
@@ -189,30 +204,21 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
   Stage<IT, kLinP> xr;
   Stage<IT, N> br;
   frag cr[KS];
-  float dtr = 0.0f;
   const int64_t hx = static_cast<int64_t>(h) * a.dim + pt0 * kLinP;
   auto fetch = [&](int t) {
     const int rows = t1 - t < kLinQ ? t1 - t : kLinQ;
     const int64_t row = q.start + t;
     xr.load(a.x + (row * a.x_stride + hx) * es, a.x_stride, rows, tid);
     br.load(a.B + (row * a.B_stride + static_cast<int64_t>(grp) * N) * es, a.B_stride, rows, tid);
-    if (wave == 0) {
-      dtr = 1.0f;
-      if (a.dt != nullptr) {
-        const rsrc_t r = make_rsrc(a.dt + row * a.dt_stride + h, ((rows - 1) * static_cast<uint32_t>(a.dt_stride) + 1) * 4);
-        dtr = new_token_dt(bload_f32(r, lane * static_cast<uint32_t>(a.dt_stride) * 4, 0), bias, a.dt_softplus);
-      }
-    }
   };
-  auto fetch_out = [&](int t) {   // C rows and z of the wavefront's tokens: column i = 16 wrow + li
+  auto fetch_C = [&](int t) {   // C rows of the wavefront's tokens: column i = 16 wrow + li
     const int rows = t1 - t < kLinQ ? t1 - t : kLinQ;
     const int64_t row = q.start + t;
     const uint32_t cb = static_cast<uint32_t>(a.C_stride * es);
     const rsrc_t rc = make_rsrc(a.C + (row * a.C_stride + static_cast<int64_t>(grp) * N) * es, (rows - 1) * cb + N * es);
-    const uint32_t i = 16 * wrow + li;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
-      const uint32_t at = i * cb + (32 * k + 8 * g) * es;
+      const uint32_t at = (16 * wrow + li) * cb + (32 * k + 8 * g) * es;
       if constexpr (IT == kF32) {
         const u32x4 u = bload16<false>(rc, at, 0), v = bload16<false>(rc, at + 16, 0);
         cr[k] = __builtin_bit_cast(frag, u32x8{u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w});
@@ -221,14 +227,53 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
       }
     }
   };
+  // raw dt of the wavefront's chunk of the four that start at t (lane = token)
+  auto fetch_dt = [&](int t) {
+    float v = 1.0f;
+    const int left = t1 - t - kLinQ * wave;
+    if (a.dt != nullptr && left > 0) {
+      const int rows = left < kLinQ ? left : kLinQ;
+      const uint32_t sb = static_cast<uint32_t>(a.dt_stride) * 4;
+      const rsrc_t r = make_rsrc(a.dt + (q.start + t + kLinQ * wave) * a.dt_stride + h, (rows - 1) * sb + 4);
+      v = bload_f32(r, lane * sb, 0);
+    }
+    return v;
+  };
+  // each wavefront turns one chunk's dt into its decays and weights
+  auto scan_dt = [&](int t, float raw) {
+    const bool in = t + kLinQ * wave + lane < t1;
+    float dtv = a.dt != nullptr ? new_token_dt(raw, bias, a.dt_softplus) : 1.0f;
+    dtv = in ? dtv : 0.0f;
+    // sums of dt A in fp64: differences of far positions keep their relative accuracy
+    double l = static_cast<double>(dtv) * static_cast<double>(A);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const double o = __shfl_up(l, d);
+      if (lane >= d) l += o;
+    }
+    const double end = __shfl(l, 63);
+    const double l2 = l * 1.4426950408889634074;
+    L.l2[wave][lane] = static_cast<float>(l2);
+    if constexpr (IT == kF32) L.l2lo[wave][lane] = static_cast<float>(l2 - static_cast<float>(l2));
+    L.e[wave][lane] = expf(static_cast<float>(l));
+    L.dt[wave][lane] = dtv;
+    L.w[wave][lane] = in ? expf(static_cast<float>(end - l)) * dtv : 0.0f;
+    if (lane == 0) {
+      L.decay[wave] = expf(static_cast<float>(end));
+      L.total[wave] = static_cast<float>(end);
+    }
+  };
 
   double seg_total = 0.0;
+  float dtr = 1.0f;
   if (t0 < t1) {
+    dtr = fetch_dt(t0);
     fetch(t0);
-    if constexpr (!kStateOnly) fetch_out(t0);
+    if constexpr (!kStateOnly) fetch_C(t0);
   }
   for (int t = t0; t < t1; t += kLinQ) {
     const int rows = t1 - t < kLinQ ? t1 - t : kLinQ;
+    const int c4 = ((t - t0) / kLinQ) & 3;
     if (t > t0) __syncthreads();   // every read of the previous chunk's tiles is done
     xr.store(L.Xs, LinLds<IT, N>::kP, tid);
     br.store(L.Bs, LinLds<IT, N>::kN, tid);
@@ -248,57 +293,57 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
       for (int n = 0; n < NT; ++n)
         narrow4<IT>(L.Ss + (16 * wave + li) * LinLds<IT, N>::kN + 16 * n + 4 * g, IT == kF16 ? S[n] * sc : S[n]);
     }
-    if (wave == 0) {
-      // sums of dt A in fp64: differences of far positions keep their relative accuracy
-      const float dtv = lane < rows ? dtr : 0.0f;
-      double l = static_cast<double>(dtv) * static_cast<double>(A);
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const double o = __shfl_up(l, d);
-        if (lane >= d) l += o;
-      }
-      const double end = __shfl(l, 63);
-      const float lh = static_cast<float>(l);
-      L.lh[lane] = lh;
-      L.ll[lane] = static_cast<float>(l - lh);
-      L.e[lane] = expf(lh);
-      L.dt[lane] = dtv;
-      L.w[lane] = lane < rows ? expf(static_cast<float>(end - l)) * dtv : 0.0f;
-      if (lane == 0) {
-        L.decay = expf(static_cast<float>(end));
-        L.total = static_cast<float>(end);
-      }
-    }
+    if (c4 == 0) scan_dt(t, dtr);
     __syncthreads();
-    frag cc[KS];
-    if constexpr (!kStateOnly) {
-#pragma unroll
-      for (int k = 0; k < KS; ++k) cc[k] = cr[k];
-    }
-    if (t + kLinQ < t1) {
-      fetch(t + kLinQ);
-      if constexpr (!kStateOnly) fetch_out(t + kLinQ);
-    }
+    if (t + kLinQ < t1) fetch(t + kLinQ);
+    if (c4 == 2) dtr = fetch_dt(t + 2 * kLinQ);
 
     if constexpr (!kStateOnly) {
       const int i = 16 * wrow + li;
+      u32x4 zr[4];
+      const bool has_z = a.z != nullptr;
+      if (has_z) {
+        const uint32_t zb = static_cast<uint32_t>(a.z_stride * es);
+        const rsrc_t rz = make_rsrc(a.z + ((q.start + t) * a.z_stride + hx) * es, (rows - 1) * zb + kLinP * es);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t at = i * zb + (16 * p + 4 * g) * es;
+          if constexpr (IT == kF32) {
+            zr[p] = bload16<false>(rz, at, 0);
+          } else {
+            const auto w = __builtin_amdgcn_raw_buffer_load_b64(rz, at, 0, 0);
+            zr[p] = u32x4{w[0], w[1], 0, 0};
+          }
+        }
+      }
       // masked, decay-weighted scores M^T[j][i], j = 16 jt + 4g + r
-      f32x4 M[4];
-      const float lhi = L.lh[i], lli = L.ll[i];
+      f32x4 M[4], Y[4];
+      const float lhi = L.l2[c4][i];
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
         M[jt] = f32x4{0, 0, 0, 0};
-        if (jt > wrow) continue;
 #pragma unroll
         for (int k = 0; k < KS; ++k)
-          M[jt] = mma<IT>(frag_row<IT>(L.Bs + (16 * jt + li) * LinLds<IT, N>::kN + 32 * k + 8 * g), cc[k], M[jt]);
-        const f32x4 lj = *reinterpret_cast<const f32x4*>(L.lh + 16 * jt + 4 * g);
-        const f32x4 kj = *reinterpret_cast<const f32x4*>(L.ll + 16 * jt + 4 * g);
-        const f32x4 dj = *reinterpret_cast<const f32x4*>(L.dt + 16 * jt + 4 * g);
+          M[jt] = mma<IT>(frag_row<IT>(L.Bs + (16 * jt + li) * LinLds<IT, N>::kN + 32 * k + 8 * g), cr[k], M[jt]);
+      }
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        Y[p] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          Y[p] = mma<IT>(frag_row<IT>(L.Ss + (16 * p + li) * LinLds<IT, N>::kN + 32 * k + 8 * g), cr[k], Y[p]);
+      }
+      if (t + kLinQ < t1) fetch_C(t + kLinQ);
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt) {
+        const f32x4 lj = *reinterpret_cast<const f32x4*>(L.l2[c4] + 16 * jt + 4 * g);
+        const f32x4 dj = *reinterpret_cast<const f32x4*>(L.dt[c4] + 16 * jt + 4 * g);
+        f32x4 d = lhi - lj;
+        if constexpr (IT == kF32)
+          d += L.l2lo[c4][i] - *reinterpret_cast<const f32x4*>(L.l2lo[c4] + 16 * jt + 4 * g);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float d = (lhi - lj[r]) + (lli - kj[r]);
-          const float v = M[jt][r] * ((IT == kF32 ? expf(d) : __expf(d)) * dj[r]);
+          const float v = M[jt][r] * (__builtin_amdgcn_exp2f(d[r]) * dj[r]);
           M[jt][r] = 16 * jt + 4 * g + r <= i ? v : 0.0f;
         }
       }
@@ -314,29 +359,19 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) M[jt] *= ms;
       }
-      const float ei = L.e[i], mi = pow2i(-mk);
-      f32x4 Y[4];
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        f32x4 acc = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-          acc = mma<IT>(frag_row<IT>(L.Ss + (16 * p + li) * LinLds<IT, N>::kN + 32 * k + 8 * g), cc[k], acc);
-        if constexpr (IT == kF16) acc *= *reinterpret_cast<const f32x4*>(L.sinv + 16 * p + 4 * g);
-        Y[p] = acc * ei;
-      }
+      const float ei = L.e[c4][i], mi = pow2i(-mk);
       f32x4 X[4];
       bool bad = false;
       const frag m0 = to_frag<IT>(stack(M[0], M[1])), m1 = to_frag<IT>(stack(M[2], M[3]));
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        f32x4 acc = f32x4{0, 0, 0, 0};
-        acc = mma<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 0, 16 * p, lane), m0, acc);
-        if (wrow >= 2) acc = mma<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 32, 16 * p, lane), m1, acc);
-        X[p] = acc;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) bad |= !(fabsf(acc[r]) < __builtin_inff());
+        X[p] = mma<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 0, 16 * p, lane), m0, f32x4{0, 0, 0, 0});
+        X[p] = mma<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 32, 16 * p, lane), m1, X[p]);
       }
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) bad |= !(fabsf(X[p][r]) < __builtin_inff());
       if (__builtin_expect(__ballot(bad) != 0, 0)) {
         // a non-finite x may have met the zero weight of a later token
 #pragma unroll
@@ -346,31 +381,31 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
         }
       }
       if (i < rows) {
-        const int64_t row = q.start + t + i;
+        elem* yp = reinterpret_cast<elem*>(a.y) + (q.start + t + i) * a.y_stride + hx + 4 * g;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const f32x4 xi = widen4<IT>(L.Xs + i * LinLds<IT, N>::kP + 16 * p + 4 * g);
-          f32x4 v = Y[p] + X[p] * mi + xi * Dh;
-          if (a.z != nullptr) {
-            const f32x4 zi = widen4<IT>(reinterpret_cast<const elem*>(a.z) + row * a.z_stride + hx + 16 * p + 4 * g);
+          if constexpr (IT == kF16) Y[p] *= *reinterpret_cast<const f32x4*>(L.sinv + 16 * p + 4 * g);
+          f32x4 v = Y[p] * ei + X[p] * mi + widen4<IT>(L.Xs + i * LinLds<IT, N>::kP + 16 * p + 4 * g) * Dh;
+          if (has_z) {
+            const f32x4 zi = widen4_raw<IT>(zr[p]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] *= silu(zi[r]);
           }
-          narrow4<IT>(reinterpret_cast<elem*>(a.y) + row * a.y_stride + hx + 16 * p + 4 * g, v);
+          narrow4<IT>(yp + 16 * p, v);
         }
       }
     }
 
     // state: S^T[n][p] of the wavefront's 16 rows p = 16 wave + li
-    const float decay = L.decay;
-    if (wave == 0) seg_total += L.total;
+    const float decay = L.decay[c4];
+    if constexpr (kStateOnly) seg_total += L.total[c4];
     frag u0[2], u1[2], u2[2];
     f32x8 wx[2];
     int sk = 0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const f32x4 w0 = *reinterpret_cast<const f32x4*>(L.w + 32 * k + 4 * g);
-      const f32x4 w1 = *reinterpret_cast<const f32x4*>(L.w + 32 * k + 16 + 4 * g);
+      const f32x4 w0 = *reinterpret_cast<const f32x4*>(L.w[c4] + 32 * k + 4 * g);
+      const f32x4 w1 = *reinterpret_cast<const f32x4*>(L.w[c4] + 32 * k + 16 + 4 * g);
       wx[k] = from_frag<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 32 * k, 16 * wave, lane)) * stack(w0, w1);
     }
     if constexpr (IT == kF16) {
@@ -386,24 +421,28 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
     for (int k = 0; k < 2; ++k) {
       const f32x8 v = IT == kF16 ? wx[k] * up : wx[k];
       u0[k] = to_frag<IT>(v);
-      if constexpr (IT != kF32) {
+      if constexpr (kParts > 1) {
         const f32x8 v1 = v - from_frag<IT>(u0[k]);
         u1[k] = to_frag<IT>(v1);
-        if constexpr (IT == kBF16) u2[k] = to_frag<IT>(v1 - from_frag<IT>(u1[k]));
+        if constexpr (kParts > 2) u2[k] = to_frag<IT>(v1 - from_frag<IT>(u1[k]));
       }
     }
     const float dup = IT == kF16 ? decay * up : decay;
 #pragma unroll
+    for (int n = 0; n < NT; ++n) S[n] *= dup;
+#pragma unroll
     for (int n = 0; n < NT; ++n) {
-      f32x4 acc = S[n] * dup;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const frag b = frag_col<IT>(L.Bs, LinLds<IT, N>::kN, 32 * k, 16 * n, lane);
-        if constexpr (IT == kBF16) acc = mma<IT>(b, u2[k], acc);
-        if constexpr (IT != kF32) acc = mma<IT>(b, u1[k], acc);
-        acc = mma<IT>(b, u0[k], acc);
+        if constexpr (kParts > 2) S[n] = mma<IT>(b, u2[k], S[n]);
+        if constexpr (kParts > 1) S[n] = mma<IT>(b, u1[k], S[n]);
+        S[n] = mma<IT>(b, u0[k], S[n]);
       }
-      S[n] = IT == kF16 ? acc * down : acc;
+    }
+    if constexpr (IT == kF16) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) S[n] *= down;
     }
   }
 

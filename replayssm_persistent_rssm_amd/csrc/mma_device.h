@@ -164,6 +164,18 @@ __device__ __forceinline__ f32x4 widen4(const typename Mma<IT>::elem* p) {
   }
 }
 
+// The same from raw storage in registers (16-bit types: the first two words).
+template <int IT>
+__device__ __forceinline__ f32x4 widen4_raw(u32x4 w) {
+  if constexpr (IT == kF32) return __builtin_bit_cast(f32x4, w);
+  else if constexpr (IT == kBF16)
+    return f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                 __uint_as_float(w.y & 0xffff0000u)};
+  else
+    return f32x4{f16_bits_to_float(w.x & 0xffffu), f16_bits_to_float(w.x >> 16), f16_bits_to_float(w.y & 0xffffu),
+                 f16_bits_to_float(w.y >> 16)};
+}
+
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
@@ -188,9 +200,12 @@ __device__ __forceinline__ float sum_groups(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-// v * 1 / (1 + exp(-v)); exp overflows to infinity for very negative v, where
-// the quotient is the right -0.
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
+// v / (1 + exp(-v)) by the hardware's exp2 and reciprocal (each within one unit
+// of the last place; the argument's rounding adds 2^-24 |v|, which only matters where
+// the result is tiny).  exp overflows to infinity for very negative v: the result is -0.
+__device__ __forceinline__ float silu(float v) {
+  return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
+}
 
 // Workgroup order that gives each of the 8 XCDs (workgroups are dealt to them in
 // turn) one contiguous range of items, so that neighbouring items, which

@@ -470,13 +470,22 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
       for (int d = 0; d < DT; ++d) O[d] *= alpha;
     }
     __builtin_amdgcn_wave_barrier();
-    const frag P = to_frag<IT>(stack(S[0], S[1]));
+    // the matrix cores idle beside the cache's stream: the weights go through in two
+    // parts, so that only the output is rounded
+    const f32x8 w = stack(S[0], S[1]);
+    const frag P = to_frag<IT>(w);
     if (__builtin_expect(bad, 0)) {
 #pragma unroll
       for (int d = 0; d < DT; ++d) O[d] = mma_seen<IT>(frag_col<IT>(Vt, kPitch, 0, 16 * d, lane), P, O[d]);
     } else {
+      frag P1;
+      if constexpr (IT != kF32) P1 = to_frag<IT>(w - from_frag<IT>(P));
 #pragma unroll
-      for (int d = 0; d < DT; ++d) O[d] = mma<IT>(frag_col<IT>(Vt, kPitch, 0, 16 * d, lane), P, O[d]);
+      for (int d = 0; d < DT; ++d) {
+        const frag vf = frag_col<IT>(Vt, kPitch, 0, 16 * d, lane);
+        if constexpr (IT != kF32) O[d] = mma<IT>(vf, P1, O[d]);
+        O[d] = mma<IT>(vf, P, O[d]);
+      }
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -510,15 +519,17 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
   }
 }
 
-// Joins the splits of one (token, head): one wavefront, lanes over head_dim.
+// Joins the splits of one (token, head): the wavefronts share the splits, eight
+// partial outputs of each in flight, lanes over head_dim.
 template <int IT, int D>
 __global__ __launch_bounds__(kPagedBlock) void paged_join_kernel(PagedArgs a) {
   typedef typename Mma<IT>::elem elem;
-  constexpr int E = D / 64;
+  constexpr int E = D / 64, W = kPagedBlock / 64, U = 8;
+  __shared__ float jo[W][D], jl[W];
   const int lane = threadIdx.x & 63;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kPagedBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row = blockIdx.x;
   const int64_t token = row / a.Hq;
-  if (token >= a.num_tokens) return;
   // rows that belong to no sequence were not computed: leave them alone
   int lo = 0, hi = a.num_seqs;
   while (lo < hi) {   // first sequence whose end lies past the token
@@ -540,34 +551,35 @@ __global__ __launch_bounds__(kPagedBlock) void paged_join_kernel(PagedArgs a) {
   float l = 0.0f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
-  for (int k0 = 0; k0 < a.nsplit; k0 += 64) {
-    float f = 0.0f, lk = 0.0f;
-    if (k0 + lane < a.nsplit) {
-      f = __builtin_amdgcn_exp2f(ml[2 * (k0 + lane)] - base);
-      lk = ml[2 * (k0 + lane) + 1] * f;
-    }
-    l += lk;
-    const int n = a.nsplit - k0 < 64 ? a.nsplit - k0 : 64;
-    for (int k = 0; k < n; ++k) {
-      const float w = __shfl(f, k);
-      if (w != 0.0f) {   // an empty split wrote no output
+  for (int k0 = wave * U; k0 < a.nsplit; k0 += W * U) {
+    float p[U][E], w[U];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(po[static_cast<int64_t>(k0 + k) * D + e], w, o[e]);
-      }
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u < a.nsplit ? k0 + u : a.nsplit - 1;
+      w[u] = k0 + u < a.nsplit ? __builtin_amdgcn_exp2f(ml[2 * k] - base) : 0.0f;
+      l = w[u] != 0.0f ? fmaf(ml[2 * k + 1], w[u], l) : l;
+#pragma unroll
+      for (int e = 0; e < E; ++e) p[u][e] = po[static_cast<int64_t>(k) * D + e];
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = w[u] != 0.0f ? fmaf(p[u][e], w[u], o[e]) : o[e];
   }
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+  for (int e = 0; e < E; ++e) jo[wave][lane * E + e] = o[e];
+  if (lane == 0) jl[wave] = l;
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d >= D) return;
+  l = (jl[0] + jl[1]) + (jl[2] + jl[3]);
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-  elem* out = reinterpret_cast<elem*>(a.out) + token * a.out_stride + static_cast<int64_t>(head) * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float v = o[e] * inv;
-    if constexpr (IT == kF32) out[e] = v;
-    else if constexpr (IT == kBF16) out[e] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
-    else out[e] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
-  }
-  if (a.lse != nullptr && lane == 0) a.lse[token * a.Hq + head] = (m + log2f(l)) * kLn2;
+  const float v = ((jo[0][d] + jo[1][d]) + (jo[2][d] + jo[3][d])) * inv;
+  elem* out = reinterpret_cast<elem*>(a.out) + token * a.out_stride + static_cast<int64_t>(head) * D + d;
+  if constexpr (IT == kF32) *out = v;
+  else if constexpr (IT == kBF16) *out = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+  else *out = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+  if (a.lse != nullptr && d == 0) a.lse[token * a.Hq + head] = (m + log2f(l)) * kLn2;
 }
 
 // Append: one thread a 16-byte vector of one new token's keys and values.

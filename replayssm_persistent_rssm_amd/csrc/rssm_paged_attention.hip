@@ -256,8 +256,7 @@ rssm_status rssm_paged_attention(const rssm_paged_attention_desc* d, const rssm_
   const int64_t grid = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * p.row_tiles * p.nsplit;
   st = launch(kernel_for(p.rows16 ? kPagedRow : kPagedTile, d), grid, params, hip_stream, "paged_attention");
   if (st != RSSM_OK || p.nsplit == 1) return st;
-  return launch(kernel_for(kPagedJoin, d), (out_rows + kPagedBlock / 64 - 1) / (kPagedBlock / 64), params, hip_stream,
-                "paged_join");
+  return launch(kernel_for(kPagedJoin, d), out_rows, params, hip_stream, "paged_join");
 }
 
 }  // extern "C"
