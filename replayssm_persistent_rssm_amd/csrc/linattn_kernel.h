@@ -97,9 +97,8 @@ __device__ __forceinline__ int scale_exp(float m) {
 template <int IT, int N>
 struct LinLds {
   typedef typename Mma<IT>::elem elem;
-  static constexpr int kPad = 16 / sizeof(elem);   // one 16-byte step: rows land 4 banks apart
-  static constexpr int kN = N + kPad;
-  static constexpr int kP = kLinP + kPad;
+  static constexpr int kN = tile_pitch<IT>(N);
+  static constexpr int kP = tile_pitch<IT>(kLinP);
   elem Bs[kLinQ * kN];
   elem Ss[kLinP * kN];
   elem Xs[kLinQ * kP];

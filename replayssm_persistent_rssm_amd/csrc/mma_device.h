@@ -77,6 +77,15 @@ __device__ __forceinline__ typename Mma<IT>::frag frag_row(const typename Mma<IT
   }
 }
 
+// Row pitch, in elements, of an LDS tile of `cols` (64 or 128) columns.  16-bit: rows
+// start 8 banks apart (an odd multiple of 32 bytes), so that the 4 rows x 32 bytes of a
+// transposing read and the 8 rows x 16 bytes of a straight one fall on different banks.
+// fp32: 4 banks apart.
+template <int IT>
+constexpr int tile_pitch(int cols) {
+  return IT == kF32 ? cols + 4 : cols + 16;
+}
+
 // Split fragment by columns of a row-major LDS tile: lane l takes column
 // c0 + l % 16 of rows r0 + {4g .. 4g+3} and r0 + 16 + {4g .. 4g+3}.  16-bit: the
 // transposing read hands each lane of a 16-lane group one column of the 4x16 block
@@ -110,6 +119,7 @@ __device__ __forceinline__ typename Mma<IT>::frag frag_col(const typename Mma<IT
 // -infinities among the terms that each column sees (a NaN counts as both).
 template <int IT>
 __device__ __forceinline__ f32x4 mma_seen(typename Mma<IT>::frag v, typename Mma<IT>::frag p, f32x4 c) {
+  __builtin_amdgcn_sched_barrier(0);   // rare: one call's registers at a time
   const f32x8 x = from_frag<IT>(v), w = from_frag<IT>(p);
   f32x8 fin, pos, neg, plus, minus;
 #pragma unroll

@@ -9,7 +9,7 @@
 //                                exchanges between the four lane groups
 //   O^T[d][i] += V^T P           A = V columns (transposing LDS read), Bm = P
 // with the running maximum m and sum l of each row (one pass over K and V).
-//  * paged_tile_kernel: many rows.  4 wavefronts x 16 RB rows share the K and
+//  * paged_tile_kernel: many rows.  NW wavefronts x 16 RB rows share the K and
 //    V tiles of 64 tokens, double-buffered in LDS; the next tile is loaded
 //    into registers while the current one is computed.
 //  * paged_row_kernel: at most 16 rows (single-token decoding).  Bound by
@@ -145,32 +145,44 @@ struct RowState {
   float m, l;   // reference point of the exponents (log2 units) and the lane's part of the sum
 };
 
-// Weights of one tile of scores, and the factor for the output so far.  The
-// reference point follows the maximum only when it lags by more than 2^8: sums and
-// products stay far from overflow, and most tiles need no rescaling.
+// The reference point follows the maximum only when it lags by more than 2^8:
+// sums and products stay far from overflow, most tiles need no rescaling, and the exchange
+// between lanes is left to the tiles that do.
 template <int JT>
-__device__ __forceinline__ float softmax_tile(const PagedArgs& a, f32x4 (&S)[JT], RowState& st) {
+__device__ __forceinline__ bool lags(const PagedArgs& a, const f32x4 (&S)[JT], const RowState& st) {
   float mx = -__builtin_inff();
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt)
 #pragma unroll
     for (int r = 0; r < 4; ++r) mx = fmaxf(mx, S[jt][r]);
-  mx = max_groups(mx) * a.scale_log2;
-  const float mn = mx > st.m + 8.0f ? mx : st.m;
-  const float base = mn == -__builtin_inff() ? 0.0f : mn;   // nothing visible yet: exp2(-inf - 0) = 0
-  const float alpha = mn == st.m ? 1.0f : __builtin_amdgcn_exp2f(st.m - base);
-  st.m = mn;
-  float sum = 0.0f;
+  return mx * a.scale_log2 > st.m + 8.0f;
+}
+
+// New reference point; the factor for the sum and the output so far.
+template <int JT>
+__device__ __forceinline__ float move_reference(const PagedArgs& a, const f32x4 (&S)[JT], RowState& st) {
+  float mx = -__builtin_inff();
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float p = __builtin_amdgcn_exp2f(fmaf(S[jt][r], a.scale_log2, -base));
-      S[jt][r] = p;
-      sum += p;
-    }
-  st.l = st.l * alpha + sum;
+    for (int r = 0; r < 4; ++r) mx = fmaxf(mx, S[jt][r]);
+  const float mn = fmaxf(st.m, max_groups(mx) * a.scale_log2);
+  const float alpha = mn == st.m ? 1.0f : __builtin_amdgcn_exp2f(st.m - mn);
+  st.m = mn;
+  st.l *= alpha;
   return alpha;
+}
+
+// exp2(c S - m) of one D tile, added to the lane's sum.  Nothing visible so far: m is
+// -infinity, and 0 in its place gives the weights exp2(-infinity) = 0.
+__device__ __forceinline__ f32x4 weights(const PagedArgs& a, f32x4 S, RowState& st) {
+  const float base = st.m == -__builtin_inff() ? 0.0f : st.m;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    S[r] = __builtin_amdgcn_exp2f(fmaf(S[r], a.scale_log2, -base));
+    st.l += S[r];
+  }
+  return S;
 }
 
 // Store one row's results: the output, or this split's partial ones.
@@ -201,14 +213,14 @@ __device__ __forceinline__ int64_t shfl64(int64_t v, int from) {
   return (static_cast<int64_t>(hi) << 32) | static_cast<uint32_t>(lo);
 }
 
-template <int IT, int D, int RB>
-__global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_kernel(PagedArgs a) {
+template <int IT, int D, int RB, int NW>
+__global__ __launch_bounds__(64 * NW, IT == kF32 ? 1 : 2) void paged_tile_kernel(PagedArgs a) {
   typedef typename Mma<IT>::elem elem;
   typedef typename Mma<IT>::frag frag;
   constexpr int T = 64, JT = T / 16, KS = D / 32, DT = D / 16;
-  constexpr int kVec = 16 / sizeof(elem), kPerRow = D / kVec, kRowsPass = kPagedBlock / kPerRow, kPasses = T / kRowsPass;
-  constexpr int kPitch = D + kVec;
-  constexpr int kRows = 64 * RB;
+  constexpr int kVec = 16 / sizeof(elem), kPerRow = D / kVec, kRowsPass = 64 * NW / kPerRow, kPasses = T / kRowsPass;
+  constexpr int kPitch = tile_pitch<IT>(D);
+  constexpr int kRows = 16 * RB * NW;
   __shared__ __align__(16) elem lds[2][2][T * kPitch];   // [buffer][K, V]
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -258,44 +270,51 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
 
   const int64_t hoff = static_cast<int64_t>(kvh) * a.head_stride;
   const int vec = tid % kPerRow, srow = tid / kPerRow;
-  // One staging register set serves K, then V: K of the next tile is in flight
-  // during the scores and the softmax, V during the second product.  row_off: cache row of
-  // the lane's token.  Tokens that no row may see are read from row 0: their weights are zero.
-  u32x4 stage[kPasses];
-  auto fetch = [&](const char* cache, int64_t row_off) {
+  // row_off: cache row of the lane's token.  Tokens that no row may see are read
+  // from row 0: their weights are zero.
+  u32x4 kr[kPasses], vr[kPasses];
+  auto fetch = [&](int64_t row_off) {
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      stage[i] = ld<false, u32x4>(cache + (shfl64(row_off, srow + i * kRowsPass) + hoff + vec * kVec) * static_cast<int64_t>(sizeof(elem)));
+    for (int i = 0; i < kPasses; ++i) {
+      const int64_t at = (shfl64(row_off, srow + i * kRowsPass) + hoff + vec * kVec) * static_cast<int64_t>(sizeof(elem));
+      kr[i] = ld<false, u32x4>(a.k + at);
+      vr[i] = ld<false, u32x4>(a.v + at);
+    }
   };
-  auto put = [&](elem* tile) {
+  auto put = [&](int buf) {
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      *reinterpret_cast<u32x4*>(tile + (srow + i * kRowsPass) * kPitch + vec * kVec) = stage[i];
+    for (int i = 0; i < kPasses; ++i) {
+      const int at = (srow + i * kRowsPass) * kPitch + vec * kVec;
+      *reinterpret_cast<u32x4*>(&lds[buf][0][at]) = kr[i];
+      *reinterpret_cast<u32x4*>(&lds[buf][1][at]) = vr[i];
+    }
   };
   int64_t off = 0;
   bool ok = false, ok_next = false;
   if (v0 < v1) {
     off = cache_row(a, s, key_tile(kt, v0) * T + lane, kt.limit, ok);
-    fetch(a.k, off);
-    put(lds[0][0]);
-    fetch(a.v, off);
+    fetch(off);
     if (v0 + 1 < v1) off = cache_row(a, s, key_tile(kt, v0 + 1) * T + lane, kt.limit, ok_next);
-    put(lds[0][1]);
+    put(0);
   }
   __syncthreads();
   for (int v = v0; v < v1; ++v) {
     const int buf = (v - v0) & 1, j0 = key_tile(kt, v) * T;
     const uint64_t on_page = __ballot(ok);
     const bool more = v + 1 < v1;
-    if (more) fetch(a.k, off);
+    if (more) {
+      fetch(off);
+      ok = ok_next;
+      if (v + 2 < v1) off = cache_row(a, s, key_tile(kt, v + 2) * T + lane, kt.limit, ok_next);
+    }
     const elem* Kt = lds[buf][0];
     const elem* Vt = lds[buf][1];
-    frag P[RB][JT / 2];
+    const bool work = j0 <= wmax;
+    f32x4 S[RB][JT];
     bool bad = false;
-    if (j0 <= wmax) {
+    if (work) {
       const bool full = on_page == ~0ull && j0 + T - 1 <= wmin &&
                         (a.window == 0 || j0 > wmax - a.window || j0 + T <= a.sinks);
-      f32x4 S[RB][JT];
 #pragma unroll
       for (int jt = 0; jt < JT; ++jt) {
 #pragma unroll
@@ -314,45 +333,50 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
           bad |= nonfinite16<IT>(*reinterpret_cast<const u32x4*>(Vt + (i / kPerRow) * kPitch + (i % kPerRow) * kVec));
         bad = __ballot(bad) != 0;
       }
+      bool move = false;
 #pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        const float alpha = softmax_tile<JT>(a, S[b], rs[b]);
-        if (__ballot(alpha != 1.0f) != 0) {
+      for (int b = 0; b < RB; ++b) move |= lags<JT>(a, S[b], rs[b]);
+      if (__ballot(move) != 0) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          const float alpha = move_reference<JT>(a, S[b], rs[b]);
 #pragma unroll
           for (int d = 0; d < DT; ++d) O[b][d] *= alpha;
         }
-#pragma unroll
-        for (int h = 0; h < JT / 2; ++h) P[b][h] = to_frag<IT>(stack(S[b][2 * h], S[b][2 * h + 1]));
       }
     }
-    if (more) {
-      put(lds[buf ^ 1][0]);
-      fetch(a.v, off);
-      ok = ok_next;
-      if (v + 2 < v1) off = cache_row(a, s, key_tile(kt, v + 2) * T + lane, kt.limit, ok_next);
-    }
-    if (j0 <= wmax) {
+    if (work) {
       if (__builtin_expect(bad, 0)) {
 #pragma unroll
-        for (int h = 0; h < JT / 2; ++h)
+        for (int h = 0; h < JT / 2; ++h) {
+          frag P[RB];
+#pragma unroll
+          for (int b = 0; b < RB; ++b)
+            P[b] = to_frag<IT>(stack(weights(a, S[b][2 * h], rs[b]), weights(a, S[b][2 * h + 1], rs[b])));
 #pragma unroll
           for (int d = 0; d < DT; ++d) {
             const frag vf = frag_col<IT>(Vt, kPitch, 32 * h, 16 * d, lane);
 #pragma unroll
-            for (int b = 0; b < RB; ++b) O[b][d] = mma_seen<IT>(vf, P[b][h], O[b][d]);
+            for (int b = 0; b < RB; ++b) O[b][d] = mma_seen<IT>(vf, P[b], O[b][d]);
           }
+        }
       } else {
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+        for (int h = 0; h < JT / 2; ++h) {
+          frag P[RB];
 #pragma unroll
-          for (int h = 0; h < JT / 2; ++h) {
+          for (int b = 0; b < RB; ++b)
+            P[b] = to_frag<IT>(stack(weights(a, S[b][2 * h], rs[b]), weights(a, S[b][2 * h + 1], rs[b])));
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
             const frag vf = frag_col<IT>(Vt, kPitch, 32 * h, 16 * d, lane);
 #pragma unroll
-            for (int b = 0; b < RB; ++b) O[b][d] = mma<IT>(vf, P[b][h], O[b][d]);
+            for (int b = 0; b < RB; ++b) O[b][d] = mma<IT>(vf, P[b], O[b][d]);
           }
+        }
       }
     }
-    if (more) put(lds[buf ^ 1][1]);
+    if (more) put(buf ^ 1);
     __syncthreads();
   }
 #pragma unroll
@@ -368,7 +392,7 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
   typedef typename Mma<IT>::frag frag;
   constexpr int T = 32, JT = 2, KS = D / 32, DT = D / 16, W = kPagedBlock / 64;
   constexpr int kVec = 16 / sizeof(elem), kPerRow = D / kVec, kRowsPass = 64 / kPerRow, kPasses = T / kRowsPass;
-  constexpr int kPitch = D + kVec;
+  constexpr int kPitch = tile_pitch<IT>(D);
   constexpr int kTileBytes = W * T * kPitch * sizeof(elem), kJoinBytes = W * 16 * (D + 4) * 4;
   __shared__ __align__(16) char lds[kTileBytes > kJoinBytes ? kTileBytes : kJoinBytes];
   __shared__ float jm[W][16], jl[W][16];
@@ -464,11 +488,13 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
       if (v + 2 * W < v1) off = cache_row(a, s, key_tile(kt, v + 2 * W) * T + (lane & 31), kt.limit, ok_next);
     }
     mask_tile<JT>(a, S, j0, pos, on_page, g);
-    const float alpha = softmax_tile<JT>(a, S, rs);
-    if (__ballot(alpha != 1.0f) != 0) {
+    if (__ballot(lags<JT>(a, S, rs)) != 0) {
+      const float alpha = move_reference<JT>(a, S, rs);
 #pragma unroll
       for (int d = 0; d < DT; ++d) O[d] *= alpha;
     }
+    S[0] = weights(a, S[0], rs);
+    S[1] = weights(a, S[1], rs);
     __builtin_amdgcn_wave_barrier();
     // the matrix cores idle beside the cache's stream: the weights go through in two
     // parts, so that only the output is rounded
