@@ -113,19 +113,17 @@ __device__ __forceinline__ typename Mma<IT>::frag frag_col(const typename Mma<IT
   }
 }
 
-// c + v p for a fragment v that holds infinities or NaN: a lane's column takes
-// them only from terms whose weight p is not zero (0 times infinity is not 0).  The
-// finite part goes through one product; the others count the +infinities and
-// -infinities among the terms that each column sees (a NaN counts as both).
+// c plus the infinities and NaN of x that a lane's column sees, those whose weight
+// p is not zero (a product would make 0 times infinity a NaN).  Products of 0s and 1s count
+// the +infinities and -infinities among the terms (a NaN counts as both).
 template <int IT>
-__device__ __forceinline__ f32x4 mma_seen(typename Mma<IT>::frag v, typename Mma<IT>::frag p, f32x4 c) {
+__device__ __forceinline__ f32x4 add_odd(f32x8 x, typename Mma<IT>::frag p, f32x4 c) {
   __builtin_amdgcn_sched_barrier(0);   // rare: one call's registers at a time
-  const f32x8 x = from_frag<IT>(v), w = from_frag<IT>(p);
-  f32x8 fin, pos, neg, plus, minus;
+  const f32x8 w = from_frag<IT>(p);
+  f32x8 pos, neg, plus, minus;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const bool odd = !(fabsf(x[e]) < __builtin_inff());
-    fin[e] = odd ? 0.0f : x[e];
     pos[e] = odd && x[e] != -__builtin_inff() ? 1.0f : 0.0f;
     neg[e] = odd && x[e] != __builtin_inff() ? 1.0f : 0.0f;
     plus[e] = w[e] >= 0.0f ? (w[e] > 0.0f ? 1.0f : 0.0f) : (w[e] < 0.0f ? 0.0f : 1.0f);
@@ -134,7 +132,6 @@ __device__ __forceinline__ f32x4 mma_seen(typename Mma<IT>::frag v, typename Mma
   typedef typename Mma<IT>::frag frag;
   const f32x4 zero = f32x4{0, 0, 0, 0};
   const frag fp = to_frag<IT>(pos), fn = to_frag<IT>(neg), sp = to_frag<IT>(plus), sm = to_frag<IT>(minus);
-  c = mma<IT>(to_frag<IT>(fin), p, c);
   const f32x4 up = mma<IT>(fn, sm, mma<IT>(fp, sp, zero)), down = mma<IT>(fp, sm, mma<IT>(fn, sp, zero));
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -142,6 +139,16 @@ __device__ __forceinline__ f32x4 mma_seen(typename Mma<IT>::frag v, typename Mma
     if (down[r] != 0.0f) c[r] -= __builtin_inff();
   }
   return c;
+}
+
+// c + x p where x may hold infinities and NaN: the finite part by a product, the rest by add_odd.
+template <int IT>
+__device__ __forceinline__ f32x4 mma_seen(typename Mma<IT>::frag v, typename Mma<IT>::frag p, f32x4 c) {
+  const f32x8 x = from_frag<IT>(v);
+  f32x8 fin;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) fin[e] = fabsf(x[e]) < __builtin_inff() ? x[e] : 0.0f;
+  return add_odd<IT>(x, p, mma<IT>(to_frag<IT>(fin), p, c));
 }
 
 // Split fragment of two stacked D tiles.

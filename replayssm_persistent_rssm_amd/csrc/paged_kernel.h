@@ -108,17 +108,29 @@ __device__ __forceinline__ KeyTiles key_tiles(const PagedArgs& a, int pmin, int 
 
 __device__ __forceinline__ int key_tile(const KeyTiles& k, int v) { return v < k.sink ? v : k.lo + (v - k.sink); }
 
-// Whether any of 16 raw bytes' elements is infinite or NaN.
+// Bits set in each element of a raw word that is infinite or NaN (bit 15 and 31 for the
+// 16-bit types, bit 31 for fp32).
+template <int IT>
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) {
+  if constexpr (IT == kBF16) return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+  else if constexpr (IT == kF16) return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+  else return ((w & 0x7f800000u) + 0x00800000u) & 0x80000000u;
+}
+
 template <int IT>
 __device__ __forceinline__ bool nonfinite16(u32x4 v) {
-  uint32_t any = 0;
+  return (nonfinite_bits<IT>(v.x) | nonfinite_bits<IT>(v.y) | nonfinite_bits<IT>(v.z) | nonfinite_bits<IT>(v.w)) != 0;
+}
+
+// 16 raw bytes with every infinite or NaN element set to zero.
+template <int IT>
+__device__ __forceinline__ u32x4 finite16(u32x4 v) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if constexpr (IT == kBF16) any |= ((v[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-    else if constexpr (IT == kF16) any |= ((v[i] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
-    else any |= ((v[i] & 0x7f800000u) + 0x00800000u) & 0x80000000u;
+    const uint32_t b = nonfinite_bits<IT>(v[i]);
+    v[i] &= IT == kF32 ? (b != 0 ? 0u : ~0u) : ~((b >> 15) * 0xffffu);
   }
-  return any != 0;
+  return v;
 }
 
 // Scores of tokens a row may not see become -infinity.  bits: bit j where token
@@ -222,6 +234,7 @@ __global__ __launch_bounds__(64 * NW, IT == kF32 ? 1 : 2) void paged_tile_kernel
   constexpr int kPitch = tile_pitch<IT>(D);
   constexpr int kRows = 16 * RB * NW;
   __shared__ __align__(16) elem lds[2][2][T * kPitch];   // [buffer][K, V]
+  __shared__ int odd;   // an infinite or NaN element of V was met
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int item = xcd_order(blockIdx.x, gridDim.x);
@@ -281,7 +294,18 @@ __global__ __launch_bounds__(64 * NW, IT == kF32 ? 1 : 2) void paged_tile_kernel
       vr[i] = ld<false, u32x4>(a.v + at);
     }
   };
+  // V goes to LDS with zeros for infinite and NaN elements (0 times them is not
+  // 0); a second pass gives them to the rows that see them.
   auto put = [&](int buf) {
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) any |= nonfinite16<IT>(vr[i]);
+    any = __ballot(any) != 0;
+    if (__builtin_expect(any, 0)) {
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) vr[i] = finite16<IT>(vr[i]);
+      odd = 1;
+    }
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int at = (srow + i * kRowsPass) * kPitch + vec * kVec;
@@ -289,6 +313,8 @@ __global__ __launch_bounds__(64 * NW, IT == kF32 ? 1 : 2) void paged_tile_kernel
       *reinterpret_cast<u32x4*>(&lds[buf][1][at]) = vr[i];
     }
   };
+  if (tid == 0) odd = 0;
+  __syncthreads();
   int64_t off = 0;
   bool ok = false, ok_next = false;
   if (v0 < v1) {
@@ -297,87 +323,144 @@ __global__ __launch_bounds__(64 * NW, IT == kF32 ? 1 : 2) void paged_tile_kernel
     if (v0 + 1 < v1) off = cache_row(a, s, key_tile(kt, v0 + 1) * T + lane, kt.limit, ok_next);
     put(0);
   }
-  __syncthreads();
-  for (int v = v0; v < v1; ++v) {
-    const int buf = (v - v0) & 1, j0 = key_tile(kt, v) * T;
-    const uint64_t on_page = __ballot(ok);
-    const bool more = v + 1 < v1;
-    if (more) {
+  f32x4 S[RB][JT];
+  bool work = false;
+  uint64_t on_page = 0;
+  // first half of a tile: scores, masks, reference points
+  auto scores = [&](int v) {
+    const int j0 = key_tile(kt, v) * T;
+    work = j0 <= wmax;
+    if (!work) return;
+    const elem* Kt = lds[(v - v0) & 1][0];
+    const bool full = on_page == ~0ull && j0 + T - 1 <= wmin &&
+                      (a.window == 0 || j0 > wmax - a.window || j0 + T <= a.sinks);
+    // the next 16 keys' fragments are read while the matrix cores take the current ones
+    frag kf[2][KS];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) kf[0][k] = frag_row<IT>(Kt + li * kPitch + 32 * k + 8 * g);
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt) {
+      if (jt + 1 < JT) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) kf[(jt + 1) & 1][k] = frag_row<IT>(Kt + (16 * (jt + 1) + li) * kPitch + 32 * k + 8 * g);
+      }
+#pragma unroll
+      for (int b = 0; b < RB; ++b) S[b][jt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int b = 0; b < RB; ++b) S[b][jt] = mma<IT>(kf[jt & 1][k], Q[b][k], S[b][jt]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (!full) {
+      asm volatile("");   // a branch, not 200 selects in every tile
+#pragma unroll
+      for (int b = 0; b < RB; ++b) mask_tile<JT>(a, S[b], j0, pos[b], on_page, g);
+    }
+    bool move = false;
+#pragma unroll
+    for (int b = 0; b < RB; ++b) move |= lags<JT>(a, S[b], rs[b]);
+    if (__ballot(move) != 0) {
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        const float alpha = move_reference<JT>(a, S[b], rs[b]);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) O[b][d] *= alpha;
+      }
+    }
+  };
+  // second half: weights, output
+  auto outputs = [&](int v) {
+    if (!work) return;
+    const elem* Vt = lds[(v - v0) & 1][1];
+#pragma unroll
+    for (int h = 0; h < JT / 2; ++h) {
+      frag P[RB];
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+        P[b] = to_frag<IT>(stack(weights(a, S[b][2 * h], rs[b]), weights(a, S[b][2 * h + 1], rs[b])));
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const frag vf = frag_col<IT>(Vt, kPitch, 32 * h, 16 * d, lane);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) O[b][d] = mma<IT>(vf, P[b], O[b][d]);
+      }
+    }
+  };
+  // tile v + 1 into registers (and the pages of v + 2)
+  auto ahead = [&](int v) {
+    on_page = __ballot(ok);
+    if (v + 1 < v1) {
       fetch(off);
       ok = ok_next;
       if (v + 2 < v1) off = cache_row(a, s, key_tile(kt, v + 2) * T + lane, kt.limit, ok_next);
     }
-    const elem* Kt = lds[buf][0];
-    const elem* Vt = lds[buf][1];
-    const bool work = j0 <= wmax;
-    f32x4 S[RB][JT];
-    bool bad = false;
-    if (work) {
-      const bool full = on_page == ~0ull && j0 + T - 1 <= wmin &&
-                        (a.window == 0 || j0 > wmax - a.window || j0 + T <= a.sinks);
-#pragma unroll
-      for (int jt = 0; jt < JT; ++jt) {
-#pragma unroll
-        for (int b = 0; b < RB; ++b) S[b][jt] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const frag kf = frag_row<IT>(Kt + (16 * jt + li) * kPitch + 32 * k + 8 * g);
-#pragma unroll
-          for (int b = 0; b < RB; ++b) S[b][jt] = mma<IT>(kf, Q[b][k], S[b][jt]);
-        }
-      }
-      if (!full) {
-#pragma unroll
-        for (int b = 0; b < RB; ++b) mask_tile<JT>(a, S[b], j0, pos[b], on_page, g);
-        for (int i = lane; i < T * kPerRow; i += 64)
-          bad |= nonfinite16<IT>(*reinterpret_cast<const u32x4*>(Vt + (i / kPerRow) * kPitch + (i % kPerRow) * kVec));
-        bad = __ballot(bad) != 0;
-      }
-      bool move = false;
-#pragma unroll
-      for (int b = 0; b < RB; ++b) move |= lags<JT>(a, S[b], rs[b]);
-      if (__ballot(move) != 0) {
+  };
+  __syncthreads();
+  // With 8 wavefronts two share a SIMD: the later four run half a tile behind, so
+  // that one wavefront's exponentials meet the other's products.  Tile v + 1 is
+  // stored over tile v - 1 in the half step after the late wavefronts left it.
+  if (NW == 8 && wave >= 4) {
+    for (int v = v0; v < v1; ++v) {
+      ahead(v);
+      if (v > v0) outputs(v - 1);
+      __syncthreads();
+      scores(v);
+      if (v + 1 < v1) put((v + 1 - v0) & 1);
+      __syncthreads();
+    }
+    if (v0 < v1) outputs(v1 - 1);
+  } else {
+    for (int v = v0; v < v1; ++v) {
+      ahead(v);
+      scores(v);
+      if (NW == 8) __syncthreads();
+      outputs(v);
+      if (v + 1 < v1) put((v + 1 - v0) & 1);
+      __syncthreads();
+    }
+  }
+  if (__builtin_expect(odd, 0)) {
+    // rare: the tiles once more from the cache, for the infinities and NaN among the values of
+    // tokens that a row sees (its weight is not zero)
+#pragma unroll 1
+    for (int v = v0; v < v1; ++v) {
+      const int j0 = key_tile(kt, v) * T;
+      bool there, any = false;
+      const int64_t row = cache_row(a, s, j0 + lane, kt.limit, there);
+      const uint64_t bits = __ballot(there);
+      const elem* base = reinterpret_cast<const elem*>(a.v) + row + hoff;
+      for (int i = 0; i < kPerRow; ++i) any |= nonfinite16<IT>(*reinterpret_cast<const u32x4*>(base + i * kVec));
+      if (j0 > wmax || __ballot(any) == 0) continue;
+#pragma unroll 1
+      for (int h = 0; h < JT / 2; ++h) {
+        frag P[RB];
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-          const float alpha = move_reference<JT>(a, S[b], rs[b]);
+          f32x4 sc[JT];
 #pragma unroll
-          for (int d = 0; d < DT; ++d) O[b][d] *= alpha;
+          for (int u = 0; u < 2; ++u) {
+            const elem* kp = reinterpret_cast<const elem*>(a.k) + shfl64(row, 32 * h + 16 * u + li) + hoff + 8 * g;
+            sc[u] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < KS; ++k) sc[u] = mma<IT>(frag_row<IT>(kp + 32 * k), Q[b][k], sc[u]);
+            sc[u + 2] = sc[u];
+          }
+          mask_tile<JT>(a, sc, j0 + 32 * h, pos[b], bits >> (32 * h), g);
+          RowState t = rs[b];
+          P[b] = to_frag<IT>(stack(weights(a, sc[0], t), weights(a, sc[1], t)));
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          f32x8 x;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            x[e] = elem_to_float<IT>((reinterpret_cast<const elem*>(a.v) + hoff + li)[shfl64(row, 32 * h + 16 * (e >> 2) + 4 * g + (e & 3)) + 16 * d]);
+#pragma unroll
+          for (int b = 0; b < RB; ++b) O[b][d] = add_odd<IT>(x, P[b], O[b][d]);
         }
       }
     }
-    if (work) {
-      if (__builtin_expect(bad, 0)) {
-#pragma unroll
-        for (int h = 0; h < JT / 2; ++h) {
-          frag P[RB];
-#pragma unroll
-          for (int b = 0; b < RB; ++b)
-            P[b] = to_frag<IT>(stack(weights(a, S[b][2 * h], rs[b]), weights(a, S[b][2 * h + 1], rs[b])));
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            const frag vf = frag_col<IT>(Vt, kPitch, 32 * h, 16 * d, lane);
-#pragma unroll
-            for (int b = 0; b < RB; ++b) O[b][d] = mma_seen<IT>(vf, P[b], O[b][d]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < JT / 2; ++h) {
-          frag P[RB];
-#pragma unroll
-          for (int b = 0; b < RB; ++b)
-            P[b] = to_frag<IT>(stack(weights(a, S[b][2 * h], rs[b]), weights(a, S[b][2 * h + 1], rs[b])));
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            const frag vf = frag_col<IT>(Vt, kPitch, 32 * h, 16 * d, lane);
-#pragma unroll
-            for (int b = 0; b < RB; ++b) O[b][d] = mma<IT>(vf, P[b], O[b][d]);
-          }
-        }
-      }
-    }
-    if (more) put(buf ^ 1);
-    __syncthreads();
   }
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
