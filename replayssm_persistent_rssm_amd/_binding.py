@@ -533,6 +533,26 @@ class SsuDecodeCall:
 # long way.
 # --------------------------------------------------------------------------
 _TORCH_CODES = {}
+_calls = None
+
+
+def _fast():
+    """The marshalling extension (loaded on first use, after torch): each of its
+    functions enqueues a call whose tensors are all contiguous and as expected, and
+    returns False, with nothing enqueued, otherwise."""
+    global _calls
+    if _calls is None:
+        import torch  # noqa: F401  (the extension needs its libraries)
+        path = os.path.join(_PKG, "_fast_calls.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is not built. Build it with `python -m replayssm_persistent_rssm_amd.build` "
+                              "(or __graft_entry__.build()).")
+        import importlib.util
+        spec = importlib.util.spec_from_file_location("replayssm_persistent_rssm_amd._fast_calls", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        _calls = (mod, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    return _calls
 
 
 def _code(dt) -> int:
@@ -695,6 +715,12 @@ def rssm_linear_attention(state, A, x, B, C, dt, y, slots, seq_start, *, max_seq
     sequence), load_state int32 [R] (0: start from a zero state), D, dt_bias fp32
     [H], z, dt_softplus=True, pad_slot_id=-1, workspace (uint8 tensor of
     rssm_linear_attention_workspace's size; allocated when needed and not given)."""
+    if stream is None:
+        mod, device, current = _fast()
+        i = device()
+        if mod.linear_attention(i, current(i), False, state, A, x, B, C, dt, y, slots, seq_start, max_seq_len,
+                                load_state, D, dt_bias, z, dt_softplus, pad_slot_id, workspace):
+            return
     desc, tab, dev = _linear_marshal(state, A, x, B, C, dt, y, slots, seq_start, max_seq_len, load_state, D, dt_bias, z,
                                      dt_softplus, pad_slot_id)
     ws = _give_workspace(desc, tab, _lib.rssm_linear_attention_workspace, workspace, dev, stream)  # noqa: F841
@@ -714,6 +740,12 @@ def rssm_linear_attention_step(state, A, x, B, C, dt, y, slots, *, D=None, dt_bi
     """Enqueue the single-token form: row r of x, B, C, dt, z and y is request
     r's token.  Arguments as rssm_linear_attention without seq_start,
     max_seq_len, load_state and workspace."""
+    if stream is None:
+        mod, device, current = _fast()
+        i = device()
+        if mod.linear_attention(i, current(i), True, state, A, x, B, C, dt, y, slots, None, 1, None, D, dt_bias, z,
+                                dt_softplus, pad_slot_id, None):
+            return
     desc, tab, dev = _linear_marshal(state, A, x, B, C, dt, y, slots, None, 1, None, D, dt_bias, z, dt_softplus,
                                      pad_slot_id)
     _launch(_lib.rssm_linear_attention_step, desc, tab, dev, stream)
@@ -756,6 +788,11 @@ def rssm_paged_append(k_cache, v_cache, k_new, v_new, page_table, seq_start, kv_
     counted).  Caches [pages, page_size, kv_heads, head_dim], any strides with
     dense head_dim, both alike; page_table int32 [S, pages] (entries outside
     [0, pages) are skipped)."""
+    if stream is None:
+        mod, device, current = _fast()
+        i = device()
+        if mod.paged_append(i, current(i), k_cache, v_cache, k_new, v_new, page_table, seq_start, kv_len):
+            return
     desc, tab, dev = _paged_caches(k_cache, v_cache, page_table, seq_start, kv_len)
     N, dense = k_new.shape[0], desc.num_kv_heads * desc.head_dim
     shape = (N, desc.num_kv_heads, desc.head_dim)
@@ -791,8 +828,9 @@ def _paged_marshal(q, k_cache, v_cache, page_table, seq_start, kv_len, out, *, m
     return desc, tab, dev
 
 
-def rssm_paged_attention(q, k_cache, v_cache, page_table, seq_start, kv_len, out, *, workspace=None, stream=None,
-                         **kw) -> None:
+def rssm_paged_attention(q, k_cache, v_cache, page_table, seq_start, kv_len, out, *, max_seq_len: int,
+                         max_kv_len: int, scale=None, window: int = 0, sinks: int = 0, lse=None, workspace=None,
+                         stream=None) -> None:
     """Enqueue causal attention of each sequence's new tokens (the last
     seq_start[s+1] - seq_start[s] of its kv_len[s] cached tokens) over a paged
     cache.  q, out [N, q_heads, head_dim] (rows may be views of wider ones);
@@ -802,7 +840,14 @@ def rssm_paged_attention(q, k_cache, v_cache, page_table, seq_start, kv_len, out
     all), sinks=0 (first tokens seen beside the window), lse fp32 [N, q_heads]
     (optional output), workspace (uint8 tensor of
     rssm_paged_attention_workspace's size; allocated when needed and not given)."""
-    desc, tab, dev = _paged_marshal(q, k_cache, v_cache, page_table, seq_start, kv_len, out, **kw)
+    if stream is None:
+        mod, device, current = _fast()
+        i = device()
+        if mod.paged_attention(i, current(i), q, k_cache, v_cache, page_table, seq_start, kv_len, out, max_seq_len,
+                               max_kv_len, scale, window, sinks, lse, workspace):
+            return
+    desc, tab, dev = _paged_marshal(q, k_cache, v_cache, page_table, seq_start, kv_len, out, max_seq_len=max_seq_len,
+                                    max_kv_len=max_kv_len, scale=scale, window=window, sinks=sinks, lse=lse)
     ws = _give_workspace(desc, tab, _lib.rssm_paged_attention_workspace, workspace, dev, stream)  # noqa: F841
     _launch(_lib.rssm_paged_attention, desc, tab, dev, stream)
 
@@ -826,6 +871,12 @@ def rssm_block_norm(y, residual, residual_out, normed=None, *, z=None, post_weig
     channel_scale are fp32 [channels].  post_weight=None: no norm of the
     block's output; z, channel_scale, pre_weight and normed are optional.
     residual_out may be residual, normed may be y."""
+    if stream is None:
+        mod, device, current = _fast()
+        i = device()
+        if mod.block_norm(i, current(i), y, residual, residual_out, normed, z, post_weight, pre_weight, channel_scale,
+                          residual_scale, groups, eps):
+            return
     import torch
     dev = _device_index(y, "y")
     if y.dim() != 2:

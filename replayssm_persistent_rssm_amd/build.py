@@ -1,6 +1,7 @@
 """Build librssm_materialize.so (the operation) and librssm_pool.so (the
 contiguous-pool placement helper, a separate library so that the operation's
-library exports nothing that allocates) for gfx950 with hipcc, in-tree, no JIT.
+library exports nothing that allocates) for gfx950 with hipcc, and the
+binding's marshalling extension with the host compiler, in-tree, no JIT.
 
 Each state dtype's kernel instances live in their own translation unit and
 compile in parallel; the host launcher is one more.  Flags: -O3, C++17,
@@ -30,6 +31,9 @@ SOURCES = ["rssm_inst_f32.hip", "rssm_inst_bf16.hip", "rssm_inst_f16.hip", "rssm
            "rssm_inst_norm_f32.hip", "rssm_inst_norm_bf16.hip", "rssm_inst_norm_f16.hip",
            "rssm_linear_attention.hip", "rssm_paged_attention.hip", "rssm_block_norm.hip"]
 POOL_SOURCES = ["rssm_pool.hip"]
+# the binding's marshalling extension (host code against torch's headers)
+FAST_SOURCE = "fast_calls.cpp"
+FAST_PATH = os.path.join(PKG, "_fast_calls.so")
 ARCH = os.environ.get("RSSM_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -55,7 +59,7 @@ def _compile(src: str, verbose: bool) -> str:
 
 def _link(objs, path: str, verbose: bool) -> None:
     tmp = path + ".tmp"
-    cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
+    cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-Wl,-soname," + os.path.basename(path), "-o", tmp] + objs
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -64,14 +68,35 @@ def _link(objs, path: str, verbose: bool) -> None:
     os.replace(tmp, path)
 
 
+def _build_fast(verbose: bool) -> None:
+    """The marshalling extension, linked to the operation library beside it."""
+    import sysconfig
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = FAST_PATH + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I" + INCLUDE,
+           "-I" + sysconfig.get_paths()["include"], "-I" + inc,
+           "-I" + os.path.join(inc, "torch", "csrc", "api", "include"), os.path.join(CSRC, FAST_SOURCE), "-o", tmp,
+           "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", LIB_PATH, "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"build of {os.path.basename(FAST_PATH)} failed:\n" + res.stderr)
+    os.replace(tmp, FAST_PATH)
+
+
 def build(verbose: bool = False, jobs: int = 8) -> str:
-    """Compile and link both libraries; returns the operation library's path."""
+    """Compile and link both libraries and the binding's extension; returns the operation library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = SOURCES + POOL_SOURCES
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(jobs, len(srcs))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
     _link(objs[:len(SOURCES)], LIB_PATH, verbose)
     _link(objs[len(SOURCES):], POOL_LIB_PATH, verbose)
+    _build_fast(verbose)
     return LIB_PATH
 
 
