@@ -99,18 +99,22 @@ struct LinLds {
   typedef typename Mma<IT>::elem elem;
   static constexpr int kN = tile_pitch<IT>(N);
   static constexpr int kP = tile_pitch<IT>(kLinP);
+  static constexpr int kS = N + 16 / static_cast<int>(sizeof(elem));   // read by rows only: rows 4 banks apart
   elem Bs[kLinQ * kN];
-  elem Ss[kLinP * kN];
+  elem Ss[kLinP * kS];
   elem Xs[kLinQ * kP];
-  // four chunks at a time: l_i in log2 units (and, for fp32, the part that its rounding
-  // dropped), exp(l_i), dt_i, w_i; the whole chunk's decay and its logarithm
-  float l2[4][kLinQ], l2lo[IT == kF32 ? 4 : 1][kLinQ], e[4][kLinQ], dt[4][kLinQ], w[4][kLinQ];
+  // four chunks at a time: l_i in log2 units from the end of the 16 tokens before i's
+  // tile, exp(l_i), dt_i, w_i, and for tiles 1 .. 3 the weight exp(l_ref - l_j) dt_j of an
+  // earlier token up to the tile's start (both factors of exp(l_i - l_j) then shrink
+  // where the decay does, and only the tile on the diagonal needs one exponential a pair)
+  float lr[4][kLinQ], e[4][kLinQ], dt[4][kLinQ], w[4][kLinQ], before[4][3][kLinQ];
+  // the whole chunk's decay and its logarithm
   float decay[4], total[4];
   float sinv[kLinP];   // fp16: inverse scale of each state row in Ss
 };
 
-// Stage `rows` x COLS elements at `base` (row stride `stride` elements) into
-// registers, rows past `rows` as zeros: the buffer size ends with the last row.
+// Stages 64 rows of COLS elements through registers, rows past the sequence as
+// zeros: the buffer size ends with its last row.
 template <int IT, int COLS>
 struct Stage {
   typedef typename Mma<IT>::elem elem;
@@ -118,23 +122,68 @@ struct Stage {
   static constexpr int kPerRow = COLS / kVec;
   static constexpr int kN = kLinQ * kPerRow / kLinBlock;
   u32x4 v[kN];
-  __device__ __forceinline__ void load(const char* base, int64_t stride, int rows, int tid) {
-    const uint32_t rb = static_cast<uint32_t>(stride * sizeof(elem));
-    const rsrc_t r = make_rsrc(base, rows > 0 ? (rows - 1) * rb + COLS * sizeof(elem) : 0);
+  uint32_t at[kN];
+  __device__ __forceinline__ void init(uint32_t row_bytes, int tid) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int at = tid + i * kLinBlock;
-      v[i] = bload16<false>(r, (at / kPerRow) * rb + (at % kPerRow) * 16, 0);
+      const int k = tid + i * kLinBlock;
+      at[i] = (k / kPerRow) * row_bytes + (k % kPerRow) * 16;
     }
+  }
+  __device__ __forceinline__ void load(const char* base, uint32_t row_bytes, int rows) {
+    const rsrc_t r = make_rsrc(base, (rows - 1) * row_bytes + COLS * sizeof(elem));
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = bload16<false>(r, at[i], 0);
   }
   __device__ __forceinline__ void store(elem* tile, int pitch, int tid) const {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int at = tid + i * kLinBlock;
-      *reinterpret_cast<u32x4*>(tile + (at / kPerRow) * pitch + (at % kPerRow) * kVec) = v[i];
+      const int k = tid + i * kLinBlock;
+      *reinterpret_cast<u32x4*>(tile + (k / kPerRow) * pitch + (k % kPerRow) * kVec) = v[i];
     }
   }
 };
+
+// exp(x) from the hardware's exp2: the product x log2(e) is carried in two parts, so that
+// the result is within a few units of the last place at any x.
+__device__ __forceinline__ float exp_near(float x) {
+  const float y = x * 1.44269502f;                              // log2(e) = 1.44269502 + 1.92596e-8
+  const float r = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269502f, -y));
+  const float e = __builtin_amdgcn_exp2f(y);
+  return fabsf(y) < 150.0f ? fmaf(e, r * 0.693147181f, e) : e;   // far out: 0, infinity or NaN as it is
+}
+
+// softplus(raw + bias) = max(v, 0) + log(1 + t), t = exp(-|v|), with the sum's
+// rounding error (Knuth's TwoSum) carried to t.  log(1 + t) = 2 artanh(s), s = t / (2 + t)
+// <= 1/3, by its series up to s^15: small dt keep their relative accuracy.
+__device__ __forceinline__ float prompt_dt(float raw, float bias, int softplus) {
+  const float v = raw + bias;
+  if (!softplus) return v;
+  const float bb = v - raw;
+  const float lo = (raw - (v - bb)) + (bias - bb);
+  const float t0 = exp_near(-fabsf(v));
+  const float t = fmaf(t0, v > 0.0f ? -lo : lo, t0);
+  const float d = 2.0f + t;
+  float rc = __builtin_amdgcn_rcpf(d);
+  rc = fmaf(rc, fmaf(-d, rc, 1.0f), rc);
+  const float s = t * rc, q = s * s;
+  float p = 2.0f / 15.0f;
+  p = fmaf(p, q, 2.0f / 13.0f);
+  p = fmaf(p, q, 2.0f / 11.0f);
+  p = fmaf(p, q, 2.0f / 9.0f);
+  p = fmaf(p, q, 2.0f / 7.0f);
+  p = fmaf(p, q, 2.0f / 5.0f);
+  p = fmaf(p, q, 2.0f / 3.0f);
+  const float l = fmaf(s * q, p, 2.0f * s);
+  return v > 0.0f ? v + (lo + l) : l;
+}
+
+// v of the lane n places up (n < 0: down) in the lane's row of 16, 0 past its end.
+template <int n>
+__device__ __forceinline__ float row_shift(float v) {
+  constexpr int ctrl = n > 0 ? 0x110 + n : 0x100 - n;   // row_shr : row_shl
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, true));
+}
 
 template <int IT, int ST, int N, bool kStateOnly>
 __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_kernel(LinArgs a) {
@@ -204,20 +253,33 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
   Stage<IT, N> br;
   frag cr[KS];
   const int64_t hx = static_cast<int64_t>(h) * a.dim + pt0 * kLinP;
+  const uint32_t xb = static_cast<uint32_t>(a.x_stride * es), Bb = static_cast<uint32_t>(a.B_stride * es);
+  const uint32_t cb = static_cast<uint32_t>(a.C_stride * es), zb = static_cast<uint32_t>(a.z_stride * es);
+  const uint32_t yb = static_cast<uint32_t>(a.y_stride * es);
+  // addresses of the chunk to load next (x, B, C) and of the current one (z, y)
+  const int64_t first = q.start + t0;
+  const char* px = a.x + (first * a.x_stride + hx) * es;
+  const char* pB = a.B + (first * a.B_stride + static_cast<int64_t>(grp) * N) * es;
+  const char* pC = a.C + (first * a.C_stride + static_cast<int64_t>(grp) * N) * es;
+  const char* pz = a.z + (first * a.z_stride + hx) * es;
+  char* py = a.y + (first * a.y_stride + hx) * es;
+  xr.init(xb, tid);
+  br.init(Bb, tid);
+  const uint32_t c_at = (16 * wrow + li) * cb + 8 * g * es, z_at = (16 * wrow + li) * zb + 4 * g * es;
   auto fetch = [&](int t) {
     const int rows = t1 - t < kLinQ ? t1 - t : kLinQ;
-    const int64_t row = q.start + t;
-    xr.load(a.x + (row * a.x_stride + hx) * es, a.x_stride, rows, tid);
-    br.load(a.B + (row * a.B_stride + static_cast<int64_t>(grp) * N) * es, a.B_stride, rows, tid);
+    xr.load(px, xb, rows);
+    br.load(pB, Bb, rows);
+    px += static_cast<int64_t>(kLinQ) * xb;
+    pB += static_cast<int64_t>(kLinQ) * Bb;
   };
   auto fetch_C = [&](int t) {   // C rows of the wavefront's tokens: column i = 16 wrow + li
     const int rows = t1 - t < kLinQ ? t1 - t : kLinQ;
-    const int64_t row = q.start + t;
-    const uint32_t cb = static_cast<uint32_t>(a.C_stride * es);
-    const rsrc_t rc = make_rsrc(a.C + (row * a.C_stride + static_cast<int64_t>(grp) * N) * es, (rows - 1) * cb + N * es);
+    const rsrc_t rc = make_rsrc(pC, (rows - 1) * cb + N * es);
+    pC += static_cast<int64_t>(kLinQ) * cb;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
-      const uint32_t at = (16 * wrow + li) * cb + (32 * k + 8 * g) * es;
+      const uint32_t at = c_at + 32 * k * es;
       if constexpr (IT == kF32) {
         const u32x4 u = bload16<false>(rc, at, 0), v = bload16<false>(rc, at + 16, 0);
         cr[k] = __builtin_bit_cast(frag, u32x8{u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w});
@@ -238,28 +300,44 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
     }
     return v;
   };
-  // each wavefront turns one chunk's dt into its decays and weights
+  // Each wavefront turns one chunk's dt into its decays and weights.  Sums of dt A run
+  // inside tiles of 16 tokens (lane rows), forwards and backwards, and the tiles' totals
+  // multiply as exponentials: every exponent is a sum of terms of one sign, with no
+  // cancellation however far the chunk decays.
   auto scan_dt = [&](int t, float raw) {
     const bool in = t + kLinQ * wave + lane < t1;
-    float dtv = a.dt != nullptr ? new_token_dt(raw, bias, a.dt_softplus) : 1.0f;
+    float dtv = a.dt != nullptr ? prompt_dt(raw, bias, a.dt_softplus) : 1.0f;
     dtv = in ? dtv : 0.0f;
-    // sums of dt A in fp64: differences of far positions keep their relative accuracy
-    double l = static_cast<double>(dtv) * static_cast<double>(A);
+    const float da = dtv * A;
+    float f = da, r = da;   // inclusive sums up to, and from, the lane's token
+    f += row_shift<1>(f);
+    r += row_shift<-1>(r);
+    f += row_shift<2>(f);
+    r += row_shift<-2>(r);
+    f += row_shift<4>(f);
+    r += row_shift<-4>(r);
+    f += row_shift<8>(f);
+    r += row_shift<-8>(r);
+    float T[4], E[4];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double o = __shfl_up(l, d);
-      if (lane >= d) l += o;
+    for (int k = 0; k < 4; ++k) {
+      T[k] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), 16 * k + 15));
+      E[k] = exp_near(T[k]);
     }
-    const double end = __shfl(l, 63);
-    const double l2 = l * 1.4426950408889634074;
-    L.l2[wave][lane] = static_cast<float>(l2);
-    if constexpr (IT == kF32) L.l2lo[wave][lane] = static_cast<float>(l2 - static_cast<float>(l2));
-    L.e[wave][lane] = expf(static_cast<float>(l));
+    float e = exp_near(f), c = in ? exp_near(row_shift<-1>(r)) * dtv : 0.0f;
+    L.lr[wave][lane] = f * 1.44269504f;
     L.dt[wave][lane] = dtv;
-    L.w[wave][lane] = in ? expf(static_cast<float>(end - l)) * dtv : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      e *= lane >= 16 * (k + 1) ? E[k] : 1.0f;
+      L.before[wave][k][lane] = lane < 16 * (k + 1) ? c : 0.0f;
+      c *= lane < 16 * (k + 1) ? E[k + 1] : 1.0f;
+    }
+    L.e[wave][lane] = e;
+    L.w[wave][lane] = c;
     if (lane == 0) {
-      L.decay[wave] = expf(static_cast<float>(end));
-      L.total[wave] = static_cast<float>(end);
+      L.decay[wave] = (E[0] * E[1]) * (E[2] * E[3]);
+      L.total[wave] = (T[0] + T[1]) + (T[2] + T[3]);
     }
   };
 
@@ -290,7 +368,7 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        narrow4<IT>(L.Ss + (16 * wave + li) * LinLds<IT, N>::kN + 16 * n + 4 * g, IT == kF16 ? S[n] * sc : S[n]);
+        narrow4<IT>(L.Ss + (16 * wave + li) * LinLds<IT, N>::kS + 16 * n + 4 * g, IT == kF16 ? S[n] * sc : S[n]);
     }
     if (c4 == 0) scan_dt(t, dtr);
     __syncthreads();
@@ -302,48 +380,56 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
       u32x4 zr[4];
       const bool has_z = a.z != nullptr;
       if (has_z) {
-        const uint32_t zb = static_cast<uint32_t>(a.z_stride * es);
-        const rsrc_t rz = make_rsrc(a.z + ((q.start + t) * a.z_stride + hx) * es, (rows - 1) * zb + kLinP * es);
+        const rsrc_t rz = make_rsrc(pz, (rows - 1) * zb + kLinP * es);
+        pz += static_cast<int64_t>(kLinQ) * zb;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const uint32_t at = i * zb + (16 * p + 4 * g) * es;
           if constexpr (IT == kF32) {
-            zr[p] = bload16<false>(rz, at, 0);
+            zr[p] = bload16<false>(rz, z_at + 16 * p * es, 0);
           } else {
-            const auto w = __builtin_amdgcn_raw_buffer_load_b64(rz, at, 0, 0);
+            const auto w = __builtin_amdgcn_raw_buffer_load_b64(rz, z_at + 16 * p * es, 0, 0);
             zr[p] = u32x4{w[0], w[1], 0, 0};
           }
         }
       }
       // masked, decay-weighted scores M^T[j][i], j = 16 jt + 4g + r
       f32x4 M[4], Y[4];
-      const float lhi = L.l2[c4][i];
+      const float lri = L.lr[c4][i];
+      // scores (4 tiles of 16 tokens), then the starting state's part (4 tiles of 16 rows): the
+      // next tile's fragments are read while the matrix cores take the current ones
+      frag f[2][KS];
+      auto read = [&](int u, frag (&to)[KS]) {
+        const elem* src = u < 4 ? L.Bs + (16 * u + li) * LinLds<IT, N>::kN : L.Ss + (16 * (u - 4) + li) * LinLds<IT, N>::kS;
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt) {
-        M[jt] = f32x4{0, 0, 0, 0};
+        for (int k = 0; k < KS; ++k) to[k] = frag_row<IT>(src + 32 * k + 8 * g);
+      };
+      read(0, f[0]);
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-          M[jt] = mma<IT>(frag_row<IT>(L.Bs + (16 * jt + li) * LinLds<IT, N>::kN + 32 * k + 8 * g), cr[k], M[jt]);
-      }
+      for (int u = 0; u < 8; ++u) {
+        if (u < 7) read(u + 1, f[(u + 1) & 1]);
+        f32x4 acc = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        Y[p] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-          Y[p] = mma<IT>(frag_row<IT>(L.Ss + (16 * p + li) * LinLds<IT, N>::kN + 32 * k + 8 * g), cr[k], Y[p]);
+        for (int k = 0; k < KS; ++k) acc = mma<IT>(f[u & 1][k], cr[k], acc);
+        if (u < 4) M[u] = acc;
+        else Y[u - 4] = acc;
+        __builtin_amdgcn_sched_barrier(0);
       }
       if (t + kLinQ < t1) fetch_C(t + kLinQ);
+      const float ai = __builtin_amdgcn_exp2f(lri);
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
-        const f32x4 lj = *reinterpret_cast<const f32x4*>(L.l2[c4] + 16 * jt + 4 * g);
-        const f32x4 dj = *reinterpret_cast<const f32x4*>(L.dt[c4] + 16 * jt + 4 * g);
-        f32x4 d = lhi - lj;
-        if constexpr (IT == kF32)
-          d += L.l2lo[c4][i] - *reinterpret_cast<const f32x4*>(L.l2lo[c4] + 16 * jt + 4 * g);
+        if (jt < wrow) {          // earlier tiles: every token is visible
+          M[jt] *= *reinterpret_cast<const f32x4*>(L.before[c4][wrow - 1] + 16 * jt + 4 * g) * ai;
+        } else if (jt == wrow) {  // the diagonal
+          const f32x4 d = lri - *reinterpret_cast<const f32x4*>(L.lr[c4] + 16 * jt + 4 * g);
+          const f32x4 dj = *reinterpret_cast<const f32x4*>(L.dt[c4] + 16 * jt + 4 * g);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float v = M[jt][r] * (__builtin_amdgcn_exp2f(d[r]) * dj[r]);
-          M[jt][r] = 16 * jt + 4 * g + r <= i ? v : 0.0f;
+          for (int r = 0; r < 4; ++r) {
+            const float v = M[jt][r] * (__builtin_amdgcn_exp2f(d[r]) * dj[r]);
+            M[jt][r] = 4 * g + r <= li ? v : 0.0f;
+          }
+        } else {
+          M[jt] = f32x4{0, 0, 0, 0};
         }
       }
       int mk = 0;
@@ -379,19 +465,24 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
           X[p] = mma_seen<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 32, 16 * p, lane), m1, X[p]);
         }
       }
-      if (i < rows) {
-        elem* yp = reinterpret_cast<elem*>(a.y) + (q.start + t + i) * a.y_stride + hx + 4 * g;
+      elem* yp = reinterpret_cast<elem*>(py + i * yb) + 4 * g;
+      py += static_cast<int64_t>(kLinQ) * yb;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        if constexpr (IT == kF16) Y[p] *= *reinterpret_cast<const f32x4*>(L.sinv + 16 * p + 4 * g);
+        Y[p] = Y[p] * ei + X[p] * mi + widen4<IT>(L.Xs + i * LinLds<IT, N>::kP + 16 * p + 4 * g) * Dh;
+      }
+      if (has_z) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          if constexpr (IT == kF16) Y[p] *= *reinterpret_cast<const f32x4*>(L.sinv + 16 * p + 4 * g);
-          f32x4 v = Y[p] * ei + X[p] * mi + widen4<IT>(L.Xs + i * LinLds<IT, N>::kP + 16 * p + 4 * g) * Dh;
-          if (has_z) {
-            const f32x4 zi = widen4_raw<IT>(zr[p]);
+          const f32x4 zi = widen4_raw<IT>(zr[p]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] *= silu(zi[r]);
-          }
-          narrow4<IT>(yp + 16 * p, v);
+          for (int r = 0; r < 4; ++r) Y[p][r] *= silu(zi[r]);
         }
+      }
+      if (i < rows) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) narrow4<IT>(yp + 16 * p, Y[p]);
       }
     }
 
