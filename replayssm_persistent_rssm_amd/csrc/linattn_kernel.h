@@ -100,17 +100,17 @@ struct LinLds {
   static constexpr int kN = tile_pitch<IT>(N);
   static constexpr int kP = tile_pitch<IT>(kLinP);
   static constexpr int kS = N + 16 / static_cast<int>(sizeof(elem));   // read by rows only: rows 4 banks apart
-  elem Bs[kLinQ * kN];
-  elem Ss[kLinP * kS];
-  elem Xs[kLinQ * kP];
+  alignas(16) elem Bs[kLinQ * kN];
+  alignas(16) elem Ss[kLinP * kS];
+  alignas(16) elem Xs[kLinQ * kP];
   // four chunks at a time: l_i in log2 units from the end of the 16 tokens before i's
   // tile, exp(l_i), dt_i, w_i, and for tiles 1 .. 3 the weight exp(l_ref - l_j) dt_j of an
   // earlier token up to the tile's start (both factors of exp(l_i - l_j) then shrink
   // where the decay does, and only the tile on the diagonal needs one exponential a pair)
-  float lr[4][kLinQ], e[4][kLinQ], dt[4][kLinQ], w[4][kLinQ], before[4][3][kLinQ];
+  alignas(16) float lr[4][kLinQ], e[4][kLinQ], dt[4][kLinQ], w[4][kLinQ], before[4][3][kLinQ];
   // the whole chunk's decay and its logarithm
   float decay[4], total[4];
-  float sinv[kLinP];   // fp16: inverse scale of each state row in Ss
+  alignas(16) float sinv[kLinP];   // fp16: inverse scale of each state row in Ss
 };
 
 // Stages 64 rows of COLS elements through registers, rows past the sequence as
@@ -372,7 +372,7 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
     }
     if (c4 == 0) scan_dt(t, dtr);
     __syncthreads();
-    if (t + kLinQ < t1) fetch(t + kLinQ);
+    if (kStateOnly && t + kLinQ < t1) fetch(t + kLinQ);
     if (c4 == 2) dtr = fetch_dt(t + 2 * kLinQ);
 
     if constexpr (!kStateOnly) {
@@ -414,7 +414,10 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
         else Y[u - 4] = acc;
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (t + kLinQ < t1) fetch_C(t + kLinQ);
+      if (t + kLinQ < t1) {
+        fetch(t + kLinQ);
+        fetch_C(t + kLinQ);
+      }
       const float ai = __builtin_amdgcn_exp2f(lri);
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
@@ -446,18 +449,14 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
       }
       const float ei = L.e[c4][i], mi = pow2i(-mk);
       f32x4 X[4];
-      bool bad = false;
       const frag m0 = to_frag<IT>(stack(M[0], M[1])), m1 = to_frag<IT>(stack(M[2], M[3]));
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         X[p] = mma<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 0, 16 * p, lane), m0, f32x4{0, 0, 0, 0});
         X[p] = mma<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 32, 16 * p, lane), m1, X[p]);
       }
-#pragma unroll
-      for (int p = 0; p < 4; ++p)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) bad |= !(fabsf(X[p][r]) < __builtin_inff());
-      if (__builtin_expect(__ballot(bad) != 0, 0)) {
+      const f32x4 xs = (X[0] + X[1]) + (X[2] + X[3]);
+      if (__builtin_expect(__ballot(!(fabsf((xs[0] + xs[1]) + (xs[2] + xs[3])) < __builtin_inff())) != 0, 0)) {
         // a non-finite x may have met the zero weight of a later token
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
@@ -510,11 +509,14 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const f32x8 v = IT == kF16 ? wx[k] * up : wx[k];
-      u0[k] = to_frag<IT>(v);
-      if constexpr (kParts > 1) {
-        const f32x8 v1 = v - from_frag<IT>(u0[k]);
-        u1[k] = to_frag<IT>(v1);
-        if constexpr (kParts > 2) u2[k] = to_frag<IT>(v1 - from_frag<IT>(u1[k]));
+      if constexpr (IT == kBF16) {
+        f32x8 left = v;
+        u0[k] = take_bf16(left);
+        u1[k] = take_bf16(left);
+        if constexpr (kParts > 2) u2[k] = take_bf16(left);
+      } else {
+        u0[k] = to_frag<IT>(v);
+        if constexpr (kParts > 1) u1[k] = to_frag<IT>(v - from_frag<IT>(u0[k]));
       }
     }
     const float dup = IT == kF16 ? decay * up : decay;

@@ -61,6 +61,20 @@ __device__ __forceinline__ typename Mma<IT>::frag to_frag(f32x8 v) {
   return __builtin_convertvector(v, typename Mma<IT>::frag);
 }
 
+// The leading 8 significant bits of each value as bf16 (cut off, so that three turns
+// take all 24 exactly); `v` keeps the rest.
+__device__ __forceinline__ bf16x8 take_bf16(f32x8& v) {
+  u32x4 p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = __float_as_uint(v[2 * i]), b = __float_as_uint(v[2 * i + 1]);
+    p[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+    v[2 * i] -= __uint_as_float(a & 0xffff0000u);
+    v[2 * i + 1] -= __uint_as_float(b & 0xffff0000u);
+  }
+  return __builtin_bit_cast(bf16x8, p);
+}
+
 template <int IT>
 __device__ __forceinline__ f32x8 from_frag(typename Mma<IT>::frag v) {
   return __builtin_convertvector(v, f32x8);

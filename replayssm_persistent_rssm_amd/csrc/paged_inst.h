@@ -6,7 +6,7 @@
 
 namespace rssm {
 
-enum : int { kPagedTile8 = 0, kPagedTile4 = 1, kPagedRow = 2, kPagedJoin = 3 };
+enum : int { kPagedTile = 0, kPagedRow = 1, kPagedJoin = 2 };
 
 // Row blocks of 16 a wavefront of paged_tile_kernel holds: two share each K and V
 // fragment read from LDS; fp32 operands take the registers of two 16-bit ones.
@@ -14,8 +14,7 @@ constexpr int paged_row_blocks(int dtype) { return dtype == kF32 ? 1 : 2; }
 
 template <int IT, int D>
 const void* paged_fn(int which) {
-  if (which == kPagedTile8) return reinterpret_cast<const void*>(&paged_tile_kernel<IT, D, paged_row_blocks(IT), 8>);
-  if (which == kPagedTile4) return reinterpret_cast<const void*>(&paged_tile_kernel<IT, D, paged_row_blocks(IT), 4>);
+  if (which == kPagedTile) return reinterpret_cast<const void*>(&paged_tile_kernel<IT, D, paged_row_blocks(IT)>);
   if (which == kPagedRow) return reinterpret_cast<const void*>(&paged_row_kernel<IT, D>);
   return reinterpret_cast<const void*>(&paged_join_kernel<IT, D>);
 }

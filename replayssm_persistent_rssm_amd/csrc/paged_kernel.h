@@ -9,7 +9,7 @@
 //                                exchanges between the four lane groups
 //   O^T[d][i] += V^T P           A = V columns (transposing LDS read), Bm = P
 // with the running maximum m and sum l of each row (one pass over K and V).
-//  * paged_tile_kernel: many rows.  NW wavefronts x 16 RB rows share the K and
+//  * paged_tile_kernel: many rows.  4 wavefronts x 16 RB rows share the K and
 //    V tiles of 64 tokens, double-buffered in LDS; the next tile is loaded
 //    into registers while the current one is computed.
 //  * paged_row_kernel: at most 16 rows (single-token decoding).  Bound by
@@ -160,14 +160,12 @@ struct RowState {
 // The reference point follows the maximum only when it lags by more than 2^8:
 // sums and products stay far from overflow, most tiles need no rescaling, and the exchange
 // between lanes is left to the tiles that do.
-template <int JT>
-__device__ __forceinline__ bool lags(const PagedArgs& a, const f32x4 (&S)[JT], const RowState& st) {
-  float mx = -__builtin_inff();
-#pragma unroll
-  for (int jt = 0; jt < JT; ++jt)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) mx = fmaxf(mx, S[jt][r]);
+__device__ __forceinline__ bool lags(const PagedArgs& a, float mx, const RowState& st) {
   return mx * a.scale_log2 > st.m + 8.0f;
+}
+
+__device__ __forceinline__ float max4(float m, f32x4 v) {
+  return fmaxf(fmaxf(fmaxf(m, v[0]), fmaxf(v[1], v[2])), v[3]);
 }
 
 // New reference point; the factor for the sum and the output so far.
@@ -175,9 +173,7 @@ template <int JT>
 __device__ __forceinline__ float move_reference(const PagedArgs& a, const f32x4 (&S)[JT], RowState& st) {
   float mx = -__builtin_inff();
 #pragma unroll
-  for (int jt = 0; jt < JT; ++jt)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) mx = fmaxf(mx, S[jt][r]);
+  for (int jt = 0; jt < JT; ++jt) mx = max4(mx, S[jt]);
   const float mn = fmaxf(st.m, max_groups(mx) * a.scale_log2);
   const float alpha = mn == st.m ? 1.0f : __builtin_amdgcn_exp2f(st.m - mn);
   st.m = mn;
@@ -225,14 +221,14 @@ __device__ __forceinline__ int64_t shfl64(int64_t v, int from) {
   return (static_cast<int64_t>(hi) << 32) | static_cast<uint32_t>(lo);
 }
 
-template <int IT, int D, int RB, int NW>
-__global__ __launch_bounds__(64 * NW, IT == kF32 ? 1 : 2) void paged_tile_kernel(PagedArgs a) {
+template <int IT, int D, int RB>
+__global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_kernel(PagedArgs a) {
   typedef typename Mma<IT>::elem elem;
   typedef typename Mma<IT>::frag frag;
   constexpr int T = 64, JT = T / 16, KS = D / 32, DT = D / 16;
-  constexpr int kVec = 16 / sizeof(elem), kPerRow = D / kVec, kRowsPass = 64 * NW / kPerRow, kPasses = T / kRowsPass;
+  constexpr int kVec = 16 / sizeof(elem), kPerRow = D / kVec, kRowsPass = kPagedBlock / kPerRow, kPasses = T / kRowsPass;
   constexpr int kPitch = tile_pitch<IT>(D);
-  constexpr int kRows = 16 * RB * NW;
+  constexpr int kRows = 64 * RB;
   __shared__ __align__(16) elem lds[2][2][T * kPitch];   // [buffer][K, V]
   __shared__ int odd;   // an infinite or NaN element of V was met
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
@@ -359,7 +355,12 @@ __global__ __launch_bounds__(64 * NW, IT == kF32 ? 1 : 2) void paged_tile_kernel
     }
     bool move = false;
 #pragma unroll
-    for (int b = 0; b < RB; ++b) move |= lags<JT>(a, S[b], rs[b]);
+    for (int b = 0; b < RB; ++b) {
+      float mx = -__builtin_inff();
+#pragma unroll
+      for (int jt = 0; jt < JT; ++jt) mx = max4(mx, S[b][jt]);
+      move |= lags(a, mx, rs[b]);
+    }
     if (__ballot(move) != 0) {
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
@@ -397,28 +398,12 @@ __global__ __launch_bounds__(64 * NW, IT == kF32 ? 1 : 2) void paged_tile_kernel
     }
   };
   __syncthreads();
-  // With 8 wavefronts two share a SIMD: the later four run half a tile behind, so
-  // that one wavefront's exponentials meet the other's products.  Tile v + 1 is
-  // stored over tile v - 1 in the half step after the late wavefronts left it.
-  if (NW == 8 && wave >= 4) {
-    for (int v = v0; v < v1; ++v) {
-      ahead(v);
-      if (v > v0) outputs(v - 1);
-      __syncthreads();
-      scores(v);
-      if (v + 1 < v1) put((v + 1 - v0) & 1);
-      __syncthreads();
-    }
-    if (v0 < v1) outputs(v1 - 1);
-  } else {
-    for (int v = v0; v < v1; ++v) {
-      ahead(v);
-      scores(v);
-      if (NW == 8) __syncthreads();
-      outputs(v);
-      if (v + 1 < v1) put((v + 1 - v0) & 1);
-      __syncthreads();
-    }
+  for (int v = v0; v < v1; ++v) {
+    ahead(v);
+    scores(v);
+    outputs(v);
+    if (v + 1 < v1) put((v + 1 - v0) & 1);
+    __syncthreads();
   }
   if (__builtin_expect(odd, 0)) {
     // rare: the tiles once more from the cache, for the infinities and NaN among the values of
@@ -571,7 +556,7 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
       if (v + 2 * W < v1) off = cache_row(a, s, key_tile(kt, v + 2 * W) * T + (lane & 31), kt.limit, ok_next);
     }
     mask_tile<JT>(a, S, j0, pos, on_page, g);
-    if (__ballot(lags<JT>(a, S, rs)) != 0) {
+    if (__ballot(lags(a, max4(max4(-__builtin_inff(), S[0]), S[1]), rs)) != 0) {
       const float alpha = move_reference<JT>(a, S, rs);
 #pragma unroll
       for (int d = 0; d < DT; ++d) O[d] *= alpha;

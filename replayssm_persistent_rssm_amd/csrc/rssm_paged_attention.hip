@@ -91,22 +91,19 @@ rssm_status check_ptrs(const Ptr* p, int n, bool optional) {
 }
 
 struct Plan {
-  int kernel;         // kPagedRow (at most 16 rows a sequence and key/value head), kPagedTile4 or kPagedTile8
+  bool rows16;        // at most 16 rows a (sequence, key/value head): the streaming kernel
   int row_tiles, nsplit, split_tiles;
 };
 
 // The split of the key axis: none when the row tiles fill the chip; otherwise
-// enough that about kFill wavefronts run.  Fixed numbers of tiles a split keep ragged lengths
+// enough that about kFill workgroups run.  Fixed numbers of tiles a split keep ragged lengths
 // balanced.  A split reads at least kLeast tiles, so that joining costs little beside it.
 Plan plan_of(const rssm_paged_attention_desc* d) {
   Plan p;
   const int64_t group = d->num_q_heads / d->num_kv_heads;
   const int64_t rows = d->max_seq_len * group;
-  const bool rows16 = rows <= 16;
-  const int64_t block_rows = 16 * paged_row_blocks(d->dtype);   // of one wavefront
-  // 8 wavefronts share each tile of keys when there are rows for them
-  p.kernel = rows16 ? kPagedRow : (rows > 4 * block_rows ? kPagedTile8 : kPagedTile4);
-  const int64_t T = rows16 ? 32 : 64, tile_rows = rows16 ? 16 : block_rows * (p.kernel == kPagedTile8 ? 8 : 4);
+  p.rows16 = rows <= 16;
+  const int64_t T = p.rows16 ? 32 : 64, tile_rows = p.rows16 ? 16 : 64 * paged_row_blocks(d->dtype);
   p.row_tiles = static_cast<int>(std::max<int64_t>(1, (rows + tile_rows - 1) / tile_rows));
   int64_t tiles = (d->max_kv_len + T - 1) / T;
   if (d->window > 0) {
@@ -114,12 +111,11 @@ Plan plan_of(const rssm_paged_attention_desc* d) {
     tiles = std::min(tiles, (d->sinks + T - 1) / T + (d->window + span) / T + 2);
   }
   const int64_t items = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * p.row_tiles;
-  const int64_t waves = items * (p.kernel == kPagedTile8 ? 8 : 4);
-  const int64_t kFill = rows16 ? 4096 : 2048, kLeast = rows16 ? 16 : 4;
+  const int64_t kFill = p.rows16 ? 1024 : 512, kLeast = p.rows16 ? 16 : 4;
   p.nsplit = 1;
   p.split_tiles = 1 << 30;
-  if (items > 0 && waves <= (rows16 ? kFill : kFill / 2) && tiles >= 2 * kLeast) {
-    const int64_t want = (kFill + waves - 1) / waves;
+  if (items > 0 && items <= (p.rows16 ? kFill : kFill / 2) && tiles >= 2 * kLeast) {
+    const int64_t want = (kFill + items - 1) / items;
     const int64_t per = std::max(kLeast, (tiles + want - 1) / want);
     const int64_t n = (tiles + per - 1) / per;
     if (n > 1) {
@@ -178,10 +174,9 @@ void fill_args(PagedArgs* a, const rssm_paged_attention_desc* d, const rssm_page
   a->split_tiles = 1 << 30;
 }
 
-rssm_status launch(const void* fn, int64_t grid, void** params, void* stream, const char* name,
-                   int block = kPagedBlock) {
+rssm_status launch(const void* fn, int64_t grid, void** params, void* stream, const char* name) {
   if (grid > INT32_MAX) return fail(RSSM_ERR_INVALID_ARGUMENT, "%s: too many workgroups", name);
-  hipError_t e = hipLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(block), params, 0,
+  hipError_t e = hipLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kPagedBlock), params, 0,
                                  static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(RSSM_ERR_HIP, "launch of %s failed: %s", name, hipGetErrorString(e));
   return RSSM_OK;
@@ -256,10 +251,10 @@ rssm_status rssm_paged_attention(const rssm_paged_attention_desc* d, const rssm_
   if (verbose())
     std::fprintf(stderr, "[rssm_paged_attention] %s seqs=%d heads=%d/%d dim=%d %s row_tiles=%d splits=%d\n",
                  dtype_name(d->dtype), d->num_seqs, d->num_q_heads, d->num_kv_heads, d->head_dim,
-                 p.kernel == kPagedRow ? "rows" : "tiles", p.row_tiles, p.nsplit);
+                 p.rows16 ? "rows" : "tiles", p.row_tiles, p.nsplit);
   void* params[] = {&a};
   const int64_t grid = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * p.row_tiles * p.nsplit;
-  st = launch(kernel_for(p.kernel, d), grid, params, hip_stream, "paged_attention", p.kernel == kPagedTile8 ? 512 : 256);
+  st = launch(kernel_for(p.rows16 ? kPagedRow : kPagedTile, d), grid, params, hip_stream, "paged_attention");
   if (st != RSSM_OK || p.nsplit == 1) return st;
   return launch(kernel_for(kPagedJoin, d), out_rows, params, hip_stream, "paged_join");
 }
