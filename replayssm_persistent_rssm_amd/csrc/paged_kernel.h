@@ -467,9 +467,10 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int item = xcd_order(blockIdx.x, gridDim.x);
-  const int split = item % a.nsplit;
-  item /= a.nsplit;
-  const int kvh = item % a.Hkv, s = item / a.Hkv;
+  // heads first: workgroups that run together read neighbouring rows of the same pages
+  const int kvh = item % a.Hkv;
+  item /= a.Hkv;
+  const int split = item % a.nsplit, s = item / a.nsplit;
   const PagedSeq sq = paged_seq(a, s);
   const int rows = sq.q_len * a.group;
   if (rows == 0) return;
@@ -502,10 +503,10 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         if constexpr (IT == kF32) {
-          kr[jt][2 * k] = ld<true, u32x4>(p + 128 * k);
-          kr[jt][2 * k + 1] = ld<true, u32x4>(p + 128 * k + 16);
+          kr[jt][2 * k] = ld<false, u32x4>(p + 128 * k);
+          kr[jt][2 * k + 1] = ld<false, u32x4>(p + 128 * k + 16);
         } else {
-          kr[jt][k] = ld<true, u32x4>(p + 64 * k);
+          kr[jt][k] = ld<false, u32x4>(p + 64 * k);
         }
       }
     }
