@@ -567,11 +567,25 @@ __global__ __launch_bounds__(kLinBlock) void linattn_scan_kernel(LinArgs a, int 
     run = load_state4<ST>(a.state + (q.slot * a.state_stride + hs) * ss);
   float* w = a.ws_state + static_cast<int64_t>(s) * a.nseg * wtile + hs;
   *reinterpret_cast<f32x4*>(w) = run;
-  for (int k = 0; (k + 1) * static_cast<int64_t>(a.seg_len) < q.len; ++k) {
-    w += wtile;
-    const float d = expf(sload(a.ws_decay + (static_cast<int64_t>(s) * a.nseg + k) * a.H + h));
-    run = run * d + *reinterpret_cast<const f32x4*>(w);
-    *reinterpret_cast<f32x4*>(w) = run;
+  const float* dec = a.ws_decay + static_cast<int64_t>(s) * a.nseg * a.H + h;
+  const int steps = q.len > 0 ? (q.len - 1) / a.seg_len : 0;   // stretches that another one follows
+  constexpr int U = 8;   // loads in flight
+  for (int k0 = 0; k0 < steps; k0 += U) {
+    f32x4 own[U];
+    float d[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u < steps ? k0 + u : steps - 1;
+      own[u] = *reinterpret_cast<const f32x4*>(w + (k + 1) * wtile);
+      d[u] = sload(dec + static_cast<int64_t>(k) * a.H);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k0 + u < steps) {
+        run = run * exp_near(d[u]) + own[u];
+        *reinterpret_cast<f32x4*>(w + (k0 + u + 1) * wtile) = run;
+      }
+    }
   }
 }
 

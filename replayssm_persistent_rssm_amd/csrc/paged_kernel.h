@@ -68,14 +68,22 @@ __device__ __forceinline__ int page_of(const PagedArgs& a, int j) {
   return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(j)) * a.page_magic) >> a.page_shift);
 }
 
-// Cache row of token j of sequence s in elements (head 0); row 0 of the cache,
-// and ok = false, when the token lies on no page or at or past `limit`.
-__device__ __forceinline__ int64_t cache_row(const PagedArgs& a, int s, int j, int limit, bool& ok) {
+// Page table entry of token j of sequence s (of its first token past the table's end).
+__device__ __forceinline__ int page_entry(const PagedArgs& a, int s, int j) {
   const int pi = page_of(a, j);
-  ok = (j < limit) & (pi < a.max_pages);
-  const int page = gload(a.table + s * a.table_stride + (ok ? pi : 0));
-  ok &= (page >= 0) & (page < a.num_pages);
+  return gload(a.table + s * a.table_stride + (pi < a.max_pages ? pi : 0));
+}
+
+// Cache row of token j in elements (head 0), given its table entry; row 0 of the
+// cache, and ok = false, when the token lies on no page or at or past `limit`.
+__device__ __forceinline__ int64_t page_row(const PagedArgs& a, int page, int j, int limit, bool& ok) {
+  const int pi = page_of(a, j);
+  ok = (j < limit) & (pi < a.max_pages) & (page >= 0) & (page < a.num_pages);
   return ok ? page * a.page_stride + (j - pi * a.page_size) * a.row_stride : 0;
+}
+
+__device__ __forceinline__ int64_t cache_row(const PagedArgs& a, int s, int j, int limit, bool& ok) {
+  return page_row(a, page_entry(a, s, j), j, limit, ok);
 }
 
 // Tiles of T keys that rows at positions [pmin, pmax] see: the first `sink`
@@ -311,12 +319,14 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
   };
   if (tid == 0) odd = 0;
   __syncthreads();
-  int64_t off = 0;
-  bool ok = false, ok_next = false;
+  // Loads complete in order, so the table entries of a tile are requested before
+  // the previous tile's keys and first looked at a tile later.
+  int entry = 0;
+  bool ok = false;
   if (v0 < v1) {
-    off = cache_row(a, s, key_tile(kt, v0) * T + lane, kt.limit, ok);
+    const int64_t off = cache_row(a, s, key_tile(kt, v0) * T + lane, kt.limit, ok);
+    if (v0 + 1 < v1) entry = page_entry(a, s, key_tile(kt, v0 + 1) * T + lane);
     fetch(off);
-    if (v0 + 1 < v1) off = cache_row(a, s, key_tile(kt, v0 + 1) * T + lane, kt.limit, ok_next);
     put(0);
   }
   f32x4 S[RB][JT];
@@ -388,13 +398,13 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
       }
     }
   };
-  // tile v + 1 into registers (and the pages of v + 2)
+  // tile v + 1 into registers, the table entries of v + 2
   auto ahead = [&](int v) {
     on_page = __ballot(ok);
     if (v + 1 < v1) {
+      const int64_t off = page_row(a, entry, key_tile(kt, v + 1) * T + lane, kt.limit, ok);
+      if (v + 2 < v1) entry = page_entry(a, s, key_tile(kt, v + 2) * T + lane);
       fetch(off);
-      ok = ok_next;
-      if (v + 2 < v1) off = cache_row(a, s, key_tile(kt, v + 2) * T + lane, kt.limit, ok_next);
     }
   };
   __syncthreads();
@@ -515,12 +525,12 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
       vr[i] = ld<true, u32x4>(a.v + (shfl64(row_off, srow + i * kRowsPass) + hoff + vec * kVec) * static_cast<int64_t>(sizeof(elem)));
   };
   const int first = v0 + wave;
-  int64_t off = 0;
-  bool ok = false, ok_next = false;
+  int entry = 0;
+  bool ok = false;
   if (first < v1) {
-    off = cache_row(a, s, key_tile(kt, first) * T + (lane & 31), kt.limit, ok);
+    const int64_t off = cache_row(a, s, key_tile(kt, first) * T + (lane & 31), kt.limit, ok);
+    if (first + W < v1) entry = page_entry(a, s, key_tile(kt, first + W) * T + (lane & 31));
     fetch(off);
-    if (first + W < v1) off = cache_row(a, s, key_tile(kt, first + W) * T + (lane & 31), kt.limit, ok_next);
   }
   for (int v = first; v < v1; v += W) {
     const int j0 = key_tile(kt, v) * T;
@@ -551,10 +561,10 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
       *reinterpret_cast<u32x4*>(Vt + (srow + i * kRowsPass) * kPitch + vec * kVec) = vr[i];
     }
     bad = __ballot(bad) != 0;
-    if (v + W < v1) {
+    if (v + W < v1) {   // (loads complete in order: entries before the keys, looked at a tile later)
+      const int64_t off = page_row(a, entry, key_tile(kt, v + W) * T + (lane & 31), kt.limit, ok);
+      if (v + 2 * W < v1) entry = page_entry(a, s, key_tile(kt, v + 2 * W) * T + (lane & 31));
       fetch(off);
-      ok = ok_next;
-      if (v + 2 * W < v1) off = cache_row(a, s, key_tile(kt, v + 2 * W) * T + (lane & 31), kt.limit, ok_next);
     }
     mask_tile<JT>(a, S, j0, pos, on_page, g);
     if (__ballot(lags(a, max4(max4(-__builtin_inff(), S[0]), S[1]), rs)) != 0) {

@@ -110,7 +110,7 @@ Split split_of(const rssm_linear_attention_desc* d) {
   const int64_t chunks = (static_cast<int64_t>(d->max_seq_len) + kLinQ - 1) / kLinQ;
   constexpr int64_t kFill = 512;
   if (items == 0 || items >= kFill || chunks < 8) return {1, static_cast<int>(std::max<int64_t>(chunks, 1) * kLinQ)};
-  const int64_t want = std::min((2 * kFill + items - 1) / items, chunks / 4);
+  const int64_t want = std::min((kFill + items - 1) / items, chunks / 4);
   if (want <= 1) return {1, static_cast<int>(chunks * kLinQ)};
   const int64_t per = (chunks + want - 1) / want;
   return {static_cast<int>((chunks + per - 1) / per), static_cast<int>(per * kLinQ)};

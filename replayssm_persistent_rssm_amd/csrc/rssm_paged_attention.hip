@@ -111,7 +111,8 @@ Plan plan_of(const rssm_paged_attention_desc* d) {
     tiles = std::min(tiles, (d->sinks + T - 1) / T + (d->window + span) / T + 2);
   }
   const int64_t items = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * p.row_tiles;
-  const int64_t kFill = p.rows16 ? 4096 : 512, kLeast = p.rows16 ? 32 : 4;
+  const int64_t kFill = p.rows16 ? 4096 : 512;
+  const int64_t kLeast = p.rows16 ? std::min<int64_t>(32, std::max<int64_t>(8, tiles / 32)) : 4;
   p.nsplit = 1;
   p.split_tiles = 1 << 30;
   if (items > 0 && items <= (p.rows16 ? kFill : kFill / 2) && tiles >= 2 * kLeast) {
