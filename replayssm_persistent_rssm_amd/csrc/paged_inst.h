@@ -6,7 +6,7 @@
 
 namespace rssm {
 
-enum : int { kPagedTile = 0, kPagedRow = 1, kPagedJoin = 2 };
+enum : int { kPagedTile = 0, kPagedRow = 1, kPagedJoin = 2, kPagedJoinShare = 3 };
 
 // Row blocks of 16 a wavefront of paged_tile_kernel holds: two share each K and V
 // fragment read from LDS; fp32 operands take the registers of two 16-bit ones.
@@ -16,7 +16,8 @@ template <int IT, int D>
 const void* paged_fn(int which) {
   if (which == kPagedTile) return reinterpret_cast<const void*>(&paged_tile_kernel<IT, D, paged_row_blocks(IT)>);
   if (which == kPagedRow) return reinterpret_cast<const void*>(&paged_row_kernel<IT, D>);
-  return reinterpret_cast<const void*>(&paged_join_kernel<IT, D>);
+  if (which == kPagedJoin) return reinterpret_cast<const void*>(&paged_join_kernel<IT, D, false>);
+  return reinterpret_cast<const void*>(&paged_join_kernel<IT, D, true>);
 }
 
 template <int IT>

@@ -624,17 +624,19 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
   }
 }
 
-// Joins the splits of one (token, head): the wavefronts share the splits, eight
-// partial outputs of each in flight, lanes over head_dim.
-template <int IT, int D>
+// Joins the splits of a (token, head), eight partial outputs in flight, lanes over
+// head_dim.  kShare: the workgroup's wavefronts share the splits of one row (many
+// splits); otherwise each takes a row of its own.
+template <int IT, int D, bool kShare>
 __global__ __launch_bounds__(kPagedBlock) void paged_join_kernel(PagedArgs a) {
   typedef typename Mma<IT>::elem elem;
   constexpr int E = D / 64, W = kPagedBlock / 64, U = 8;
   __shared__ float jo[W][D], jl[W];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = blockIdx.x;
+  const int64_t row = kShare ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * W + wave;
   const int64_t token = row / a.Hq;
+  if (token >= a.num_tokens) return;
   // rows that belong to no sequence were not computed: leave them alone
   int lo = 0, hi = a.num_seqs;
   while (lo < hi) {   // first sequence whose end lies past the token
@@ -656,7 +658,7 @@ __global__ __launch_bounds__(kPagedBlock) void paged_join_kernel(PagedArgs a) {
   float l = 0.0f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.0f;
-  for (int k0 = wave * U; k0 < a.nsplit; k0 += W * U) {
+  for (int k0 = kShare ? wave * U : 0; k0 < a.nsplit; k0 += kShare ? W * U : U) {
     float p[U][E], w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -667,24 +669,32 @@ __global__ __launch_bounds__(kPagedBlock) void paged_join_kernel(PagedArgs a) {
       for (int e = 0; e < E; ++e) p[u][e] = po[static_cast<int64_t>(k) * D + e];
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u)   // (an empty split wrote no output)
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = w[u] != 0.0f ? fmaf(p[u][e], w[u], o[e]) : o[e];
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e) jo[wave][lane * E + e] = o[e];
-  if (lane == 0) jl[wave] = l;
-  __syncthreads();
+  elem* out = reinterpret_cast<elem*>(a.out) + token * a.out_stride + static_cast<int64_t>(head) * D;
+  auto store = [&](int d, float v) {
+    if constexpr (IT == kF32) out[d] = v;
+    else if constexpr (IT == kBF16) out[d] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+    else out[d] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+  };
   const int d = threadIdx.x;
-  if (d >= D) return;
-  l = (jl[0] + jl[1]) + (jl[2] + jl[3]);
+  if constexpr (kShare) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) jo[wave][lane * E + e] = o[e];
+    if (lane == 0) jl[wave] = l;
+    __syncthreads();
+    l = (jl[0] + jl[1]) + (jl[2] + jl[3]);
+  }
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-  const float v = ((jo[0][d] + jo[1][d]) + (jo[2][d] + jo[3][d])) * inv;
-  elem* out = reinterpret_cast<elem*>(a.out) + token * a.out_stride + static_cast<int64_t>(head) * D + d;
-  if constexpr (IT == kF32) *out = v;
-  else if constexpr (IT == kBF16) *out = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
-  else *out = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
-  if (a.lse != nullptr && d == 0) a.lse[token * a.Hq + head] = (m + log2f(l)) * kLn2;
+  if constexpr (kShare) {
+    if (d < D) store(d, ((jo[0][d] + jo[1][d]) + (jo[2][d] + jo[3][d])) * inv);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) store(lane * E + e, o[e] * inv);
+  }
+  if (a.lse != nullptr && (kShare ? d : lane) == 0) a.lse[token * a.Hq + head] = (m + log2f(l)) * kLn2;
 }
 
 // Append: one thread a 16-byte vector of one new token's keys and values.

@@ -257,7 +257,10 @@ rssm_status rssm_paged_attention(const rssm_paged_attention_desc* d, const rssm_
   const int64_t grid = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * p.row_tiles * p.nsplit;
   st = launch(kernel_for(p.rows16 ? kPagedRow : kPagedTile, d), grid, params, hip_stream, "paged_attention");
   if (st != RSSM_OK || p.nsplit == 1) return st;
-  return launch(kernel_for(kPagedJoin, d), out_rows, params, hip_stream, "paged_join");
+  // few rows with many splits: a workgroup a row, otherwise a wavefront a row
+  const bool share = p.nsplit > 16 && out_rows < 4096;
+  return launch(kernel_for(share ? kPagedJoinShare : kPagedJoin, d), share ? out_rows : (out_rows + 3) / 4, params,
+                hip_stream, "paged_join");
 }
 
 }  // extern "C"
