@@ -238,7 +238,9 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
   constexpr int kPitch = tile_pitch<IT>(D);
   constexpr int kRows = 64 * RB;
   __shared__ __align__(16) elem lds[2][2][T * kPitch];   // [buffer][K, V]
-  __shared__ int odd;   // an infinite or NaN element of V was met
+  __shared__ int64_t rows_at[4][T];   // cache rows (elements) of a tile's tokens (tile v in slot v mod 4),
+  __shared__ uint64_t on_pages[4];    // and which of them lie on a page
+  __shared__ int odd;                 // an output is infinite or NaN
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int item = xcd_order(blockIdx.x, gridDim.x);
@@ -277,38 +279,29 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
 
   f32x4 O[RB][DT];
   RowState rs[RB];
-#pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    rs[b].m = -__builtin_inff();
-    rs[b].l = 0.0f;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) O[b][d] = f32x4{0, 0, 0, 0};
-  }
-
   const int64_t hoff = static_cast<int64_t>(kvh) * a.head_stride;
   const int vec = tid % kPerRow, srow = tid / kPerRow;
-  // row_off: cache row of the lane's token.  Tokens that no row may see are read
-  // from row 0: their weights are zero.
+  const char* const kbase = a.k + (hoff + vec * kVec) * static_cast<int64_t>(sizeof(elem));
+  const char* const vbase = a.v + (hoff + vec * kVec) * static_cast<int64_t>(sizeof(elem));
+  // Tokens that no row may see are read from row 0: their weights are zero.
   u32x4 kr[kPasses], vr[kPasses];
-  auto fetch = [&](int64_t row_off) {
+  auto fetch = [&](int slot) {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const int64_t at = (shfl64(row_off, srow + i * kRowsPass) + hoff + vec * kVec) * static_cast<int64_t>(sizeof(elem));
-      kr[i] = ld<false, u32x4>(a.k + at);
-      vr[i] = ld<false, u32x4>(a.v + at);
+      const int64_t at = rows_at[slot][srow + i * kRowsPass] * static_cast<int64_t>(sizeof(elem));
+      kr[i] = ld<false, u32x4>(kbase + at);
+      vr[i] = ld<false, u32x4>(vbase + at);
     }
   };
-  // V goes to LDS with zeros for infinite and NaN elements (0 times them is not
-  // 0); a second pass gives them to the rows that see them.
+  // An infinite or NaN element of V would reach rows that may not see it (0 times it is
+  // not 0).  The tiles run as if there were none; when an output came out infinite or NaN they
+  // run once more with zeros for such elements, and a last pass gives them to the rows that
+  // see them.
+  bool clean = false;
   auto put = [&](int buf) {
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) any |= nonfinite16<IT>(vr[i]);
-    any = __ballot(any) != 0;
-    if (__builtin_expect(any, 0)) {
+    if (__builtin_expect(clean, 0)) {
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) vr[i] = finite16<IT>(vr[i]);
-      odd = 1;
     }
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
@@ -317,18 +310,18 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
       *reinterpret_cast<u32x4*>(&lds[buf][1][at]) = vr[i];
     }
   };
-  if (tid == 0) odd = 0;
-  __syncthreads();
-  // Loads complete in order, so the table entries of a tile are requested before
-  // the previous tile's keys and first looked at a tile later.
+  // The page table is read by one wavefront a tile, in turn, two tiles ahead: `entry` is requested
+  // a tile before page_rows turns it into cache rows (loads complete in order, so it must not
+  // be looked at while keys that were requested before it are in flight).
   int entry = 0;
-  bool ok = false;
-  if (v0 < v1) {
-    const int64_t off = cache_row(a, s, key_tile(kt, v0) * T + lane, kt.limit, ok);
-    if (v0 + 1 < v1) entry = page_entry(a, s, key_tile(kt, v0 + 1) * T + lane);
-    fetch(off);
-    put(0);
-  }
+  auto page_rows = [&](int v) {
+    bool ok;
+    const int64_t row = page_row(a, entry, key_tile(kt, v) * T + lane, kt.limit, ok);
+    rows_at[(v - v0) & 3][lane] = row;
+    const uint64_t bits = __ballot(ok);
+    if (lane == 0) on_pages[(v - v0) & 3] = bits;
+  };
+  auto turn = [&](int v) { return ((v - v0) & 3) == wave && v < v1; };
   f32x4 S[RB][JT];
   bool work = false;
   uint64_t on_page = 0;
@@ -398,24 +391,49 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
       }
     }
   };
-  // tile v + 1 into registers, the table entries of v + 2
-  auto ahead = [&](int v) {
-    on_page = __ballot(ok);
-    if (v + 1 < v1) {
-      const int64_t off = page_row(a, entry, key_tile(kt, v + 1) * T + lane, kt.limit, ok);
-      if (v + 2 < v1) entry = page_entry(a, s, key_tile(kt, v + 2) * T + lane);
-      fetch(off);
+  if (tid == 0) odd = 0;
+  for (;;) {
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      rs[b].m = -__builtin_inff();
+      rs[b].l = 0.0f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) O[b][d] = f32x4{0, 0, 0, 0};
     }
-  };
-  __syncthreads();
-  for (int v = v0; v < v1; ++v) {
-    ahead(v);
-    scores(v);
-    outputs(v);
-    if (v + 1 < v1) put((v + 1 - v0) & 1);
+    for (int v = v0; v < v0 + 3; ++v)
+      if (turn(v)) entry = page_entry(a, s, key_tile(kt, v) * T + lane);
+    if (turn(v0)) page_rows(v0);
+    if (turn(v0 + 1)) page_rows(v0 + 1);
     __syncthreads();
+    if (v0 < v1) {
+      fetch(0);
+      put(0);
+    }
+    __syncthreads();
+    for (int v = v0; v < v1; ++v) {
+      const uint64_t bits = on_pages[(v - v0) & 3];
+      on_page = (static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(bits >> 32)))) << 32) |
+                static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(bits)));
+      if (turn(v + 3)) entry = page_entry(a, s, key_tile(kt, v + 3) * T + lane);
+      if (v + 1 < v1) fetch((v + 1 - v0) & 3);
+      scores(v);
+      outputs(v);
+      if (v + 1 < v1) put((v + 1 - v0) & 1);
+      if (turn(v + 2)) page_rows(v + 2);   // over tile v - 2's, which no wavefront reads any more
+      __syncthreads();
+    }
+    if (clean) break;
+    float any = 0.0f;
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int d = 0; d < DT; ++d) any += (O[b][d][0] + O[b][d][1]) + (O[b][d][2] + O[b][d][3]);
+    if (__ballot(!(fabsf(any) < __builtin_inff())) != 0) odd = 1;
+    __syncthreads();
+    if (__builtin_expect(odd == 0, 1)) break;
+    clean = true;
   }
-  if (__builtin_expect(odd, 0)) {
+  if (__builtin_expect(clean, 0)) {
     // rare: the tiles once more from the cache, for the infinities and NaN among the values of
     // tokens that a row sees (its weight is not zero)
 #pragma unroll 1
