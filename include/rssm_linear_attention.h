@@ -110,13 +110,13 @@ typedef struct {
 rssm_status rssm_linear_attention_workspace(const rssm_linear_attention_desc *desc, int64_t *bytes);
 
 /* Enqueue the prompt form on `hip_stream`.  Arithmetic: chunks of 64 tokens
- * on the matrix cores; logarithms of decays are summed in fp64 inside a chunk,
- * the state and every sum are held in fp32, and the new state carries at least
- * 22 bits of each product.  16-bit inputs: for y, the decay-weighted scores and
- * the chunk's starting state are rounded once to the input dtype before their
- * products (fp16 with a power-of-two scale, so nothing overflows or
- * underflows).  Token t's output depends on tokens up to t only, non-finite
- * inputs included. */
+ * on the matrix cores; the state and every sum are held in fp32.  The products
+ * of the state update carry at least 22 bits for an fp32 state and 16 for a
+ * 16-bit one.  16-bit inputs: for y, the decay-weighted scores and the chunk's
+ * starting state are rounded once to the input dtype before their products (fp16
+ * with a power-of-two scale, so nothing overflows or underflows).  Token t's
+ * output depends on tokens up to t only, non-finite inputs included; a dt_raw of
+ * -infinity under softplus skips its token. */
 rssm_status rssm_linear_attention(const rssm_linear_attention_desc *desc, const rssm_linear_attention_tables *tables,
                                   void *hip_stream);
 

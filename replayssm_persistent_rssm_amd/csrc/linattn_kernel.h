@@ -17,16 +17,23 @@
 //                                          input type (fp16: scaled by a power of two)
 // Wavefront w owns tokens 16w .. 16w+15 of y and state rows 16w .. 16w+15 of the
 // update.  The next chunk's inputs are loaded into registers while the current
-// one is computed.
+// one is computed.  A chunk of 64 keeps two workgroups a compute unit (54 KiB of LDS
+// and 199 registers for bf16); a third (168 registers) ran no faster.
 //
 // When sequences x heads are too few to fill the chip, the token axis is split into
 // stretches: one launch folds each stretch from a zero state (kStateOnly), a second scans the
 // stretches' states and decays, a third computes the outputs from the
 // scanned starting states.
+//
+// Bound by the vector ALUs and LDS together.  12 ragged prompts, 13,640 tokens, 256 heads in 8
+// groups, gated, fp32 state: 0.58 ms, 2.7 TB/s of the bytes it cannot do without (0.60 ms with z and
+// y in 8-byte pieces).  Of that, the gate takes 13%, three quarters of the score and
+// starting-state products 13%, two of the three parts of the state update 6% (each timed by leaving it
+// out).  One prompt of 16,384 tokens, 64 heads, bf16 state, in 8 stretches: 0.22 ms, a quarter of it the
+// fold.
 #pragma once
 
 #include "mma_device.h"
-#include "ssu_kernel.h"
 
 namespace rssm {
 
@@ -50,6 +57,10 @@ struct LinArgs {
   int32_t num_seqs, num_tokens, H, hpg, dim, num_slots, pad, max_seq_len, dt_softplus;
   int32_t nseg, seg_len;  // stretches of the token axis and their length (a multiple of 64)
 };
+
+// State row of row m of D tile p of y^T: the four rows that a lane group holds of tiles 2k and
+// 2k + 1 are 8 consecutive ones, 16 bytes of z and y.
+__device__ __forceinline__ constexpr int row_of(int p, int m) { return 32 * (p >> 1) + 4 * (p & 1) + 8 * (m >> 2) + (m & 3); }
 
 constexpr int kLinQ = 64;       // tokens a chunk
 constexpr int kLinP = 64;       // state rows a workgroup
@@ -86,12 +97,12 @@ __device__ __forceinline__ void store_state4(char* p, f32x4 v) {
 __device__ __forceinline__ float pow2i(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
 
 // Exponent k such that 2^k brings a magnitude m (finite, >= 0) to about
-// 2^12; 0 for m = 0 or non-finite m.  Within +-60 so that 2^k times the fp32 sums stays finite.
+// 2^12; 0 for m = 0 or non-finite m.  At most 60, so that 2^k times fp32 sums stays finite.
 __device__ __forceinline__ int scale_exp(float m) {
   const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
   if (!(m > 0.0f) || e == 128) return 0;
   const int k = 12 - e;
-  return k > 60 ? 60 : (k < -60 ? -60 : k);
+  return k > 60 ? 60 : (k < -110 ? -110 : k);
 }
 
 template <int IT, int N>
@@ -160,7 +171,8 @@ __device__ __forceinline__ float prompt_dt(float raw, float bias, int softplus) 
   const float v = raw + bias;
   if (!softplus) return v;
   const float bb = v - raw;
-  const float lo = (raw - (v - bb)) + (bias - bb);
+  // (an infinite v has no rounding error: softplus is 0 or infinity)
+  const float lo = fabsf(v) < __builtin_inff() ? (raw - (v - bb)) + (bias - bb) : 0.0f;
   const float t0 = exp_near(-fabsf(v));
   const float t = fmaf(t0, v > 0.0f ? -lo : lo, t0);
   const float d = 2.0f + t;
@@ -265,7 +277,7 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
   char* py = a.y + (first * a.y_stride + hx) * es;
   xr.init(xb, tid);
   br.init(Bb, tid);
-  const uint32_t c_at = (16 * wrow + li) * cb + 8 * g * es, z_at = (16 * wrow + li) * zb + 4 * g * es;
+  const uint32_t c_at = (16 * wrow + li) * cb + 8 * g * es, z_at = (16 * wrow + li) * zb + 8 * g * es;
   auto fetch = [&](int t) {
     const int rows = t1 - t < kLinQ ? t1 - t : kLinQ;
     xr.load(px, xb, rows);
@@ -377,20 +389,14 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
 
     if constexpr (!kStateOnly) {
       const int i = 16 * wrow + li;
-      u32x4 zr[4];
       const bool has_z = a.z != nullptr;
+      u32x4 zw[IT == kF32 ? 4 : 2];
       if (has_z) {
         const rsrc_t rz = make_rsrc(pz, (rows - 1) * zb + kLinP * es);
         pz += static_cast<int64_t>(kLinQ) * zb;
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          if constexpr (IT == kF32) {
-            zr[p] = bload16<false>(rz, z_at + 16 * p * es, 0);
-          } else {
-            const auto w = __builtin_amdgcn_raw_buffer_load_b64(rz, z_at + 16 * p * es, 0, 0);
-            zr[p] = u32x4{w[0], w[1], 0, 0};
-          }
-        }
+        for (int k = 0; k < (IT == kF32 ? 4 : 2); ++k)
+          zw[k] = bload16<false>(rz, z_at + (IT == kF32 ? row_of(k, 0) : 32 * k) * es, 0);
       }
       // masked, decay-weighted scores M^T[j][i], j = 16 jt + 4g + r
       f32x4 M[4], Y[4];
@@ -399,7 +405,7 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
       // next tile's fragments are read while the matrix cores take the current ones
       frag f[2][KS];
       auto read = [&](int u, frag (&to)[KS]) {
-        const elem* src = u < 4 ? L.Bs + (16 * u + li) * LinLds<IT, N>::kN : L.Ss + (16 * (u - 4) + li) * LinLds<IT, N>::kS;
+        const elem* src = u < 4 ? L.Bs + (16 * u + li) * LinLds<IT, N>::kN : L.Ss + row_of(u - 4, li) * LinLds<IT, N>::kS;
 #pragma unroll
         for (int k = 0; k < KS; ++k) to[k] = frag_row<IT>(src + 32 * k + 8 * g);
       };
@@ -452,36 +458,44 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
       const frag m0 = to_frag<IT>(stack(M[0], M[1])), m1 = to_frag<IT>(stack(M[2], M[3]));
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        X[p] = mma<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 0, 16 * p, lane), m0, f32x4{0, 0, 0, 0});
-        X[p] = mma<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 32, 16 * p, lane), m1, X[p]);
+        X[p] = mma<IT>(frag_col<IT, 8>(L.Xs, LinLds<IT, N>::kP, 0, row_of(p, 0), lane), m0, f32x4{0, 0, 0, 0});
+        X[p] = mma<IT>(frag_col<IT, 8>(L.Xs, LinLds<IT, N>::kP, 32, row_of(p, 0), lane), m1, X[p]);
       }
       const f32x4 xs = (X[0] + X[1]) + (X[2] + X[3]);
       if (__builtin_expect(__ballot(!(fabsf((xs[0] + xs[1]) + (xs[2] + xs[3])) < __builtin_inff())) != 0, 0)) {
         // a non-finite x may have met the zero weight of a later token
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          X[p] = mma_seen<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 0, 16 * p, lane), m0, f32x4{0, 0, 0, 0});
-          X[p] = mma_seen<IT>(frag_col<IT>(L.Xs, LinLds<IT, N>::kP, 32, 16 * p, lane), m1, X[p]);
+          X[p] = mma_seen<IT>(frag_col<IT, 8>(L.Xs, LinLds<IT, N>::kP, 0, row_of(p, 0), lane), m0, f32x4{0, 0, 0, 0});
+          X[p] = mma_seen<IT>(frag_col<IT, 8>(L.Xs, LinLds<IT, N>::kP, 32, row_of(p, 0), lane), m1, X[p]);
         }
       }
-      elem* yp = reinterpret_cast<elem*>(py + i * yb) + 4 * g;
+      elem* yp = reinterpret_cast<elem*>(py + i * yb) + 8 * g;
       py += static_cast<int64_t>(kLinQ) * yb;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        if constexpr (IT == kF16) Y[p] *= *reinterpret_cast<const f32x4*>(L.sinv + 16 * p + 4 * g);
-        Y[p] = Y[p] * ei + X[p] * mi + widen4<IT>(L.Xs + i * LinLds<IT, N>::kP + 16 * p + 4 * g) * Dh;
+        if constexpr (IT == kF16) Y[p] *= *reinterpret_cast<const f32x4*>(L.sinv + row_of(p, 4 * g));
+        Y[p] = Y[p] * ei + X[p] * mi;
       }
-      if (has_z) {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const f32x4 zi = widen4_raw<IT>(zr[p]);
+      for (int k = 0; k < 2; ++k) {
+        const f32x8 xi = from_frag<IT>(frag_row<IT>(L.Xs + i * LinLds<IT, N>::kP + 32 * k + 8 * g));
+        f32x8 v = stack(Y[2 * k], Y[2 * k + 1]) + xi * Dh;
+        if (has_z) {
+          f32x8 zi;
+          if constexpr (IT == kF32) zi = __builtin_bit_cast(f32x8, u32x8{zw[2 * k].x, zw[2 * k].y, zw[2 * k].z, zw[2 * k].w, zw[2 * k + 1].x, zw[2 * k + 1].y, zw[2 * k + 1].z, zw[2 * k + 1].w});
+          else zi = from_frag<IT>(__builtin_bit_cast(frag, zw[k]));
 #pragma unroll
-          for (int r = 0; r < 4; ++r) Y[p][r] *= silu(zi[r]);
+          for (int e = 0; e < 8; ++e) v[e] *= silu(zi[e]);
         }
-      }
-      if (i < rows) {
-#pragma unroll
-        for (int p = 0; p < 4; ++p) narrow4<IT>(yp + 16 * p, Y[p]);
+        if (i < rows) {
+          if constexpr (IT == kF32) {
+            *reinterpret_cast<f32x4*>(yp + 32 * k) = f32x4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<f32x4*>(yp + 32 * k + 4) = f32x4{v[4], v[5], v[6], v[7]};
+          } else {
+            *reinterpret_cast<u32x4*>(yp + 32 * k) = __builtin_bit_cast(u32x4, to_frag<IT>(v));
+          }
+        }
       }
     }
 
@@ -590,9 +604,11 @@ __global__ __launch_bounds__(kLinBlock) void linattn_scan_kernel(LinArgs a, int 
 }
 
 // Single-token form: one workgroup a (request, head, 64 state rows), 16 rows a
-// wavefront.  The state streams through registers once (16-byte loads and
+// wavefront.  The state streams through registers once (16-byte non-temporal loads and
 // stores, all of a wavefront's rows in flight); each lane folds its columns
-// and the row's readout is summed over the lanes that share it.
+// and the row's readout is summed over the lanes that share it.  Bound by memory:
+// 256 requests of 256 heads of 64 x 128 bf16 in 0.365 ms, 5.95 TB/s read and written; one
+// request 4.4 us, most of it the launch.
 template <int IT, int ST, int N>
 __global__ __launch_bounds__(kLinBlock) void linattn_step_kernel(LinArgs a) {
   typedef typename Mma<IT>::elem elem;
@@ -623,7 +639,7 @@ __global__ __launch_bounds__(kLinBlock) void linattn_step_kernel(LinArgs a) {
   }
   float dt = 1.0f;
   if (a.dt != nullptr)
-    dt = new_token_dt(sload(a.dt + b * a.dt_stride + h), a.dt_bias != nullptr ? sload(a.dt_bias + h) : 0.0f, a.dt_softplus);
+    dt = prompt_dt(sload(a.dt + b * a.dt_stride + h), a.dt_bias != nullptr ? sload(a.dt_bias + h) : 0.0f, a.dt_softplus);
   const float decay = expf(dt * sload(a.A + h));
   const float Dh = a.D != nullptr ? sload(a.D + h) : 0.0f;
   const int64_t hx = static_cast<int64_t>(h) * a.dim + row0 + rr;

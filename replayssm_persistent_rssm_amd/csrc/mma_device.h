@@ -104,12 +104,13 @@ constexpr int tile_pitch(int cols) {
 // c0 + l % 16 of rows r0 + {4g .. 4g+3} and r0 + 16 + {4g .. 4g+3}.  16-bit: the
 // transposing read hands each lane of a 16-lane group one column of the 4x16 block
 // whose row q, columns 4k .. 4k+3 lane 4q + k addresses.
-template <int IT>
+// kStep: distance between the lanes' groups of 4 columns (4: consecutive columns).
+template <int IT, int kStep = 4>
 __device__ __forceinline__ typename Mma<IT>::frag frag_col(const typename Mma<IT>::elem* tile, int stride, int r0,
                                                            int c0, int lane) {
   const int g = lane >> 4, i = lane & 15;
   if constexpr (IT == kF32) {
-    const float* p = tile + (r0 + 4 * g) * stride + c0 + i;
+    const float* p = tile + (r0 + 4 * g) * stride + c0 + kStep * (i >> 2) + (i & 3);
     f32x8 v;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -119,7 +120,7 @@ __device__ __forceinline__ typename Mma<IT>::frag frag_col(const typename Mma<IT
     return v;
   } else {
     typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
-    const uint16_t* p = tile + (r0 + 4 * g + (i >> 2)) * stride + c0 + (i & 3) * 4;
+    const uint16_t* p = tile + (r0 + 4 * g + (i >> 2)) * stride + c0 + (i & 3) * kStep;
     const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p));
     const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 16 * stride));
     const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
@@ -193,18 +194,6 @@ __device__ __forceinline__ f32x4 widen4(const typename Mma<IT>::elem* p) {
                    f16_bits_to_float(w.y >> 16)};
     }
   }
-}
-
-// The same from raw storage in registers (16-bit types: the first two words).
-template <int IT>
-__device__ __forceinline__ f32x4 widen4_raw(u32x4 w) {
-  if constexpr (IT == kF32) return __builtin_bit_cast(f32x4, w);
-  else if constexpr (IT == kBF16)
-    return f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                 __uint_as_float(w.y & 0xffff0000u)};
-  else
-    return f32x4{f16_bits_to_float(w.x & 0xffffu), f16_bits_to_float(w.x >> 16), f16_bits_to_float(w.y & 0xffffu),
-                 f16_bits_to_float(w.y >> 16)};
 }
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));

@@ -104,7 +104,9 @@ struct Split { int nseg, seg_len; };
 
 // Stretches of the token axis.  Every stretch but the last is folded twice (its
 // state, then its outputs), so the axis is split only when the (sequence, head)
-// tiles leave compute units idle.
+// tiles leave compute units idle: fewer than two workgroups for each of 256 of them.  Then
+// as many stretches as fill that (one prompt of 16,384 tokens and 64 heads: 226 us with 8
+// stretches, 229 with 16, 241 with 24), each of at least four chunks.
 Split split_of(const rssm_linear_attention_desc* d) {
   const int64_t items = static_cast<int64_t>(d->num_seqs) * d->num_heads * (d->dim / kLinP);
   const int64_t chunks = (static_cast<int64_t>(d->max_seq_len) + kLinQ - 1) / kLinQ;

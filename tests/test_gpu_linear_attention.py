@@ -166,6 +166,19 @@ def test_nonfinite_token_stays_causal(rp, it, where, value):
     ref.check(y[rows], ey[rows], ref.y_bound(ey, ym, y.dtype)[rows], "y")
 
 
+@pytest.mark.parametrize("it", ["bf16", "f16", "f32"])
+def test_dt_of_minus_infinity_skips_a_token(rp, it):
+    """softplus(-inf) = 0: the state passes the token unchanged, in both forms."""
+    p = make([70, 1], H=4, hpg=2, it=it, st="f32", seed=16)
+    p["dt"][5], p["dt"][40], p["dt"][70] = -math.inf, -math.inf, -math.inf
+    check_prompt(rp, p)
+    q = make([1, 1], H=4, hpg=2, it=it, st="f32", seed=17)
+    q["dt"][1] = -math.inf
+    _, state = run_step(rp, q)
+    s = int(q["slots"][1])
+    assert torch.equal(state[s].cpu(), q["state"][s])
+
+
 def test_pad_and_guarded_slots(rp):
     p = make([20, 30, 40], H=4, hpg=2, it="bf16", st="f32", seed=13)
     p["slots"] = torch.tensor([-1, 3, 1000], dtype=torch.int32)
