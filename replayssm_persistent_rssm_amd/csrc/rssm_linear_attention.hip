@@ -106,13 +106,15 @@ struct Split { int nseg, seg_len; };
 // state, then its outputs), so the axis is split only when the (sequence, head)
 // tiles leave compute units idle: fewer than two workgroups for each of 256 of them.  Then
 // as many stretches as fill that (one prompt of 16,384 tokens and 64 heads: 226 us with 8
-// stretches, 229 with 16, 241 with 24), each of at least four chunks.
+// stretches, 229 with 16, 241 with 24), at most one a chunk (7 prompts up to 605 tokens of 2 heads:
+// 18.5 us, 32.9 with four chunks a stretch) and 64, because the scan is serial (one prompt of
+// 16,384 tokens and one head: 34.5 us with 64, 51.5 with 256).
 Split split_of(const rssm_linear_attention_desc* d) {
   const int64_t items = static_cast<int64_t>(d->num_seqs) * d->num_heads * (d->dim / kLinP);
   const int64_t chunks = (static_cast<int64_t>(d->max_seq_len) + kLinQ - 1) / kLinQ;
-  constexpr int64_t kFill = 512;
-  if (items == 0 || items >= kFill || chunks < 8) return {1, static_cast<int>(std::max<int64_t>(chunks, 1) * kLinQ)};
-  const int64_t want = std::min((kFill + items - 1) / items, chunks / 4);
+  constexpr int64_t kFill = 512, kMaxStretches = 64;
+  if (items == 0 || items >= kFill || chunks < 3) return {1, static_cast<int>(std::max<int64_t>(chunks, 1) * kLinQ)};
+  const int64_t want = std::min(std::min((kFill + items - 1) / items, chunks), kMaxStretches);
   if (want <= 1) return {1, static_cast<int>(chunks * kLinQ)};
   const int64_t per = (chunks + want - 1) / want;
   return {static_cast<int>((chunks + per - 1) / per), static_cast<int>(per * kLinQ)};
