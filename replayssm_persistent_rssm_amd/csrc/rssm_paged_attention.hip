@@ -96,7 +96,9 @@ struct Plan {
 };
 
 // The split of the key axis.  Row tiles: none when they give every compute unit a
-// workgroup, otherwise enough for two each, of at least 4 tiles of keys.  Single tokens: up to 4,096
+// workgroup, otherwise as many as fit two each in one round (2,000 new tokens over 40,000, 4 heads of
+// 128: 235 us with 504 workgroups, 303 with 567), of at least 2 tiles of keys (3 times 5 new tokens over 4,000, 16 heads of
+// 64: 15.3 us, 19.5 with 4).  Single tokens: up to 4,096
 // workgroups, because ragged lengths leave many of them without work (64 requests of
 // 1 to 8,192 tokens: 296 us with 1,024, 290 with 2,048, 250 with 4,096 or 8,192), each of at
 // least 8 tiles (short caches) to 32 (long ones, where joining costs more: one request of
@@ -115,11 +117,11 @@ Plan plan_of(const rssm_paged_attention_desc* d) {
   }
   const int64_t items = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * p.row_tiles;
   const int64_t kFill = p.rows16 ? 4096 : 512;
-  const int64_t kLeast = p.rows16 ? std::min<int64_t>(32, std::max<int64_t>(8, tiles / 32)) : 4;
+  const int64_t kLeast = p.rows16 ? std::min<int64_t>(32, std::max<int64_t>(8, tiles / 32)) : 2;
   p.nsplit = 1;
   p.split_tiles = 1 << 30;
   if (items > 0 && items <= (p.rows16 ? kFill : kFill / 2) && tiles >= 2 * kLeast) {
-    const int64_t want = (kFill + items - 1) / items;
+    const int64_t want = p.rows16 ? (kFill + items - 1) / items : kFill / items;
     const int64_t per = std::max(kLeast, (tiles + want - 1) / want);
     const int64_t n = (tiles + per - 1) / per;
     if (n > 1) {
