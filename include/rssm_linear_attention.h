@@ -35,8 +35,8 @@ extern "C" {
  *   dstate             64 or 128 (columns)
  *   num_slots          slots of the state pool >= 1
  *   pad_slot_id        slot sentinel to skip (state and y rows left untouched)
- *   max_seq_len        longest sequence of the call >= 0 (prompt form; longer
- *                      ones are cut to it)
+ *   max_seq_len        longest sequence of the call, in [0, 2^30] (prompt form;
+ *                      longer ones are cut to it)
  *   state_dtype        RSSM_F32 | RSSM_BF16 | RSSM_F16
  *   input_dtype        x, B, C, z and y: RSSM_F32 | RSSM_BF16 | RSSM_F16
  *   dt_softplus        1: dt = softplus(dt_raw + bias); 0: dt = dt_raw + bias

@@ -681,6 +681,7 @@ def _linear_marshal(state, A, x, B, C, dt, y, slots, seq_start=None, max_seq_len
             slot_stride = state.stride(0)
     f32, i32, idt = torch.float32, torch.int32, x.dtype
     R = slots.shape[0]
+    max_seq_len, pad_slot_id = int(max_seq_len), int(pad_slot_id)
     row, brow = H * dim, G * dstate
     shape, bshape = (N, H, dim), (N, G, dstate)
     xp, xs = _rows(x, "x", idt, shape, row, dev)
@@ -890,7 +891,7 @@ def rssm_block_norm(y, residual, residual_out, normed=None, *, z=None, post_weig
     zp, zs = _rows(z, "z", idt, shape, C, dev) if z is not None else (None, ys)
     np_, ns = _rows(normed, "normed", idt, shape, C, dev) if normed is not None else (None, ys)
     desc = RssmNormDesc(_scalar("rows", R), _scalar("channels", C), _scalar("groups", groups), _code(idt), _code(rdt),
-                        eps, residual_scale, ys, zs, rs, os_, ns)
+                        float(eps), float(residual_scale), ys, zs, rs, os_, ns)
     tab = RssmNormTables(yp, zp, rp, _vec(post_weight, "post_weight", f32, C, dev),
                          _vec(pre_weight, "pre_weight", f32, C, dev),
                          _vec(channel_scale, "channel_scale", f32, C, dev), op, np_)

@@ -40,7 +40,8 @@ rssm_status check_desc(const rssm_linear_attention_desc* d, bool step) {
     return fail(RSSM_ERR_INVALID_ARGUMENT, "heads_per_group (%d) must be >= 1 and divide num_heads (%d)",
                 d->heads_per_group, d->num_heads);
   if (d->num_slots < 1) return fail(RSSM_ERR_INVALID_ARGUMENT, "num_slots must be >= 1 (got %d)", d->num_slots);
-  if (d->max_seq_len < 0) return fail(RSSM_ERR_INVALID_ARGUMENT, "max_seq_len must be >= 0 (got %d)", d->max_seq_len);
+  if (d->max_seq_len < 0 || d->max_seq_len > (1 << 30))
+    return fail(RSSM_ERR_INVALID_ARGUMENT, "max_seq_len must be in [0, 2^30] (got %d)", d->max_seq_len);
   if (d->dt_softplus != 0 && d->dt_softplus != 1)
     return fail(RSSM_ERR_INVALID_ARGUMENT, "dt_softplus must be 0 or 1 (got %d)", d->dt_softplus);
   for (int dt : {d->state_dtype, d->input_dtype})
@@ -104,8 +105,9 @@ struct Split { int nseg, seg_len; };
 
 // Stretches of the token axis.  Every stretch but the last is folded twice (its
 // state, then its outputs), so the axis is split only when the (sequence, head)
-// tiles leave compute units idle: fewer than two workgroups for each of 256 of them.  Then
-// as many stretches as fill that (one prompt of 16,384 tokens and 64 heads: 226 us with 8
+// tiles leave compute units without a workgroup (5 prompts of 1,500 tokens, 64 heads, 320 tiles: 104 us
+// whole, 130 in two stretches).  Then as many stretches as give each two (8 ragged prompts up to
+// 2,500, 24 heads: 89 us with three, 116 with two; one prompt of 16,384 tokens and 64 heads: 226 us with 8
 // stretches, 229 with 16, 241 with 24), at most one a chunk (7 prompts up to 605 tokens of 2 heads:
 // 18.5 us, 32.9 with four chunks a stretch) and 64, because the scan is serial (one prompt of
 // 16,384 tokens and one head: 34.5 us with 64, 51.5 with 256).
@@ -113,7 +115,7 @@ Split split_of(const rssm_linear_attention_desc* d) {
   const int64_t items = static_cast<int64_t>(d->num_seqs) * d->num_heads * (d->dim / kLinP);
   const int64_t chunks = (static_cast<int64_t>(d->max_seq_len) + kLinQ - 1) / kLinQ;
   constexpr int64_t kFill = 512, kMaxStretches = 64;
-  if (items == 0 || items >= kFill || chunks < 3) return {1, static_cast<int>(std::max<int64_t>(chunks, 1) * kLinQ)};
+  if (items == 0 || items > kFill / 2 || chunks < 3) return {1, static_cast<int>(std::max<int64_t>(chunks, 1) * kLinQ)};
   const int64_t want = std::min(std::min((kFill + items - 1) / items, chunks), kMaxStretches);
   if (want <= 1) return {1, static_cast<int>(chunks * kLinQ)};
   const int64_t per = (chunks + want - 1) / want;

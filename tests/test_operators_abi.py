@@ -32,7 +32,7 @@ def lin_desc(rp, **kw):
 
 BAD_LINEAR = [
     (dict(num_seqs=-1), 1, "num_seqs"), (dict(num_tokens=-1), 1, "num_tokens"), (dict(num_heads=0), 1, "num_heads"),
-    (dict(heads_per_group=7), 1, "divide"), (dict(num_slots=0), 1, "num_slots"), (dict(max_seq_len=-1), 1, "max_seq_len"),
+    (dict(heads_per_group=7), 1, "divide"), (dict(num_slots=0), 1, "num_slots"), (dict(max_seq_len=-1), 1, "max_seq_len"), (dict(max_seq_len=2 ** 30 + 1), 1, "max_seq_len"),
     (dict(dt_softplus=2), 1, "dt_softplus"), (dict(state_dtype=9), 1, "dtype"), (dict(state_dtype=3), 2, "f32, bf16 or f16"),
     (dict(input_dtype=4), 2, "f32, bf16 or f16"), (dict(dim=32), 2, "dim=32"), (dict(dstate=256), 2, "dstate=256"),
     (dict(state_slot_stride=100), 1, "state_slot_stride"), (dict(state_slot_stride=64 * 64 * 128 + 2), 1, "16 bytes"),
