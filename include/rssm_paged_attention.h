@@ -12,7 +12,8 @@
  *     o = sum_j exp(scale q.k_j - m) v_j / sum_j exp(scale q.k_j - m)
  * over the visible tokens j <= p with (window == 0 or j > p - window or
  * j < sinks).  Tokens on a page outside [0, num_pages) are not visible.  A query that
- * sees nothing gets zeros (lse -infinity).
+ * sees nothing gets zeros (lse -infinity); one with a NaN among its visible scores gets NaN
+ * (lse too).
  *
  * Plain C types only.  Every pointer is DEVICE memory owned by the caller;
  * the library allocates nothing and never synchronises.

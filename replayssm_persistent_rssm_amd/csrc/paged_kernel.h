@@ -653,7 +653,8 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
 
 // Joins the splits of a (token, head), eight partial outputs in flight, lanes over
 // head_dim.  kShare: the workgroup's wavefronts share the splits of one row (many
-// splits); otherwise each takes a row of its own.
+// splits); otherwise each takes a row of its own.  Maxima leave NaN out, so the weight of a
+// split whose scores are all NaN is zero: its NaN reaches the row through the sum.
 template <int IT, int D, bool kShare>
 __global__ __launch_bounds__(kPagedBlock) void paged_join_kernel(PagedArgs a) {
   typedef typename Mma<IT>::elem elem;
@@ -691,12 +692,12 @@ __global__ __launch_bounds__(kPagedBlock) void paged_join_kernel(PagedArgs a) {
     for (int u = 0; u < U; ++u) {
       const int k = k0 + u < a.nsplit ? k0 + u : a.nsplit - 1;
       w[u] = k0 + u < a.nsplit ? __builtin_amdgcn_exp2f(ml[2 * k] - base) : 0.0f;
-      l = w[u] != 0.0f ? fmaf(ml[2 * k + 1], w[u], l) : l;
+      l = fmaf(ml[2 * k + 1], w[u], l);   // the sum of a split with a NaN score is NaN, whatever its weight
 #pragma unroll
       for (int e = 0; e < E; ++e) p[u][e] = po[static_cast<int64_t>(k) * D + e];
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)   // (an empty split wrote no output)
+    for (int u = 0; u < U; ++u)   // a weight of zero hides an infinity or NaN among the split's values
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = w[u] != 0.0f ? fmaf(p[u][e], w[u], o[e]) : o[e];
   }
