@@ -69,7 +69,7 @@ typedef struct {
 
 /* Device tensors (G = H / heads_per_group):
  *   state          [slots][H][dim][dstate] state dtype, read and written
- *   A              [H] fp32
+ *   A              [H] fp32 (-infinity: a head that keeps nothing; its dt must be above 0)
  *   D, dt_bias     [H] fp32 each, or NULL
  *   x, z, y        [num_tokens][H][dim] input dtype (z may be NULL)
  *   B, C           [num_tokens][G][dstate] input dtype

@@ -17,8 +17,8 @@
 //                                          input type (fp16: scaled by a power of two)
 // Wavefront w owns tokens 16w .. 16w+15 of y and state rows 16w .. 16w+15 of the
 // update.  The next chunk's inputs are loaded into registers while the current
-// one is computed.  A chunk of 64 keeps two workgroups a compute unit (54 KiB of LDS
-// and 199 registers for bf16); a third (168 registers) ran no faster.
+// one is computed.  A chunk of 64 keeps two workgroups a compute unit (57 KiB of LDS
+// and 201 registers for bf16); a third (168 registers) ran no faster.
 //
 // When sequences x heads are too few to fill the chip, the token axis is split into
 // stretches: one launch folds each stretch from a zero state (kStateOnly), a second scans the
@@ -119,6 +119,9 @@ struct LinLds {
   // earlier token up to the tile's start (both factors of exp(l_i - l_j) then shrink
   // where the decay does, and only the tile on the diagonal needs one exponential a pair)
   alignas(16) float lr[4][kLinQ], e[4][kLinQ], dt[4][kLinQ], w[4][kLinQ], before[4][3][kLinQ];
+  // for the diagonal, in log2 units: dt_i A, and its sum from the start of i's group of 4 tokens
+  // (k = 0), of the group before (1) and of the one before that (2) up to i
+  alignas(16) float da[4][kLinQ], since[4][3][kLinQ];
   // the whole chunk's decay and its logarithm
   float decay[4], total[4];
   alignas(16) float sinv[kLinP];   // fp16: inverse scale of each state row in Ss
@@ -196,6 +199,15 @@ __device__ __forceinline__ float row_shift(float v) {
   constexpr int ctrl = n > 0 ? 0x110 + n : 0x100 - n;   // row_shr : row_shl
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, true));
 }
+
+// Selections by masks in vector registers: the chunk kernel's scalar registers are all taken, and
+// further lane masks there would be spilled inside its loop.
+__device__ __forceinline__ int lane_mask(bool on) {
+  int m = on ? -1 : 0;
+  asm("" : "+v"(m));   // not folded back into a compare
+  return m;
+}
+__device__ __forceinline__ float and_bits(float v, int m) { return __int_as_float(__float_as_int(v) & m); }
 
 template <int IT, int ST, int N, bool kStateOnly>
 __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_kernel(LinArgs a) {
@@ -312,15 +324,19 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
     }
     return v;
   };
+  // all bits set where the token one (two) before the lane's is in its group of 4, and where the
+  // group of keys 4g .. 4g + 3 is an earlier one than the lane's token's
+  const int in_group1 = lane_mask((lane & 3) >= 1), in_group2 = lane_mask((lane & 3) >= 2), earlier = lane_mask(g < li >> 2);
   // Each wavefront turns one chunk's dt into its decays and weights.  Sums of dt A run
   // inside tiles of 16 tokens (lane rows), forwards and backwards, and the tiles' totals
-  // multiply as exponentials: every exponent is a sum of terms of one sign, with no
-  // cancellation however far the chunk decays.
+  // multiply as exponentials; inside a tile, the sums between two tokens are put together from
+  // groups of 4.  No exponent is a difference of sums: nothing cancels however far a token
+  // decays, and an infinite A leaves each token its own term.
   auto scan_dt = [&](int t, float raw) {
     const bool in = t + kLinQ * wave + lane < t1;
     float dtv = a.dt != nullptr ? prompt_dt(raw, bias, a.dt_softplus) : 1.0f;
     dtv = in ? dtv : 0.0f;
-    const float da = dtv * A;
+    const float da = in ? dtv * A : 0.0f;
     float f = da, r = da;   // inclusive sums up to, and from, the lane's token
     f += row_shift<1>(f);
     r += row_shift<-1>(r);
@@ -337,6 +353,15 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
       E[k] = exp_near(T[k]);
     }
     float e = exp_near(f), c = in ? exp_near(row_shift<-1>(r)) * dtv : 0.0f;
+    float b = da + and_bits(row_shift<1>(da), in_group1);
+    b += and_bits(row_shift<2>(b), in_group2);   // from the start of the lane's group of 4
+    const float T4 = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(b), 0xff, 0xf, 0xf, true));   // whole group
+    L.da[wave][lane] = da * 1.44269504f;
+    L.since[wave][0][lane] = b * 1.44269504f;
+    b += row_shift<4>(T4);
+    L.since[wave][1][lane] = b * 1.44269504f;
+    b += row_shift<8>(T4);
+    L.since[wave][2][lane] = b * 1.44269504f;
     L.lr[wave][lane] = f * 1.44269504f;
     L.dt[wave][lane] = dtv;
 #pragma unroll
@@ -401,6 +426,9 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
       // masked, decay-weighted scores M^T[j][i], j = 16 jt + 4g + r
       f32x4 M[4], Y[4];
       const float lri = L.lr[c4][i];
+      const float later = L.since[c4][g < li >> 2 ? (li >> 2) - 1 - g : 0][i];
+      const f32x4 a4 = *reinterpret_cast<const f32x4*>(L.da[c4] + 16 * wrow + 4 * g);
+      const f32x4 dj = *reinterpret_cast<const f32x4*>(L.dt[c4] + 16 * wrow + 4 * g);
       // scores (4 tiles of 16 tokens), then the starting state's part (4 tiles of 16 rows): the
       // next tile's fragments are read while the matrix cores take the current ones
       frag f[2][KS];
@@ -430,8 +458,12 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
         if (jt < wrow) {          // earlier tiles: every token is visible
           M[jt] *= *reinterpret_cast<const f32x4*>(L.before[c4][wrow - 1] + 16 * jt + 4 * g) * ai;
         } else if (jt == wrow) {  // the diagonal
-          const f32x4 d = lri - *reinterpret_cast<const f32x4*>(L.lr[c4] + 16 * jt + 4 * g);
-          const f32x4 dj = *reinterpret_cast<const f32x4*>(L.dt[c4] + 16 * jt + 4 * g);
+          // log decay from token j to token i > j: the tokens after j in j's group of 4 (j = 4g + r),
+          // and those of later groups up to i
+          f32x4 d;
+          d[3] = and_bits(later, earlier);
+#pragma unroll
+          for (int r = 2; r >= 0; --r) d[r] = d[r + 1] + (4 * g + r + 1 <= li ? a4[r + 1] : 0.0f);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float v = M[jt][r] * (__builtin_amdgcn_exp2f(d[r]) * dj[r]);

@@ -6,6 +6,8 @@ import pytest
 import torch
 
 import operators_ref as ref
+from test_gpu_linear_attention import check_prompt, run_step
+from test_gpu_linear_attention import make as linear
 from test_gpu_paged_attention import attend
 from test_gpu_paged_attention import make as paged
 
@@ -63,3 +65,39 @@ def test_nan_key_in_a_split_of_low_scores(rp, it, ql, kv):
     p["kc"][int(p["table"][0, 0]), 5, 0] = math.nan
     p["kc"][int(p["table"][0, 1000 // 48]), 1000 % 48, 0] = 50 * p["q"][0, 0]
     check_nonfinite(rp, p)
+
+
+def decays(it, st, A, seed, **kw):
+    """dt as given (no softplus), and nothing but the recurrence in y."""
+    p = linear(it=it, st=st, H=len(A), hpg=len(A), seed=seed, z=False, D=False, **kw)
+    p["A"], p["dt_bias"] = -torch.tensor(A), None
+    return p
+
+
+@pytest.mark.parametrize("it,far", [("f16", 100.0)] + [(it, far) for it in ("bf16", "f32") for far in (100.0, 1e4, 1e8, 1e30)])
+def test_small_decays_after_a_far_one(rp, it, far):
+    """One token whose decay forgets everything leaves the decays between later tokens as they are."""
+    p = decays(it, "f32", [16.0, 5000.0, 0.5], 40, lens=[100, 33])
+    p["dt"] = torch.tensor([0.01, 1e-4, 0.02]).expand(133, 3) * (0.5 + torch.rand(133, 1, generator=torch.Generator().manual_seed(1)))
+    for t in (0, 3, 31, 40, 41, 70, 102):
+        p["dt"][t], p["x"][t] = far, 0
+    check_prompt(rp, p, softplus=False)
+
+
+@pytest.mark.parametrize("it", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("lens", [[1, 70, 130], [1500]])
+@pytest.mark.parametrize("constant", [False, True])
+def test_heads_without_memory(rp, it, lens, constant):
+    """A of -infinity: the state is the last token's term alone, in prompts and in single tokens."""
+    p = decays(it, "f32", [math.inf, 1.0], 41, lens=lens, dt=not constant)
+    if not constant:
+        p["dt"] = 0.01 + 0.1 * torch.rand(p["dt"].shape, generator=torch.Generator().manual_seed(2))
+    check_prompt(rp, p, softplus=False)
+    q = decays(it, "f32", [math.inf, 1.0], 42, lens=[1, 1], dt=not constant)
+    if not constant:
+        q["dt"] = q["dt"].abs() + 0.01
+    y, state = run_step(rp, q, dt_softplus=False)
+    ey, ym, pool, pm = ref.linear_attention(q["state"], q["A"], q["x"], q["B"], q["C"], q["dt"], q["slots"], q["seqs"],
+                                            softplus=False)
+    ref.check(y, ey, ref.half_step(y.dtype) * ey.abs() + ref.FP32_CHAIN * ym + torch.finfo(y.dtype).tiny, "y")
+    ref.check(state, pool, ref.state_bound(pool, pm, state.dtype), "state")
