@@ -156,14 +156,19 @@ __device__ __forceinline__ f32x4 add_odd(f32x8 x, typename Mma<IT>::frag p, f32x
   return c;
 }
 
+// x with zeros for infinities and NaN.
+template <int IT>
+__device__ __forceinline__ typename Mma<IT>::frag finite_part(f32x8 x) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = fabsf(x[e]) < __builtin_inff() ? x[e] : 0.0f;
+  return to_frag<IT>(x);
+}
+
 // c + x p where x may hold infinities and NaN: the finite part by a product, the rest by add_odd.
 template <int IT>
 __device__ __forceinline__ f32x4 mma_seen(typename Mma<IT>::frag v, typename Mma<IT>::frag p, f32x4 c) {
   const f32x8 x = from_frag<IT>(v);
-  f32x8 fin;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) fin[e] = fabsf(x[e]) < __builtin_inff() ? x[e] : 0.0f;
-  return add_odd<IT>(x, p, mma<IT>(to_frag<IT>(fin), p, c));
+  return add_odd<IT>(x, p, mma<IT>(finite_part<IT>(x), p, c));
 }
 
 // Split fragment of two stacked D tiles.

@@ -606,12 +606,17 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
     // parts, so that only the output is rounded
     const f32x8 w = stack(S[0], S[1]);
     const frag P = to_frag<IT>(w);
+    frag P1;
+    if constexpr (IT != kF32) P1 = to_frag<IT>(w - from_frag<IT>(P));
     if (__builtin_expect(bad, 0)) {
+      // the same products over the finite values, so that one that no query sees changes no bit
 #pragma unroll
-      for (int d = 0; d < DT; ++d) O[d] = mma_seen<IT>(frag_col<IT>(Vt, kPitch, 0, 16 * d, lane), P, O[d]);
+      for (int d = 0; d < DT; ++d) {
+        const f32x8 x = from_frag<IT>(frag_col<IT>(Vt, kPitch, 0, 16 * d, lane));
+        if constexpr (IT != kF32) O[d] = mma<IT>(finite_part<IT>(x), P1, O[d]);
+        O[d] = add_odd<IT>(x, P, mma<IT>(finite_part<IT>(x), P, O[d]));
+      }
     } else {
-      frag P1;
-      if constexpr (IT != kF32) P1 = to_frag<IT>(w - from_frag<IT>(P));
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         const frag vf = frag_col<IT>(Vt, kPitch, 0, 16 * d, lane);

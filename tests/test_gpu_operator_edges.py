@@ -101,3 +101,25 @@ def test_heads_without_memory(rp, it, lens, constant):
                                             softplus=False)
     ref.check(y, ey, ref.half_step(y.dtype) * ey.abs() + ref.FP32_CHAIN * ym + torch.finfo(y.dtype).tiny, "y")
     ref.check(state, pool, ref.state_bound(pool, pm, state.dtype), "state")
+
+
+@pytest.mark.parametrize("it", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("ql", [1, 40])
+def test_masked_values_change_no_bit(rp, it, value, window, ql):
+    """Finite or not, a value that no query sees leaves every output as it is."""
+    lens = [150, 90, 3000]
+    p = paged(lens, [ql] * 3, 4, 2, 64, 16, it, seed=60)
+    spare = next(a for a in range(p["kc"].shape[0]) if a not in p["table"])
+    p["table"][p["table"] == 0] = spare                     # no sequence holds page 0,
+    p["table"][1, 2] = -1                                   # whose first row is read in place of what is off the cache
+    seen = {(int(p["table"][s, j // 16]), j % 16) for s, n in enumerate(lens) for j in range(n)
+            if int(p["table"][s, j // 16]) >= 0 and (window == 0 or j > n - ql - window)}
+    out, lse = attend(rp, p, window=window)
+    for a in range(p["kc"].shape[0]):
+        for b in range(16):
+            if (a, b) not in seen:
+                p["vc"][a, b] = value
+    again, lse2 = attend(rp, p, window=window)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
