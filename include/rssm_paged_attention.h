@@ -108,8 +108,10 @@ rssm_status rssm_paged_append(const rssm_paged_attention_desc *desc, const rssm_
 rssm_status rssm_paged_attention_workspace(const rssm_paged_attention_desc *desc, int64_t *bytes);
 
 /* Enqueue the attention on `hip_stream`.  Arithmetic: scores, maxima, sums and
- * outputs in fp32 on the matrix cores; 16-bit dtypes round the softmax
- * weights once to the input dtype for their product with V.  A value that a query may not
+ * outputs in fp32 on the matrix cores.  For their product with V, 16-bit dtypes round
+ * the softmax weights once to the input dtype when max_seq_len * (num_q_heads /
+ * num_kv_heads) > 16, and take them in two parts (16 bits and more) otherwise; fp16
+ * weights below 2^-21 of the row's largest are within 2^-32 of it.  A value that a query may not
  * see never reaches its output, non-finite values included. */
 rssm_status rssm_paged_attention(const rssm_paged_attention_desc *desc, const rssm_paged_attention_tables *tables,
                                  void *hip_stream);

@@ -176,9 +176,15 @@ struct RowState {
 
 // The reference point follows the maximum only when it lags by more than 2^8:
 // sums and products stay far from overflow, most tiles need no rescaling, and the exchange
-// between lanes is left to the tiles that do.
+// between lanes is left to the tiles that do.  fp16: the reference lies 2^7 below the maximum it was
+// taken from, so that weights reach up to 2^15 and one below 2^-25 of the largest, of which a
+// long cache may hold many, is not rounded to zero (2^-32 is; 2^-21 and more keep all their bits).
+template <int IT>
+constexpr float kBelow = IT == kF16 ? 7.0f : 0.0f;
+
+template <int IT>
 __device__ __forceinline__ bool lags(const PagedArgs& a, float mx, const RowState& st) {
-  return mx * a.scale_log2 > st.m + 8.0f;
+  return mx * a.scale_log2 > st.m + (kBelow<IT> + 8.0f);
 }
 
 __device__ __forceinline__ float max4(float m, f32x4 v) {
@@ -186,26 +192,27 @@ __device__ __forceinline__ float max4(float m, f32x4 v) {
 }
 
 // New reference point; the factor for the sum and the output so far.
-template <int JT>
+template <int IT, int JT>
 __device__ __forceinline__ float move_reference(const PagedArgs& a, const f32x4 (&S)[JT], RowState& st) {
   float mx = -__builtin_inff();
 #pragma unroll
   for (int jt = 0; jt < JT; ++jt) mx = max4(mx, S[jt]);
-  const float mn = fmaxf(st.m, max_groups(mx) * a.scale_log2);
+  const float mn = fmaxf(st.m, max_groups(mx) * a.scale_log2 - kBelow<IT>);
   const float alpha = mn == st.m ? 1.0f : __builtin_amdgcn_exp2f(st.m - mn);
   st.m = mn;
   st.l *= alpha;
   return alpha;
 }
 
-// exp2(c S - m) of one D tile, added to the lane's sum.  Nothing visible so far: m is
+// exp2(c S - m) of one D tile, added to `sum`, the lane's part of the key tile's sum (a running sum that
+// took them one by one would lose weights below its last place).  Nothing visible so far: m is
 // -infinity, and 0 in its place gives the weights exp2(-infinity) = 0.
-__device__ __forceinline__ f32x4 weights(const PagedArgs& a, f32x4 S, RowState& st) {
-  const float base = st.m == -__builtin_inff() ? 0.0f : st.m;
+__device__ __forceinline__ f32x4 weights(const PagedArgs& a, f32x4 S, float m, float& sum) {
+  const float base = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     S[r] = __builtin_amdgcn_exp2f(fmaf(S[r], a.scale_log2, -base));
-    st.l += S[r];
+    sum += S[r];
   }
   return S;
 }
@@ -371,12 +378,12 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
       float mx = -__builtin_inff();
 #pragma unroll
       for (int jt = 0; jt < JT; ++jt) mx = max4(mx, S[b][jt]);
-      move |= lags(a, mx, rs[b]);
+      move |= lags<IT>(a, mx, rs[b]);
     }
     if (__ballot(move) != 0) {
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
-        const float alpha = move_reference<JT>(a, S[b], rs[b]);
+        const float alpha = move_reference<IT, JT>(a, S[b], rs[b]);
 #pragma unroll
         for (int d = 0; d < DT; ++d) O[b][d] *= alpha;
       }
@@ -386,12 +393,15 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
   auto outputs = [&](int v) {
     if (!work) return;
     const elem* Vt = lds[(v - v0) & 1][1];
+    float sum[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) sum[b] = 0.0f;
 #pragma unroll
     for (int h = 0; h < JT / 2; ++h) {
       frag P[RB];
 #pragma unroll
       for (int b = 0; b < RB; ++b)
-        P[b] = to_frag<IT>(stack(weights(a, S[b][2 * h], rs[b]), weights(a, S[b][2 * h + 1], rs[b])));
+        P[b] = to_frag<IT>(stack(weights(a, S[b][2 * h], rs[b].m, sum[b]), weights(a, S[b][2 * h + 1], rs[b].m, sum[b])));
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         const frag vf = frag_col<IT>(Vt, kPitch, 32 * h, 16 * d, lane);
@@ -399,6 +409,8 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
         for (int b = 0; b < RB; ++b) O[b][d] = mma<IT>(vf, P[b], O[b][d]);
       }
     }
+#pragma unroll
+    for (int b = 0; b < RB; ++b) rs[b].l += sum[b];
   };
   if (tid == 0) odd = 0;
   for (;;) {
@@ -469,8 +481,8 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_tile_ke
             sc[u + 2] = sc[u];
           }
           mask_tile<JT>(a, sc, j0 + 32 * h, pos[b], bits >> (32 * h), g);
-          RowState t = rs[b];
-          P[b] = to_frag<IT>(stack(weights(a, sc[0], t), weights(a, sc[1], t)));
+          float unused = 0.0f;
+          P[b] = to_frag<IT>(stack(weights(a, sc[0], rs[b].m, unused), weights(a, sc[1], rs[b].m, unused)));
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
@@ -594,16 +606,19 @@ __global__ __launch_bounds__(kPagedBlock, IT == kF32 ? 1 : 2) void paged_row_ker
       fetch(off);
     }
     mask_tile<JT>(a, S, j0, pos, on_page, g);
-    if (__ballot(lags(a, max4(max4(-__builtin_inff(), S[0]), S[1]), rs)) != 0) {
-      const float alpha = move_reference<JT>(a, S, rs);
+    if (__ballot(lags<IT>(a, max4(max4(-__builtin_inff(), S[0]), S[1]), rs)) != 0) {
+      const float alpha = move_reference<IT, JT>(a, S, rs);
 #pragma unroll
       for (int d = 0; d < DT; ++d) O[d] *= alpha;
     }
-    S[0] = weights(a, S[0], rs);
-    S[1] = weights(a, S[1], rs);
+    float sum = 0.0f;
+    S[0] = weights(a, S[0], rs.m, sum);
+    S[1] = weights(a, S[1], rs.m, sum);
+    rs.l += sum;
     __builtin_amdgcn_wave_barrier();
     // the matrix cores idle beside the cache's stream: the weights go through in two
-    // parts, so that only the output is rounded
+    // parts (16 bits and more; fp16 within 2^-32 of the row's largest weight), so that the
+    // output's rounding is the one that counts
     const f32x8 w = stack(S[0], S[1]);
     const frag P = to_frag<IT>(w);
     frag P1;

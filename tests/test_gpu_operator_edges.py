@@ -123,3 +123,23 @@ def test_masked_values_change_no_bit(rp, it, value, window, ql):
                 p["vc"][a, b] = value
     again, lse2 = attend(rp, p, window=window)
     assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+def test_f16_weights_far_below_the_largest(rp):
+    """60,000 keys of weight just below 2^-25 of the largest are 1/600 of the sum: row tiles that walk the
+    whole cache (enough sequences that it is not split) may not lose them."""
+    n, S, ql = 60000, 257, 17
+    p = paged([n], [ql], 1, 1, 64, 1000, "f16", seed=61, spare=0, extra_cols=0)
+    p["kc"][:], p["vc"][:], p["q"][:] = 0, 1, 0
+    p["q"][:, :, 0] = 12
+    p["kc"][int(p["table"][0, 0]), 0, 0, 0] = 11.6          # 12 x 11.6 / 8 = 17.4 = 25.1 log(2)
+    e, mag, el, err = ref.paged_attention(p["q"], p["kc"], p["vc"], p["table"], p["seqs"], p["kv"])
+    p["q"], p["table"], p["kv"] = p["q"].repeat(S, 1, 1), p["table"].repeat(S, 1), p["kv"].repeat(S)
+    p["seqs"] = [(s * ql, ql) for s in range(S)]
+    p["seq_start"] = torch.arange(S + 1).int() * ql
+    c = [p[k].cuda() for k in ("q", "kc", "vc", "table", "seq_start", "kv", "q")]
+    assert rp.rssm_paged_attention_workspace(*c, max_seq_len=ql, max_kv_len=n) == 0
+    out, lse = attend(rp, p)
+    rep = lambda t: t.repeat(S, *[1] * (t.dim() - 1))       # noqa: E731
+    ref.check(out, rep(e), rep(ref.out_bound(e, mag, err, out.dtype)), "out")
+    ref.check(lse, rep(el), rep(err + 2.0 ** -20 * el.abs().clamp(min=1)), "lse")
