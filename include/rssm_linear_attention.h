@@ -112,11 +112,16 @@ rssm_status rssm_linear_attention_workspace(const rssm_linear_attention_desc *de
 /* Enqueue the prompt form on `hip_stream`.  Arithmetic: chunks of 64 tokens
  * on the matrix cores; the state and every sum are held in fp32.  The products
  * of the state update carry at least 22 bits for an fp32 state and 16 for a
- * 16-bit one.  16-bit inputs: for y, the decay-weighted scores and the chunk's
- * starting state are rounded once to the input dtype before their products (fp16
- * with a power-of-two scale, so nothing overflows or underflows).  Token t's
- * output depends on tokens up to t only, non-finite inputs included; a dt_raw of
- * -infinity under softplus skips its token. */
+ * 16-bit one; with fp16 inputs 22 for terms dt x down to 2^-29 of the largest
+ * that the chunk adds to the same state row (decays counted), and 2^-51 of that
+ * largest below.  16-bit inputs: for y, the decay-weighted scores and the chunk's
+ * starting state are rounded once to the input dtype before their products.  fp16
+ * scales the scores of a token, and each row of the state, by a power of two that
+ * brings the largest to 2^12: nothing overflows, and entries below 2^-26 of that
+ * largest are within 2^-37 of it.  Token t's output depends on tokens up to t
+ * only, non-finite inputs included (in the state and the later tokens of its
+ * heads an infinity may come out as NaN); a dt_raw of -infinity under softplus
+ * skips its token. */
 rssm_status rssm_linear_attention(const rssm_linear_attention_desc *desc, const rssm_linear_attention_tables *tables,
                                   void *hip_stream);
 

@@ -14,7 +14,7 @@
 //       times exp(l_i), a scalar of the lane's column i
 //   y^T += x^T M^T                         A = x columns (LDS), Bm = masked weighted scores
 //   S'^T[n][p] = B^T (w x)                 A = B columns (LDS), Bm = w_j x_j in parts of the
-//                                          input type (fp16: scaled by a power of two)
+//                                          input type (fp16: scaled by powers of two)
 // Wavefront w owns tokens 16w .. 16w+15 of y and state rows 16w .. 16w+15 of the
 // update.  The next chunk's inputs are loaded into registers while the current
 // one is computed.  A chunk of 64 keeps two workgroups a compute unit (57 KiB of LDS
@@ -96,12 +96,12 @@ __device__ __forceinline__ void store_state4(char* p, f32x4 v) {
 // 2^k by exponent bits, k in [-126, 127].
 __device__ __forceinline__ float pow2i(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
 
-// Exponent k such that 2^k brings a magnitude m (finite, >= 0) to about
-// 2^12; 0 for m = 0 or non-finite m.  At most 60, so that 2^k times fp32 sums stays finite.
-__device__ __forceinline__ int scale_exp(float m) {
+// Exponent k such that 2^k brings a magnitude m (finite, >= 0) into [2^top,
+// 2^(top + 1)); 0 for m = 0 or non-finite m.  At most 60, so that 2^k times fp32 sums stays finite.
+__device__ __forceinline__ int scale_exp(float m, int top) {
   const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
   if (!(m > 0.0f) || e == 128) return 0;
-  const int k = 12 - e;
+  const int k = top - e;
   return k > 60 ? 60 : (k < -110 ? -110 : k);
 }
 
@@ -217,8 +217,11 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
   constexpr int KS = N / 32;
   constexpr int es = sizeof(elem);
   constexpr int ss = sizeof(typename Mma<ST>::elem);
-  // parts of w_j x_j in the update: enough bits for an fp32 state (bf16 8 a part, fp16
-  // 11), 16 and more for a state that is stored in 16 bits
+  // parts of w_j x_j in the update: bf16 takes 8 bits a part, enough for an fp32 state or 16 for a
+  // state that is stored in 16 bits.  fp16 takes 11, scaled by a power of two that brings the state row's
+  // largest term of the chunk below 2^15; weights fall by any factor inside a chunk, so the second part is
+  // scaled by another 2^12 and summed apart: 22 bits of terms down to 2^-29 of the largest, and
+  // 2^-51 of the largest below (unscaled, a term at 2^-26 kept 13 bits; the sum apart costs 5%)
   constexpr int kParts = IT == kF32 ? 1 : (IT == kBF16 && ST == kF32 ? 3 : 2);
   __shared__ LinLds<IT, N> L;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
@@ -399,7 +402,7 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(S[n][r]));
-        const int k = scale_exp(max_groups(m));
+        const int k = scale_exp(max_groups(m), 12);
         sc = pow2i(k);
         if (g == 0) L.sinv[16 * wave + li] = pow2i(-k);
       }
@@ -480,7 +483,7 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
         for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
           for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(M[jt][r]));
-        mk = scale_exp(max_groups(m));
+        mk = scale_exp(max_groups(m), 12);
         const float ms = pow2i(mk);
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) M[jt] *= ms;
@@ -549,7 +552,7 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(wx[k][e]));
-      sk = scale_exp(max_groups(m));
+      sk = scale_exp(max_groups(m), 14);
     }
     const float up = pow2i(sk), down = pow2i(-sk);
 #pragma unroll
@@ -562,7 +565,7 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
         if constexpr (kParts > 2) u2[k] = take_bf16(left);
       } else {
         u0[k] = to_frag<IT>(v);
-        if constexpr (kParts > 1) u1[k] = to_frag<IT>(v - from_frag<IT>(u0[k]));
+        if constexpr (kParts > 1) u1[k] = to_frag<IT>((v - from_frag<IT>(u0[k])) * 0x1p12f);
       }
     }
     const float dup = IT == kF16 ? decay * up : decay;
@@ -570,17 +573,16 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
     for (int n = 0; n < NT; ++n) S[n] *= dup;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      f32x4 low = f32x4{0, 0, 0, 0};   // fp16: the second parts' sum
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const frag b = frag_col<IT>(L.Bs, LinLds<IT, N>::kN, 32 * k, 16 * n, lane);
         if constexpr (kParts > 2) S[n] = mma<IT>(b, u2[k], S[n]);
-        if constexpr (kParts > 1) S[n] = mma<IT>(b, u1[k], S[n]);
+        if constexpr (IT == kF16) low = mma<IT>(b, u1[k], low);
+        else if constexpr (kParts > 1) S[n] = mma<IT>(b, u1[k], S[n]);
         S[n] = mma<IT>(b, u0[k], S[n]);
       }
-    }
-    if constexpr (IT == kF16) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) S[n] *= down;
+      if constexpr (IT == kF16) S[n] = (S[n] + low * 0x1p-12f) * down;
     }
   }
 

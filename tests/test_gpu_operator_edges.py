@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import operators_ref as ref
-from test_gpu_linear_attention import check_prompt, run_step
+from test_gpu_linear_attention import check_prompt, run_prompt, run_step
 from test_gpu_linear_attention import make as linear
 from test_gpu_paged_attention import attend
 from test_gpu_paged_attention import make as paged
@@ -143,3 +143,20 @@ def test_f16_weights_far_below_the_largest(rp):
     rep = lambda t: t.repeat(S, *[1] * (t.dim() - 1))       # noqa: E731
     ref.check(out, rep(e), rep(ref.out_bound(e, mag, err, out.dtype)), "out")
     ref.check(lse, rep(el), rep(err + 2.0 ** -20 * el.abs().clamp(min=1)), "lse")
+
+
+@pytest.mark.parametrize("st", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("A", [4.0, 16.0, 60.0])
+def test_f16_state_terms_of_any_size(rp, st, A):
+    """Each token writes a column of its own, so its term is all that the column holds: at least 22
+    bits of it down to 2^-29 of the row's largest term, and 2^-51 of that largest below."""
+    p = linear([64], H=1, hpg=1, it="f16", st=st, dim=64, dstate=64, seed=50, z=False, D=False)
+    p["A"], p["dt_bias"], p["dt"][:] = -torch.tensor([A]), None, 0.1
+    p["B"] = torch.eye(64).half()[:, None]
+    load = torch.zeros(1, dtype=torch.int32)
+    _, state = run_prompt(rp, p, load=load, softplus=False)
+    _, _, pool, pm = ref.linear_attention(p["state"], p["A"], p["x"], p["B"], p["C"], p["dt"], p["slots"], p["seqs"],
+                                          load=load, softplus=False)
+    s = int(p["slots"][0])
+    bound = ref.state_bound(pool, pm, state.dtype)[s] + 2.0 ** -51 * pool[s].abs().amax(-1, keepdim=True)
+    ref.check(state[s], pool[s], bound, "state")
