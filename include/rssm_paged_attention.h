@@ -39,7 +39,10 @@ extern "C" {
  *   num_pages                pages of the caches >= 1
  *   max_pages                entries of a page_table row that may be read >= 1;
  *                            tokens past max_pages * page_size are not visible
- *   max_seq_len, max_kv_len  largest q_s and kv_len of the call (larger ones are cut to them)
+ *   max_seq_len, max_kv_len  largest q_s and kv_len of the call.  Of a longer q_s the first max_seq_len
+ *                            rows are computed.  With a longer kv_len, tokens from position max_kv_len on
+ *                            are not visible; positions, and with them the causal order and the window,
+ *                            stay those of kv_len, where the append put the tokens
  *   window                   0: none, else >= 1 tokens up to and including the query's
  *   sinks                    first tokens visible beside the window (>= 0)
  *   dtype                    q, k, v and out: RSSM_F32 | RSSM_BF16 | RSSM_F16
@@ -80,8 +83,8 @@ typedef struct {
  *   page_table        [num_seqs][max_pages] int32
  *   seq_start         [num_seqs + 1] int32 ascending; kv_len [num_seqs] int32
  *   workspace         device memory of workspace_bytes, or NULL when 0 is needed
- * Guards against faults: seq_start is clamped to [0, num_tokens], kv_len to
- * [0, max_kv_len], and pages outside [0, num_pages) are neither read nor
+ * Guards against faults: seq_start is clamped to [0, num_tokens], a negative kv_len
+ * to 0, and pages outside [0, num_pages) are neither read nor
  * written; a new token whose position is negative is not appended.  Two sequences may share
  * pages as long as neither appends to them.  Alignment: caches, q, out,
  * k_new, v_new and workspace 16 bytes, their strides multiples of 16 bytes; the others 4 bytes. */

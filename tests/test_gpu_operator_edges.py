@@ -160,3 +160,31 @@ def test_f16_state_terms_of_any_size(rp, st, A):
     s = int(p["slots"][0])
     bound = ref.state_bound(pool, pm, state.dtype)[s] + 2.0 ** -51 * pool[s].abs().amax(-1, keepdim=True)
     ref.check(state[s], pool[s], bound, "state")
+
+
+@pytest.mark.parametrize("it", ["bf16", "f32"])
+@pytest.mark.parametrize("ql", [1, 40])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (60, 0), (60, 3), (120, 0)])
+def test_kv_len_past_max_kv_len(rp, it, ql, window, sinks):
+    """Positions stay those of kv_len (where the append put the tokens); keys from max_kv_len on are hidden."""
+    p = paged([200, 130, 90], [ql] * 3, 4, 2, 64, 16, it, seed=62)
+    out, lse = attend(rp, p, window=window, sinks=sinks, max_kv_len=96)
+    p["table"] = p["table"][:, :6]
+    e, mag, el, err = ref.paged_attention(p["q"], p["kc"], p["vc"], p["table"], p["seqs"], p["kv"], window=window,
+                                          sinks=sinks)
+    ref.check(out, e, ref.out_bound(e, mag, err, out.dtype), "out")
+    empty = el == -math.inf
+    assert torch.equal(lse.cpu() == -math.inf, empty) and (out.cpu()[empty] == 0).all()
+
+
+@pytest.mark.parametrize("longest", [6, 15])
+@pytest.mark.parametrize("kv", [100, 2500])
+def test_new_tokens_past_max_seq_len(rp, longest, kv):
+    """The first rows of a longer sequence are computed, at their own positions; the others stay as they are."""
+    p = paged([kv, 90], [20, 3], 4, 2, 64, 16, "bf16", seed=63)
+    out, lse = attend(rp, p, max_seq_len=longest)
+    e, mag, el, err = ref.paged_attention(p["q"], p["kc"], p["vc"], p["table"], p["seqs"], p["kv"])
+    rows = [*range(longest), 20, 21, 22]
+    ref.check(out[rows], e[rows], ref.out_bound(e, mag, err, out.dtype)[rows], "out")
+    ref.check(lse[rows], el[rows], (err + 2.0 ** -20 * el.abs().clamp(min=1))[rows], "lse")
+    assert torch.isnan(out[longest:20]).all() and torch.isnan(lse[longest:20]).all()
