@@ -43,7 +43,8 @@ extern "C" {
  *   state_slot_stride  elements between slots, >= H*dim*dstate
  *   *_token_stride     elements between rows of each tensor; rows are dense
  *                      inside, so that views of one packed projection pass
- *   workspace_bytes    bytes at tables->workspace */
+ *   workspace_bytes    bytes at tables->workspace
+ * num_seqs * num_heads * dim / 64 is below 2^24. */
 typedef struct {
   int32_t num_seqs;
   int32_t num_tokens;

@@ -49,7 +49,11 @@ extern "C" {
  *   scale                    factor of the scores
  *   *_stride                 elements: pages, rows inside a page and heads of
  *                            both caches; rows of q, out, k_new, v_new; rows of page_table
- *   workspace_bytes          bytes at tables->workspace */
+ *   workspace_bytes          bytes at tables->workspace
+ * One launch takes fewer than 2^24 workgroups: num_seqs * num_kv_heads * max_seq_len *
+ * (num_q_heads / num_kv_heads) / 64 (its last two factors rounded up) is below that for the
+ * attention, num_tokens * num_q_heads below 2^26 where a workspace is needed, and the bytes of
+ * k_new below 2^36 for the append. */
 typedef struct {
   int32_t num_seqs;
   int32_t num_tokens;

@@ -2,6 +2,7 @@
 // the launch on the caller's stream.
 #include "rssm_block_norm.h"
 
+#include <algorithm>
 #include <cstdio>
 
 #include "norm_inst.h"
@@ -75,7 +76,6 @@ extern "C" rssm_status rssm_block_norm(const rssm_block_norm_desc* d, const rssm
   a.r_stride = d->residual_row_stride;
   a.ro_stride = d->residual_out_row_stride;
   a.n_stride = d->normed_row_stride;
-  a.rows = d->rows;
   a.C = d->channels;
   a.groups = d->groups;
   a.eps = d->eps;
@@ -84,8 +84,16 @@ extern "C" rssm_status rssm_block_norm(const rssm_block_norm_desc* d, const rssm
     std::fprintf(stderr, "[rssm_block_norm] %s/%s rows=%d channels=%d groups=%d\n", dtype_name(d->input_dtype),
                  dtype_name(d->residual_dtype), d->rows, d->channels, d->groups);
   void* params[] = {&a};
-  hipError_t e = hipLaunchKernel(fn, dim3(static_cast<unsigned>(d->rows)), dim3(kNormBlock), params, 0,
-                                 static_cast<hipStream_t>(hip_stream));
-  if (e != hipSuccess) return fail(RSSM_ERR_HIP, "launch of block_norm failed: %s", hipGetErrorString(e));
+  for (int64_t row = 0; row < d->rows; row += kMaxWorkgroups) {   // as many rows as one launch takes
+    a.rows = static_cast<int32_t>(std::min<int64_t>(kMaxWorkgroups, d->rows - row));
+    hipError_t e = hipLaunchKernel(fn, dim3(static_cast<unsigned>(a.rows)), dim3(kNormBlock), params, 0,
+                                   static_cast<hipStream_t>(hip_stream));
+    if (e != hipSuccess) return fail(RSSM_ERR_HIP, "launch of block_norm failed: %s", hipGetErrorString(e));
+    a.y += a.rows * a.y_stride * ie;
+    if (a.z != nullptr) a.z += a.rows * a.z_stride * ie;
+    a.residual += a.rows * a.r_stride * re;
+    a.residual_out += a.rows * a.ro_stride * re;
+    if (a.normed != nullptr) a.normed += a.rows * a.n_stride * ie;
+  }
   return RSSM_OK;
 }

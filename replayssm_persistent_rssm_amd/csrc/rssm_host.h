@@ -15,6 +15,9 @@ void clear_error();
 bool verbose();               // RSSM_MATERIALIZE_VERBOSE
 const char* dtype_name(int d);
 
+// Workgroups of 256 threads that one launch dimension takes (fewer than 2^32 threads).
+constexpr int64_t kMaxWorkgroups = (int64_t(1) << 24) - 1;
+
 template <typename T>
 bool aligned(const T* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;

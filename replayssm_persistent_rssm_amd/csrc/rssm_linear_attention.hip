@@ -202,7 +202,8 @@ rssm_status rssm_linear_attention(const rssm_linear_attention_desc* d, const rss
     return fail(RSSM_ERR_INVALID_ARGUMENT, "workspace of %lld bytes is needed (got %lld)", static_cast<long long>(need),
                 static_cast<long long>(t->workspace == nullptr ? 0 : d->workspace_bytes));
   const int64_t items = static_cast<int64_t>(d->num_seqs) * sp.nseg * d->num_heads * (d->dim / kLinP);
-  if (items > INT32_MAX) return fail(RSSM_ERR_INVALID_ARGUMENT, "num_seqs*num_heads is too large");
+  if (items > kMaxWorkgroups)
+    return fail(RSSM_ERR_INVALID_ARGUMENT, "num_seqs*num_heads*dim/64 must be below 2^24 (got %lld)", static_cast<long long>(items));
   LinArgs a;
   fill_args(&a, d, t);
   a.nseg = sp.nseg;
@@ -238,7 +239,8 @@ rssm_status rssm_linear_attention_step(const rssm_linear_attention_desc* d, cons
   st = check_tables(d, t, true);
   if (st != RSSM_OK) return st;
   const int64_t items = static_cast<int64_t>(d->num_seqs) * d->num_heads * (d->dim / kLinP);
-  if (items > INT32_MAX) return fail(RSSM_ERR_INVALID_ARGUMENT, "num_seqs*num_heads is too large");
+  if (items > kMaxWorkgroups)
+    return fail(RSSM_ERR_INVALID_ARGUMENT, "num_seqs*num_heads*dim/64 must be below 2^24 (got %lld)", static_cast<long long>(items));
   LinArgs a;
   fill_args(&a, d, t);
   if (verbose())

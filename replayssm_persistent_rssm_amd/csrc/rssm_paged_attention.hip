@@ -180,8 +180,14 @@ void fill_args(PagedArgs* a, const rssm_paged_attention_desc* d, const rssm_page
   a->split_tiles = 1 << 30;
 }
 
+rssm_status check_grid(int64_t grid, const char* name) {
+  if (grid > kMaxWorkgroups)
+    return fail(RSSM_ERR_INVALID_ARGUMENT, "%s needs %lld workgroups, more than one launch takes (2^24 - 1)", name,
+                static_cast<long long>(grid));
+  return RSSM_OK;
+}
+
 rssm_status launch(const void* fn, int64_t grid, void** params, void* stream, const char* name) {
-  if (grid > INT32_MAX) return fail(RSSM_ERR_INVALID_ARGUMENT, "%s: too many workgroups", name);
   hipError_t e = hipLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kPagedBlock), params, 0,
                                  static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(RSSM_ERR_HIP, "launch of %s failed: %s", name, hipGetErrorString(e));
@@ -211,7 +217,10 @@ rssm_status rssm_paged_append(const rssm_paged_attention_desc* d, const rssm_pag
   void* params[] = {&a, &head_vecs};
   const void* fn = d->dtype == RSSM_F32 ? reinterpret_cast<const void*>(&paged_append_kernel<4>)
                                         : reinterpret_cast<const void*>(&paged_append_kernel<2>);
-  return launch(fn, (work + kPagedBlock - 1) / kPagedBlock, params, hip_stream, "paged_append");
+  const int64_t grid = (work + kPagedBlock - 1) / kPagedBlock;
+  st = check_grid(grid, "paged_append");
+  if (st != RSSM_OK) return st;
+  return launch(fn, grid, params, hip_stream, "paged_append");
 }
 
 rssm_status rssm_paged_attention_workspace(const rssm_paged_attention_desc* d, int64_t* bytes) {
@@ -260,12 +269,15 @@ rssm_status rssm_paged_attention(const rssm_paged_attention_desc* d, const rssm_
                  p.rows16 ? "rows" : "tiles", p.row_tiles, p.nsplit);
   void* params[] = {&a};
   const int64_t grid = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * p.row_tiles * p.nsplit;
-  st = launch(kernel_for(p.rows16 ? kPagedRow : kPagedTile, d), grid, params, hip_stream, "paged_attention");
-  if (st != RSSM_OK || p.nsplit == 1) return st;
   // few rows with many splits: a workgroup a row, otherwise a wavefront a row
   const bool share = p.nsplit > 16 && out_rows < 4096;
-  return launch(kernel_for(share ? kPagedJoinShare : kPagedJoin, d), share ? out_rows : (out_rows + 3) / 4, params,
-                hip_stream, "paged_join");
+  const int64_t join_grid = share ? out_rows : (out_rows + 3) / 4;
+  st = check_grid(grid, "paged_attention");
+  if (st == RSSM_OK && p.nsplit > 1) st = check_grid(join_grid, "paged_join");
+  if (st != RSSM_OK) return st;
+  st = launch(kernel_for(p.rows16 ? kPagedRow : kPagedTile, d), grid, params, hip_stream, "paged_attention");
+  if (st != RSSM_OK || p.nsplit == 1) return st;
+  return launch(kernel_for(share ? kPagedJoinShare : kPagedJoin, d), join_grid, params, hip_stream, "paged_join");
 }
 
 }  // extern "C"

@@ -188,3 +188,21 @@ def test_new_tokens_past_max_seq_len(rp, longest, kv):
     ref.check(out[rows], e[rows], ref.out_bound(e, mag, err, out.dtype)[rows], "out")
     ref.check(lse[rows], el[rows], (err + 2.0 ** -20 * el.abs().clamp(min=1))[rows], "lse")
     assert torch.isnan(out[longest:20]).all() and torch.isnan(lse[longest:20]).all()
+
+
+def test_norm_of_more_rows_than_one_launch_takes(rp):
+    R, C = 2 ** 24 + 3, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    y = torch.randn(R, C, generator=g, device="cuda", dtype=torch.bfloat16)
+    z = torch.randn(R, C, generator=g, device="cuda", dtype=torch.bfloat16)
+    res = torch.randn(R, C, generator=g, device="cuda")
+    out, n = torch.full_like(res, math.nan), torch.full_like(y, math.nan)
+    rp.rssm_block_norm(y, res, out, n)
+    assert torch.equal(out, res + y.float())                # one fp32 addition
+    rows = [0, 1, 2 ** 23, 2 ** 24 - 3, 2 ** 24 - 2, 2 ** 24 - 1, 2 ** 24, 2 ** 24 + 1, 2 ** 24 + 2]
+    _, _, nn, nm = ref.block_norm(y[rows].cpu(), res[rows].cpu())
+    ref.check(n[rows], nn, ref.norm_bound(nn, nm, n.dtype), "normed")
+    assert not torch.isnan(n).any()
+    rp.rssm_block_norm(y, res, out, None, z=z)              # no normed; with a gate
+    r, rm, _, _ = ref.block_norm(y[rows].cpu(), res[rows].cpu(), z=z[rows].cpu())
+    ref.check(out[rows], r, ref.norm_bound(r, rm, out.dtype), "residual")

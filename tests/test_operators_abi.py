@@ -247,3 +247,18 @@ def test_descriptors_match_the_headers(rp):
             want = [(m[2], 8 if m[1] else size[m[0]]) for m in
                     re.findall(r"(?:const )?(\w+) ?(\*?)(\w+);", body)]
             assert [(n, ctypes.sizeof(t)) for n, t in cls._fields_] == want
+
+
+def test_more_workgroups_than_one_launch_takes(rp):
+    """Refused by name before any HIP call."""
+    lib = rp.lib()
+    for fn, kw in ((lib.rssm_linear_attention, dict(num_seqs=2 ** 18)),
+                   (lib.rssm_linear_attention_step, dict(num_seqs=2 ** 18, num_tokens=2 ** 18))):
+        assert fn(ctypes.byref(lin_desc(rp, **kw)), ctypes.byref(fake(rp.RssmLinearTables)), None) == 1
+        assert "2^24" in rp.rssm_last_error()
+    tab = fake(rp.RssmPagedTables)
+    wide = dict(num_seqs=2 ** 16, max_seq_len=2 ** 14, num_tokens=2 ** 30)
+    assert lib.rssm_paged_attention(ctypes.byref(paged_desc(rp, **wide)), ctypes.byref(tab), None) == 1
+    assert "2^24" in rp.rssm_last_error()
+    assert lib.rssm_paged_append(ctypes.byref(paged_desc(rp, num_tokens=2 ** 28)), ctypes.byref(tab), None) == 1
+    assert "2^24" in rp.rssm_last_error()
