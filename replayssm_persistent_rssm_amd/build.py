@@ -1,7 +1,9 @@
 """Build librssm_materialize.so (the operation) and librssm_pool.so (the
 contiguous-pool placement helper, a separate library so that the operation's
 library exports nothing that allocates) for gfx950 with hipcc, and the
-binding's marshalling extension with the host compiler, in-tree, no JIT.
+binding's marshalling extension with the host compiler, in-tree, no JIT.  The
+extension is left out where torch is not installed: the libraries are plain C ABI
+and need neither torch nor the binding.
 
 Each state dtype's kernel instances live in their own translation unit and
 compile in parallel; the host launcher is one more.  Flags: -O3, C++17,
@@ -13,6 +15,7 @@ from __future__ import annotations
 
 import concurrent.futures
 import os
+import shutil
 import subprocess
 import sys
 
@@ -68,14 +71,25 @@ def _link(objs, path: str, verbose: bool) -> None:
     os.replace(tmp, path)
 
 
-def _build_fast(verbose: bool) -> None:
-    """The marshalling extension, linked to the operation library beside it."""
+def _cxx() -> str:
+    """Host compiler: $CXX, g++, or the compiler that comes with hipcc."""
+    return os.environ.get("CXX") or shutil.which("g++") or os.path.join(os.path.dirname(HIPCC), "amdclang++")
+
+
+def _build_fast(verbose: bool) -> bool:
+    """The marshalling extension, linked to the operation library beside it; False without torch, whose
+    tensors are all it handles."""
     import sysconfig
-    import torch
+    try:
+        import torch
+    except ImportError:
+        print(f"torch is not installed: {os.path.basename(FAST_PATH)}, the torch binding's extension, is left out",
+              file=sys.stderr)
+        return False
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = FAST_PATH + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+    cmd = [_cxx(), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I" + INCLUDE,
            "-I" + sysconfig.get_paths()["include"], "-I" + inc,
            "-I" + os.path.join(inc, "torch", "csrc", "api", "include"), os.path.join(CSRC, FAST_SOURCE), "-o", tmp,
@@ -86,6 +100,7 @@ def _build_fast(verbose: bool) -> None:
     if res.returncode != 0:
         raise RuntimeError(f"build of {os.path.basename(FAST_PATH)} failed:\n" + res.stderr)
     os.replace(tmp, FAST_PATH)
+    return True
 
 
 def build(verbose: bool = False, jobs: int = 8) -> str:
