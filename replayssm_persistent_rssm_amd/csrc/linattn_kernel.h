@@ -225,7 +225,7 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
   constexpr int kParts = IT == kF32 ? 1 : (IT == kBF16 && ST == kF32 ? 3 : 2);
   __shared__ LinLds<IT, N> L;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
-  int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Each XCD takes a range of heads of every stretch, so that the heads of a
   // B/C group meet in its L2 and ragged lengths spread evenly; when the heads
   // do not divide among the XCDs, a contiguous range of items.
@@ -247,8 +247,6 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
   const int t0 = seg * a.seg_len;
   const int t1 = q.len - t0 < a.seg_len ? q.len : t0 + a.seg_len;
   if (kStateOnly ? (q.len - t0 <= a.seg_len) : (seg > 0 && t0 >= q.len)) return;
-  // wavefronts with later tokens have more causal products: alternate which SIMD gets them
-  const int wrow = (unit & 1) ? 3 - wave : wave;
 
   const float A = sload(a.A + h);
   const float Dh = a.D != nullptr ? sload(a.D + h) : 0.0f;
@@ -292,7 +290,7 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
   char* py = a.y + (first * a.y_stride + hx) * es;
   xr.init(xb, tid);
   br.init(Bb, tid);
-  const uint32_t c_at = (16 * wrow + li) * cb + 8 * g * es, z_at = (16 * wrow + li) * zb + 8 * g * es;
+  const uint32_t c_at = (16 * wave + li) * cb + 8 * g * es, z_at = (16 * wave + li) * zb + 8 * g * es;
   auto fetch = [&](int t) {
     const int rows = t1 - t < kLinQ ? t1 - t : kLinQ;
     xr.load(px, xb, rows);
@@ -300,7 +298,7 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
     px += static_cast<int64_t>(kLinQ) * xb;
     pB += static_cast<int64_t>(kLinQ) * Bb;
   };
-  auto fetch_C = [&](int t) {   // C rows of the wavefront's tokens: column i = 16 wrow + li
+  auto fetch_C = [&](int t) {   // C rows of the wavefront's tokens: column i = 16 wave + li
     const int rows = t1 - t < kLinQ ? t1 - t : kLinQ;
     const rsrc_t rc = make_rsrc(pC, (rows - 1) * cb + N * es);
     pC += static_cast<int64_t>(kLinQ) * cb;
@@ -416,7 +414,7 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
     if (c4 == 2) dtr = fetch_dt(t + 2 * kLinQ);
 
     if constexpr (!kStateOnly) {
-      const int i = 16 * wrow + li;
+      const int i = 16 * wave + li;
       const bool has_z = a.z != nullptr;
       u32x4 zw[IT == kF32 ? 4 : 2];
       if (has_z) {
@@ -430,8 +428,8 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
       f32x4 M[4], Y[4];
       const float lri = L.lr[c4][i];
       const float later = L.since[c4][g < li >> 2 ? (li >> 2) - 1 - g : 0][i];
-      const f32x4 a4 = *reinterpret_cast<const f32x4*>(L.da[c4] + 16 * wrow + 4 * g);
-      const f32x4 dj = *reinterpret_cast<const f32x4*>(L.dt[c4] + 16 * wrow + 4 * g);
+      const f32x4 a4 = *reinterpret_cast<const f32x4*>(L.da[c4] + 16 * wave + 4 * g);
+      const f32x4 dj = *reinterpret_cast<const f32x4*>(L.dt[c4] + 16 * wave + 4 * g);
       // scores (4 tiles of 16 tokens), then the starting state's part (4 tiles of 16 rows): the
       // next tile's fragments are read while the matrix cores take the current ones
       frag f[2][KS];
@@ -458,9 +456,9 @@ __global__ __launch_bounds__(kLinBlock, IT == kF32 ? 1 : 2) void linattn_chunk_k
       const float ai = __builtin_amdgcn_exp2f(lri);
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
-        if (jt < wrow) {          // earlier tiles: every token is visible
-          M[jt] *= *reinterpret_cast<const f32x4*>(L.before[c4][wrow - 1] + 16 * jt + 4 * g) * ai;
-        } else if (jt == wrow) {  // the diagonal
+        if (jt < wave) {          // earlier tiles: every token is visible
+          M[jt] *= *reinterpret_cast<const f32x4*>(L.before[c4][wave - 1] + 16 * jt + 4 * g) * ai;
+        } else if (jt == wave) {  // the diagonal
           // log decay from token j to token i > j: the tokens after j in j's group of 4 (j = 4g + r),
           // and those of later groups up to i
           f32x4 d;
