@@ -125,7 +125,7 @@ class RssmNormTables(ctypes.Structure):
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
-            f"{LIB_PATH} is not built. Build it with `python -m replayssm_persistent_rssm_amd.build` "
+            f"{LIB_PATH} is not built. Build it with `python replayssm_persistent_rssm_amd/build.py` "
             "(or __graft_entry__.build()); there is no fallback path.")
     lib = ctypes.CDLL(LIB_PATH)
     lib.rssm_materialize.argtypes = [ctypes.POINTER(RssmDesc), ctypes.POINTER(RssmTables), ctypes.c_void_p]
@@ -179,7 +179,7 @@ def pool_lib():
     if _pool is None:
         if not os.path.exists(POOL_LIB_PATH):
             raise ImportError(f"{POOL_LIB_PATH} is not built. Build it with "
-                              "`python -m replayssm_persistent_rssm_amd.build` (or __graft_entry__.build()).")
+                              "`python replayssm_persistent_rssm_amd/build.py` (or __graft_entry__.build()).")
         pl = ctypes.CDLL(POOL_LIB_PATH)
         pl.rssm_pool_alloc.argtypes = [ctypes.c_uint64, ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_int32)]
         pl.rssm_pool_alloc.restype = ctypes.c_int
@@ -545,7 +545,7 @@ def _fast():
         import torch  # noqa: F401  (the extension needs its libraries)
         path = os.path.join(_PKG, "_fast_calls.so")
         if not os.path.exists(path):
-            raise ImportError(f"{path} is not built. Build it with `python -m replayssm_persistent_rssm_amd.build` "
+            raise ImportError(f"{path} is not built. Build it with `python replayssm_persistent_rssm_amd/build.py` "
                               "(or __graft_entry__.build()).")
         import importlib.util
         spec = importlib.util.spec_from_file_location("replayssm_persistent_rssm_amd._fast_calls", path)

@@ -29,3 +29,19 @@ def test_host_compiler(build, monkeypatch):
     monkeypatch.delenv("CXX")
     monkeypatch.setattr(build.shutil, "which", lambda name: None)
     assert build._cxx() == os.path.join(os.path.dirname(build.HIPCC), "amdclang++")
+
+
+def test_the_named_build_command_needs_no_built_library(monkeypatch):
+    """What the message about a missing library says can be run there: the package itself cannot be
+    imported yet, so the command may not go through it."""
+    import re
+    import subprocess
+
+    import replayssm_persistent_rssm_amd._binding as b
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    monkeypatch.setattr(b, "LIB_PATH", "/nowhere/lib.so")
+    with pytest.raises(ImportError) as e:
+        b._load()
+    script = re.search(r"`python (\S+\.py)`", str(e.value)).group(1)
+    code = "import runpy, sys; runpy.run_path(sys.argv[1], run_name='x'); assert 'replayssm_persistent_rssm_amd' not in sys.modules"
+    subprocess.run([sys.executable, "-c", code, script], cwd=root, check=True)
