@@ -206,3 +206,16 @@ def test_norm_of_more_rows_than_one_launch_takes(rp):
     rp.rssm_block_norm(y, res, out, None, z=z)              # no normed; with a gate
     r, rm, _, _ = ref.block_norm(y[rows].cpu(), res[rows].cpu(), z=z[rows].cpu())
     ref.check(out[rows], r, ref.norm_bound(r, rm, out.dtype), "residual")
+
+
+@pytest.mark.parametrize("it", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv", [(16, 1), (24, 1), (64, 2)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 3)])
+def test_single_tokens_of_many_heads_a_page(rp, it, Hq, Hkv, window, sinks):
+    """Up to 16 rows a key/value head stream the cache, more take row tiles."""
+    p = paged([1, 31, 200, 2500], [1] * 4, Hq, Hkv, 64, 16, it, seed=64)
+    out, lse = attend(rp, p, window=window, sinks=sinks)
+    e, mag, el, err = ref.paged_attention(p["q"], p["kc"], p["vc"], p["table"], p["seqs"], p["kv"], window=window,
+                                          sinks=sinks)
+    ref.check(out, e, ref.out_bound(e, mag, err, out.dtype), "out")
+    ref.check(lse, el, err + 2.0 ** -20 * el.abs().clamp(min=1), "lse")
