@@ -5,9 +5,10 @@
 // Python needs to read the attributes of their tensors.  Each function here
 // takes the binding's arguments, checks that every tensor is contiguous, on the
 // given device and of the expected dtype and shape, and makes the C call.  It returns True when the
-// call was enqueued; on anything else (strided views, other streams,
-// wrong arguments, a library error) it returns False and has enqueued nothing, and the binding's Python
-// code handles the call or names the error.
+// call was enqueued; on anything else (strided views, wrong arguments, a library error) it returns
+// False, and the binding's Python code handles the call or names the error.  Nothing has been enqueued
+// then, unless a later launch of a call that has several failed: the binding's call then starts over, and only
+// the last launch of each writes what the caller sees.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

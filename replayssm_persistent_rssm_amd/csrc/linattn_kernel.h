@@ -25,9 +25,10 @@
 // stretches' states and decays, a third computes the outputs from the
 // scanned starting states.
 //
-// Bound by the vector ALUs and LDS together.  12 ragged prompts, 13,640 tokens, 256 heads in 8
-// groups, gated, fp32 state: 0.58 ms, 2.7 TB/s of the bytes it cannot do without (0.60 ms with z and
-// y in 8-byte pieces).  Of that, the gate takes 13%, three quarters of the score and
+// Bound by the vector ALUs and LDS together: two wavefronts a SIMD do not fill either.  12 ragged prompts,
+// 13,649 tokens, 256 heads in 8 groups, gated, fp32 state: 0.58 ms, 2.7 TB/s of the bytes it cannot do without
+// (0.60 ms with z and y in 8-byte pieces); 466 vector, 88 matrix and 111 LDS instructions a wavefront and chunk keep
+// the vector ALUs busy 44% of the time, LDS 48% (and 10% more in bank conflicts), the matrix cores 26%.  Of that time, the gate takes 13%, three quarters of the score and
 // starting-state products 13%, two of the three parts of the state update 6% (each timed by leaving it
 // out).  One prompt of 16,384 tokens, 64 heads, bf16 state, in 8 stretches: 0.22 ms, a quarter of it the
 // fold.
@@ -639,8 +640,8 @@ __global__ __launch_bounds__(kLinBlock) void linattn_scan_kernel(LinArgs a, int 
 // wavefront.  The state streams through registers once (16-byte non-temporal loads and
 // stores, all of a wavefront's rows in flight); each lane folds its columns
 // and the row's readout is summed over the lanes that share it.  Bound by memory:
-// 256 requests of 256 heads of 64 x 128 bf16 in 0.365 ms, 5.95 TB/s read and written; one
-// request 4.4 us, most of it the launch.
+// 256 requests of 256 heads of 64 x 128 bf16 in 0.369 ms, 5.9 TB/s read and written; one
+// request 4.2 us, most of it the launch.
 template <int IT, int ST, int N>
 __global__ __launch_bounds__(kLinBlock) void linattn_step_kernel(LinArgs a) {
   typedef typename Mma<IT>::elem elem;

@@ -3,10 +3,11 @@
 // next block.
 //
 // One workgroup a row; the row stays in registers (VPT vectors of 8 channels a
-// thread), so each tensor is read or written once: the operation is bound by
-// memory.  Sums of squares go lane -> wavefront (shuffles) -> LDS in a fixed order.
-// 16,384 rows of 8,192 channels, bf16 with an fp32 residual: 0.337 ms, 4.8 TB/s, the rate of a
-// large copy on the same card (4.9); non-temporal accesses ran 21% slower.
+// thread), so each tensor is read or written once.  Sums of squares go lane -> wavefront
+// (shuffles) -> LDS in a fixed order.  16,384 rows of 8,192 channels, bf16 with an fp32 residual: 0.338 ms,
+// 4.8 TB/s, as a large copy on the same card (5.0; on a card where that copy runs at 4.0, 0.400 ms), but
+// not the memory's limit: the single-token linear attention moves equal reads and writes at 5.9 TB/s.  A row's loads,
+// reductions and stores follow one another inside its workgroup; non-temporal accesses ran 21% slower.
 #pragma once
 
 #include "mma_device.h"

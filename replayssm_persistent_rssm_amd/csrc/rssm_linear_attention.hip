@@ -105,12 +105,12 @@ struct Split { int nseg, seg_len; };
 
 // Stretches of the token axis.  Every stretch but the last is folded twice (its
 // state, then its outputs), so the axis is split only when the (sequence, head)
-// tiles leave compute units without a workgroup (5 prompts of 1,500 tokens, 64 heads, 320 tiles: 104 us
-// whole, 130 in two stretches).  Then as many stretches as give each two (8 ragged prompts up to
-// 2,500, 24 heads: 89 us with three, 116 with two; one prompt of 16,384 tokens and 64 heads: 226 us with 8
-// stretches, 229 with 16, 241 with 24), at most one a chunk (7 prompts up to 605 tokens of 2 heads:
-// 18.5 us, 32.9 with four chunks a stretch) and 64, because the scan is serial (one prompt of
-// 16,384 tokens and one head: 34.5 us with 64, 51.5 with 256).
+// tiles leave compute units without a workgroup (5 prompts of 1,500 tokens, 64 heads, 320 tiles: 103 us
+// whole, 125 in two stretches).  Then as many stretches as give each two (8 ragged prompts up to
+// 2,500, 24 heads: 90 us with three, 117 with two; one prompt of 16,384 tokens and 64 heads: 228 us with 8
+// stretches, 234 with 16, 253 with 24), at most one a chunk (7 prompts up to 605 tokens of 2 heads:
+// 18.6 us, 28.2 with four chunks a stretch) and 64, because the scan is serial (one prompt of
+// 16,384 tokens and one head: 34.5 us with 64, 52.4 with 256).
 Split split_of(const rssm_linear_attention_desc* d) {
   const int64_t items = static_cast<int64_t>(d->num_seqs) * d->num_heads * (d->dim / kLinP);
   const int64_t chunks = (static_cast<int64_t>(d->max_seq_len) + kLinQ - 1) / kLinQ;

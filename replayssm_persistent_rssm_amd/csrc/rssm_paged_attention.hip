@@ -96,13 +96,13 @@ struct Plan {
 };
 
 // The split of the key axis.  Row tiles: none when they give every compute unit a
-// workgroup, otherwise as many as fit two each in one round (2,000 new tokens over 40,000, 4 heads of
-// 128: 235 us with 504 workgroups, 303 with 567), of at least 2 tiles of keys (3 times 5 new tokens over 4,000, 16 heads of
-// 64: 15.3 us, 19.5 with 4).  Single tokens: up to 4,096
+// workgroup, otherwise as many as fit two each in one round (2,000 new tokens over 40,000, 4 query heads
+// and one key/value head of 128: 210 us with 504 workgroups, 299 with 567), of at least 2 tiles of keys (3 times 5
+// new tokens over 4,000, 16 / 4 heads of 64: 17.6 us, 20.6 with 4).  Single tokens: up to 4,096
 // workgroups, because ragged lengths leave many of them without work (64 requests of
-// 1 to 8,192 tokens: 296 us with 1,024, 290 with 2,048, 250 with 4,096 or 8,192), each of at
-// least 8 tiles (short caches) to 32 (long ones, where joining costs more: one request of
-// 131,071 tokens 65.7 us with 32, 70.8 with 16).
+// 1 to 8,192 tokens, 32 / 8 heads of 128: 229 us with 1,024, 210 with 2,048, 212 with 4,096, 224 with
+// 8,192), each of at least 8 tiles (short caches) to 32 (long ones, where joining costs more: one
+// request of 131,071 tokens 60.5 us with 32, 65.3 with 16).
 Plan plan_of(const rssm_paged_attention_desc* d) {
   Plan p;
   const int64_t group = d->num_q_heads / d->num_kv_heads;
