@@ -530,7 +530,7 @@ class SsuDecodeCall:
 # Prompt-side operators.  These calls are a few microseconds of GPU work at
 # their smallest, so the common case (contiguous tensors of the right shape) is
 # checked with few attribute reads, and everything else, errors included, goes the
-# long way: 17 us a call on the host with views of wider rows, 10 us with a stream given.
+# long way: 16 us a call on the host with views of wider rows, 10 us with a stream given.
 # --------------------------------------------------------------------------
 _TORCH_CODES = {}
 _calls = None

@@ -94,11 +94,25 @@ at::Tensor workspace(PyObject* given, int64_t bytes, int dev) {
   return at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(at::Device(at::kCUDA, dev)));
 }
 
+// Whether every tensor among the arguments is contiguous and on device a[0].  Asked first, so that views, the
+// other ordinary case, do not pay for an exception (1 to 3 us) before the binding's Python code takes them.
+bool plain(PyObject* const* a, Py_ssize_t n) {
+  if (n < 2 || !PyLong_Check(a[0])) return false;
+  int over = 0;
+  const long dev = PyLong_AsLongAndOverflow(a[0], &over);
+  for (Py_ssize_t i = 2; i < n; ++i) {
+    if (!THPVariable_Check(a[i])) continue;
+    const at::Tensor& t = THPVariable_Unpack(a[i]);
+    if (t.layout() != at::kStrided || !t.is_cuda() || t.get_device() != dev || !t.is_contiguous()) return false;
+  }
+  return true;
+}
+
 template <typename F>
-PyObject* guarded(F f) {
+PyObject* guarded(PyObject* const* a, Py_ssize_t n, F f) {
   bool done = false;
   try {
-    done = f();
+    done = plain(a, n) && f();
   } catch (...) {
     if (PyErr_Occurred()) PyErr_Clear();
     done = false;
@@ -109,7 +123,7 @@ PyObject* guarded(F f) {
 // (device, stream, step, state, A, x, B, C, dt, y, slots, seq_start, max_seq_len, load_state, D, dt_bias, z,
 //  dt_softplus, pad_slot_id, workspace)
 PyObject* linear_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&] {
+  return guarded(a, n, [&] {
     need(n == 20);
     const int dev = i32(a[0]);
     const bool step = a[2] == Py_True;
@@ -189,7 +203,7 @@ void caches(PyObject* k, PyObject* v, PyObject* table, PyObject* seq_start, PyOb
 
 // (device, stream, k_cache, v_cache, k_new, v_new, page_table, seq_start, kv_len)
 PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&] {
+  return guarded(a, n, [&] {
     need(n == 9);
     const int dev = i32(a[0]);
     rssm_paged_attention_desc d{};
@@ -208,7 +222,7 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (device, stream, q, k_cache, v_cache, page_table, seq_start, kv_len, out, max_seq_len, max_kv_len, scale, window,
 //  sinks, lse, workspace)
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&] {
+  return guarded(a, n, [&] {
     need(n == 16);
     const int dev = i32(a[0]);
     rssm_paged_attention_desc d{};
@@ -243,7 +257,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (device, stream, y, residual, residual_out, normed, z, post_weight, pre_weight, channel_scale, residual_scale,
 //  groups, eps)
 PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&] {
+  return guarded(a, n, [&] {
     need(n == 13);
     const int dev = i32(a[0]);
     const at::Tensor &y = tensor(a[2], dev), &r = tensor(a[3], dev);
