@@ -23,11 +23,15 @@ RSSM_OK, RSSM_ERR_INVALID_ARGUMENT, RSSM_ERR_UNSUPPORTED, RSSM_ERR_HIP = 0, 1, 2
 EXPORTS = ("rssm_materialize", "rssm_materialize_checkpoints", "rssm_last_error", "rssm_materialize_launch_config",
            "rssm_debug_encode_rows", "rssm_debug_row_scales", "rssm_gdn_commit", "rssm_ssu_decode",
            "rssm_linear_attention", "rssm_linear_attention_step", "rssm_linear_attention_workspace",
-           "rssm_paged_append", "rssm_paged_attention", "rssm_paged_attention_workspace", "rssm_block_norm")
+           "rssm_paged_append", "rssm_paged_attention", "rssm_paged_attention_workspace", "rssm_block_norm",
+           "rssm_causal_conv", "rssm_causal_conv_step", "rssm_selective_scan", "rssm_selective_scan_step",
+           "rssm_selective_scan_workspace", "rssm_rotary_append", "rssm_page_extend", "rssm_page_fork",
+           "rssm_page_release", "rssm_page_compact", "rssm_page_copy", "rssm_pages_workspace")
 POOL_EXPORTS = ("rssm_pool_alloc", "rssm_pool_free", "rssm_torch_pool_alloc", "rssm_torch_pool_free")
 RSSM_MAX_CHECKPOINTS = 4
 RSSM_SSU_MAX_TOKENS = 8
 RSSM_SSU_MAX_REPLAY = 16
+RSSM_PAGE_OK, RSSM_PAGE_NONE, RSSM_PAGE_REFUSED, RSSM_PAGE_SHARED = 0, 1, 2, 3
 _INT32_MAX = 2**31 - 1
 
 
@@ -122,6 +126,57 @@ class RssmNormTables(ctypes.Structure):
         "y", "z", "residual", "post_weight", "pre_weight", "channel_scale", "residual_out", "normed")]
 
 
+class RssmConvDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_seqs", "num_tokens", "channels", "width", "num_slots", "pad_slot_id", "dtype", "silu")] + [
+        (n, ctypes.c_int64) for n in ("state_slot_stride", "x_token_stride", "y_token_stride")]
+
+
+class RssmConvTables(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "x", "weight", "bias", "y", "state", "slots", "seq_start", "load_state")]
+
+
+class RssmScanDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_seqs", "num_tokens", "channels", "groups", "dstate", "num_slots", "pad_slot_id", "max_seq_len",
+        "state_dtype", "input_dtype", "dt_softplus", "reserved")] + [
+        (n, ctypes.c_int64) for n in (
+            "state_slot_stride", "x_token_stride", "dt_token_stride", "B_token_stride", "C_token_stride",
+            "z_token_stride", "y_token_stride", "workspace_bytes")]
+
+
+class RssmScanTables(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "state", "A", "D", "dt_bias", "x", "dt", "B", "C", "z", "y", "slots", "seq_start", "load_state", "workspace")]
+
+
+class RssmRotaryDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_seqs", "num_tokens", "num_q_heads", "num_kv_heads", "head_dim", "rot_dim", "interleaved", "page_size",
+        "num_pages", "max_pages", "dtype")] + [("factor", ctypes.c_float)] + [
+        (n, ctypes.c_int64) for n in (
+            "page_stride", "row_stride", "head_stride", "q_token_stride", "q_out_token_stride", "k_token_stride",
+            "v_token_stride", "table_stride")]
+
+
+class RssmRotaryTables(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "q", "q_out", "k_new", "v_new", "k_cache", "v_cache", "page_table", "seq_start", "kv_len", "positions",
+        "inv_freq")]
+
+
+class RssmPagesDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_items", "num_rows", "max_pages", "num_pages", "page_size", "num_caches")] + [
+        (n, ctypes.c_int64) for n in ("table_stride", "page_bytes", "page_stride", "token_bytes", "workspace_bytes")]
+
+
+class RssmPagesTables(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "cache_ptrs", "page_table", "kv_len", "page_ref", "src", "dst", "lengths", "status", "live", "workspace")]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -141,12 +196,24 @@ def _load():
                                ("rssm_linear_attention_step", RssmLinearDesc, RssmLinearTables),
                                ("rssm_paged_append", RssmPagedDesc, RssmPagedTables),
                                ("rssm_paged_attention", RssmPagedDesc, RssmPagedTables),
-                               ("rssm_block_norm", RssmNormDesc, RssmNormTables)):
+                               ("rssm_block_norm", RssmNormDesc, RssmNormTables),
+                               ("rssm_causal_conv", RssmConvDesc, RssmConvTables),
+                               ("rssm_causal_conv_step", RssmConvDesc, RssmConvTables),
+                               ("rssm_selective_scan", RssmScanDesc, RssmScanTables),
+                               ("rssm_selective_scan_step", RssmScanDesc, RssmScanTables),
+                               ("rssm_rotary_append", RssmRotaryDesc, RssmRotaryTables),
+                               ("rssm_page_extend", RssmPagesDesc, RssmPagesTables),
+                               ("rssm_page_fork", RssmPagesDesc, RssmPagesTables),
+                               ("rssm_page_release", RssmPagesDesc, RssmPagesTables),
+                               ("rssm_page_compact", RssmPagesDesc, RssmPagesTables),
+                               ("rssm_page_copy", RssmPagesDesc, RssmPagesTables)):
         fn = getattr(lib, name)
         fn.argtypes = [ctypes.POINTER(desc), ctypes.POINTER(tables), ctypes.c_void_p]
         fn.restype = ctypes.c_int
     for name, desc in (("rssm_linear_attention_workspace", RssmLinearDesc),
-                       ("rssm_paged_attention_workspace", RssmPagedDesc)):
+                       ("rssm_paged_attention_workspace", RssmPagedDesc),
+                       ("rssm_selective_scan_workspace", RssmScanDesc),
+                       ("rssm_pages_workspace", RssmPagesDesc)):
         fn = getattr(lib, name)
         fn.argtypes = [ctypes.POINTER(desc), ctypes.POINTER(ctypes.c_int64)]
         fn.restype = ctypes.c_int
@@ -896,6 +963,381 @@ def rssm_block_norm(y, residual, residual_out, normed=None, *, z=None, post_weig
                          _vec(pre_weight, "pre_weight", f32, C, dev),
                          _vec(channel_scale, "channel_scale", f32, C, dev), op, np_)
     _launch(_lib.rssm_block_norm, desc, tab, dev, stream)
+
+
+def _conv_marshal(x, weight, y, state, slots, seq_start=None, bias=None, load_state=None, silu: bool = True,
+                  pad_slot_id: int = -1):
+    import torch
+    dev = _device_index(x, "x")
+    if x.dim() != 2 or weight.dim() != 2 or state.dim() != 3 or slots.dim() != 1:
+        raise ValueError("x must be [tokens, channels], weight [width, channels], state [slots, width - 1, channels] and "
+                         "slots [sequences]")
+    f32, i32, dt = torch.float32, torch.int32, x.dtype
+    (N, C), W, S, R = x.shape, weight.shape[0], state.shape[0], slots.shape[0]
+    xp, xs = _rows(x, "x", dt, (N, C), C, dev)
+    yp, ys = _rows(y, "y", dt, (N, C), C, dev)
+    sp, ss = _rows(state, "state", dt, (S, W - 1, C), (W - 1) * C, dev)
+    if _device_index(weight, "weight") != dev:
+        raise ValueError(f"weight must be on cuda:{dev} (got {weight.device})")
+    desc = RssmConvDesc(R, _scalar("num_tokens", N), _scalar("channels", C), W, _scalar("num_slots", S),
+                        _scalar("pad_slot_id", pad_slot_id), _code(dt), 1 if silu else 0, ss, xs, ys)
+    tab = RssmConvTables(xp, _ptr(weight, "weight", f32, (W, C)), _vec(bias, "bias", f32, C, dev), yp, sp,
+                         _vec(slots, "slots", i32, R, dev), _vec(seq_start, "seq_start", i32, R + 1, dev),
+                         _vec(load_state, "load_state", i32, R, dev))
+    return desc, tab, dev
+
+
+def rssm_causal_conv(x, weight, y, state, slots, seq_start, *, bias=None, load_state=None, silu: bool = True,
+                     pad_slot_id: int = -1, stream=None) -> None:
+    """Enqueue the short causal convolution in front of a mixer over ragged
+    prompts: y_t = silu(bias + sum_k weight[k] x_{t - W + 1 + k}) channel by
+    channel.  x, y [N, C] (rows may be views of wider ones; y may not be x),
+    weight fp32 [W, C] (W 2 to 4), state pool [slots, W - 1, C] of x's dtype
+    (the last inputs of each sequence, oldest first, updated in place), slots
+    int32 [R], seq_start int32 [R + 1].  Keywords: bias fp32 [C], load_state
+    int32 [R] (0: zeros before the sequence), silu=True, pad_slot_id=-1."""
+    if stream is None:
+        mod, device, current = _fast()
+        i = device()
+        if mod.causal_conv(i, current(i), False, x, weight, y, state, slots, seq_start, bias, load_state, silu,
+                           pad_slot_id):
+            return
+    desc, tab, dev = _conv_marshal(x, weight, y, state, slots, seq_start, bias, load_state, silu, pad_slot_id)
+    _launch(_lib.rssm_causal_conv, desc, tab, dev, stream)
+
+
+def rssm_causal_conv_step(x, weight, y, state, slots, *, bias=None, silu: bool = True, pad_slot_id: int = -1,
+                          stream=None) -> None:
+    """Enqueue the single-token form: row r of x and y is request r's token (y
+    may be x).  Arguments as rssm_causal_conv without seq_start and load_state."""
+    if stream is None:
+        mod, device, current = _fast()
+        i = device()
+        if mod.causal_conv(i, current(i), True, x, weight, y, state, slots, None, bias, None, silu, pad_slot_id):
+            return
+    desc, tab, dev = _conv_marshal(x, weight, y, state, slots, None, bias, None, silu, pad_slot_id)
+    _launch(_lib.rssm_causal_conv_step, desc, tab, dev, stream)
+
+
+def _scan_marshal(state, A, x, B, C, dt, y, slots, seq_start=None, max_seq_len=1, load_state=None, D=None,
+                  dt_bias=None, z=None, dt_softplus: bool = True, pad_slot_id: int = -1):
+    import torch
+    dev = _device_index(state, "state")
+    if state.dim() != 3:
+        raise ValueError("state must be a pool [slots, channels, dstate]")
+    if x.dim() != 2 or B.dim() != 3 or slots.dim() != 1:
+        raise ValueError("x must be [tokens, channels], B [tokens, groups, dstate] and slots [sequences]")
+    S, Ch, n = state.shape
+    N, G, R = x.shape[0], B.shape[1], slots.shape[0]
+    f32, i32, idt = torch.float32, torch.int32, x.dtype
+    sp, ss = _rows(state, "state", state.dtype, (S, Ch, n), Ch * n, dev)
+    shape, bshape = (N, Ch), (N, G, n)
+    xp, xs = _rows(x, "x", idt, shape, Ch, dev)
+    dp, ds = _rows(dt, "dt", idt, shape, Ch, dev)
+    Bp, Bs = _rows(B, "B", idt, bshape, G * n, dev)
+    Cp, Cs = _rows(C, "C", idt, bshape, G * n, dev)
+    yp, ys = _rows(y, "y", idt, shape, Ch, dev)
+    zp, zs = _rows(z, "z", idt, shape, Ch, dev) if z is not None else (None, xs)
+    if _device_index(A, "A") != dev:
+        raise ValueError(f"A must be on cuda:{dev} (got {A.device})")
+    desc = RssmScanDesc(R, _scalar("num_tokens", N), _scalar("channels", Ch), _scalar("groups", G), n, _scalar("num_slots", S),
+                        _scalar("pad_slot_id", pad_slot_id), _scalar("max_seq_len", max_seq_len), _code(state.dtype),
+                        _code(idt), 1 if dt_softplus else 0, 0, ss, xs, ds, Bs, Cs, zs, ys, 0)
+    tab = RssmScanTables(
+        sp, _ptr(A, "A", f32, (Ch, n)), _vec(D, "D", f32, Ch, dev), _vec(dt_bias, "dt_bias", f32, Ch, dev), xp, dp, Bp, Cp, zp,
+        yp, _vec(slots, "slots", i32, R, dev), _vec(seq_start, "seq_start", i32, R + 1, dev),
+        _vec(load_state, "load_state", i32, R, dev), None)
+    return desc, tab, dev
+
+
+def rssm_selective_scan(state, A, x, B, C, dt, y, slots, seq_start, *, max_seq_len: int, load_state=None, D=None,
+                        dt_bias=None, z=None, dt_softplus: bool = True, pad_slot_id: int = -1, workspace=None,
+                        stream=None) -> None:
+    """Enqueue the selective state-space scan over ragged prompts (one layer): a
+    step size for each channel, a decay for each channel and state.  state pool
+    [slots, channels, dstate] (f32/bf16/f16, updated in place; dstate 16, 32 or
+    64), A fp32 [channels, dstate], x, dt (raw) and y [N, channels], B / C [N,
+    groups, dstate] of x's dtype, slots int32 [R], seq_start int32 [R + 1].
+    Rows of x, dt, B, C, z and y may be views of a wider row.  Keywords:
+    max_seq_len (required, the longest sequence), load_state int32 [R] (0: start
+    from a zero state), D, dt_bias fp32 [channels], z, dt_softplus=True,
+    pad_slot_id=-1, workspace (uint8 tensor of rssm_selective_scan_workspace's
+    size; allocated when needed and not given)."""
+    if stream is None:
+        mod, device, current = _fast()
+        i = device()
+        if mod.selective_scan(i, current(i), False, state, A, x, B, C, dt, y, slots, seq_start, max_seq_len, load_state,
+                              D, dt_bias, z, dt_softplus, pad_slot_id, workspace):
+            return
+    desc, tab, dev = _scan_marshal(state, A, x, B, C, dt, y, slots, seq_start, max_seq_len, load_state, D, dt_bias, z,
+                                   dt_softplus, pad_slot_id)
+    ws = _give_workspace(desc, tab, _lib.rssm_selective_scan_workspace, workspace, dev, stream)  # noqa: F841
+    _launch(_lib.rssm_selective_scan, desc, tab, dev, stream)
+
+
+def rssm_selective_scan_workspace(state, A, x, B, C, dt, y, slots, seq_start, *, max_seq_len: int) -> int:
+    """Workspace bytes of rssm_selective_scan for these arguments."""
+    desc, _, _ = _scan_marshal(state, A, x, B, C, dt, y, slots, seq_start, max_seq_len)
+    need = ctypes.c_int64()
+    _check(_lib.rssm_selective_scan_workspace(desc, need))
+    return need.value
+
+
+def rssm_selective_scan_step(state, A, x, B, C, dt, y, slots, *, D=None, dt_bias=None, z=None,
+                             dt_softplus: bool = True, pad_slot_id: int = -1, stream=None) -> None:
+    """Enqueue the single-token form: row r of x, B, C, dt, z and y is request
+    r's token.  Arguments as rssm_selective_scan without seq_start,
+    max_seq_len, load_state and workspace."""
+    if stream is None:
+        mod, device, current = _fast()
+        i = device()
+        if mod.selective_scan(i, current(i), True, state, A, x, B, C, dt, y, slots, None, 1, None, D, dt_bias, z,
+                              dt_softplus, pad_slot_id, None):
+            return
+    desc, tab, dev = _scan_marshal(state, A, x, B, C, dt, y, slots, None, 1, None, D, dt_bias, z, dt_softplus, pad_slot_id)
+    _launch(_lib.rssm_selective_scan_step, desc, tab, dev, stream)
+
+
+def rssm_rotary_append(q, q_out, k_cache, v_cache, k_new, v_new, page_table, seq_start, kv_len, inv_freq, *,
+                       interleaved: bool = False, factor: float = 1.0, positions=None, stream=None) -> None:
+    """Enqueue rotary positions of new queries and keys, and the append of keys
+    and values to a paged cache (in place of rssm_paged_append).  q [N,
+    q_heads, head_dim] -> q_out (may be q); k_new, v_new [N, kv_heads,
+    head_dim]; rows may be views of wider ones.  Caches, page_table, seq_start
+    and kv_len as rssm_paged_append.  inv_freq fp32 [rot_dim / 2]
+    (rotary_frequencies): the first rot_dim elements of each head are turned,
+    in pairs (2i, 2i + 1) when interleaved, (i, i + rot_dim / 2) otherwise, by
+    position * inv_freq[i], and scaled by factor.  Positions are the tokens'
+    places in the cache, or positions int32 [N] if given (the angle alone).
+    q = q_out = None: no queries.  k_cache, v_cache, k_new, v_new and
+    page_table None: no keys and values; with positions seq_start and kv_len may be None then too."""
+    if stream is None:
+        mod, device, current = _fast()
+        i = device()
+        if mod.rotary_append(i, current(i), q, q_out, k_cache, v_cache, k_new, v_new, page_table, seq_start, kv_len,
+                             inv_freq, interleaved, factor, positions):
+            return
+    import torch
+    i32 = torch.int32
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if k_new is not None:
+        if k_cache is None or v_cache is None or v_new is None or page_table is None or seq_start is None or kv_len is None:
+            raise ValueError("k_new comes with v_new, k_cache, v_cache, page_table, seq_start and kv_len")
+        pd, pt, dev = _paged_caches(k_cache, v_cache, page_table, seq_start, kv_len)
+        if k_new.dim() != 3:
+            raise ValueError("k_new must be [tokens, kv_heads, head_dim]")
+        N, dt, D = k_new.shape[0], k_cache.dtype, pd.head_dim
+    else:
+        if any(t is not None for t in (k_cache, v_cache, v_new, page_table)):
+            raise ValueError("k_cache, v_cache, v_new and page_table come with k_new")
+        if q is None:
+            return
+        dev = _device_index(q, "q")
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, q_heads, head_dim]")
+        N, dt, D = q.shape[0], q.dtype, q.shape[2]
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot_dim / 2]")
+    desc = RssmRotaryDesc(head_dim=D, rot_dim=2 * inv_freq.shape[0], interleaved=1 if interleaved else 0, dtype=_code(dt),
+                          factor=float(factor), num_tokens=_scalar("num_tokens", N))
+    tab = RssmRotaryTables(inv_freq=_vec(inv_freq, "inv_freq", torch.float32, inv_freq.shape[0], dev),
+                           positions=_vec(positions, "positions", i32, N, dev))
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, q_heads, head_dim]")
+        H = q.shape[1]
+        tab.q, desc.q_token_stride = _rows(q, "q", dt, (N, H, D), H * D, dev)
+        tab.q_out, desc.q_out_token_stride = _rows(q_out, "q_out", dt, (N, H, D), H * D, dev)
+        desc.num_q_heads = _scalar("q_heads", H)
+    if k_new is not None:
+        H = pd.num_kv_heads
+        tab.k_new, desc.k_token_stride = _rows(k_new, "k_new", dt, (N, H, D), H * D, dev)
+        tab.v_new, desc.v_token_stride = _rows(v_new, "v_new", dt, (N, H, D), H * D, dev)
+        for f in ("num_seqs", "num_kv_heads", "page_size", "num_pages", "max_pages", "page_stride", "row_stride",
+                  "head_stride", "table_stride"):
+            setattr(desc, f, getattr(pd, f))
+        for f in ("k_cache", "v_cache", "page_table", "seq_start", "kv_len"):
+            setattr(tab, f, getattr(pt, f))
+    elif seq_start is not None or kv_len is not None or positions is None:
+        if seq_start is None or kv_len is None:
+            raise ValueError("positions, or seq_start and kv_len, are needed")
+        if kv_len.dim() != 1:
+            raise ValueError("kv_len must be [sequences]")
+        desc.num_seqs = _scalar("num_seqs", kv_len.shape[0])
+        tab.seq_start = _vec(seq_start, "seq_start", i32, desc.num_seqs + 1, dev)
+        tab.kv_len = _vec(kv_len, "kv_len", i32, desc.num_seqs, dev)
+    _launch(_lib.rssm_rotary_append, desc, tab, dev, stream)
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, scale: float = 1.0, kind: str = "linear",
+                       trained: int = 0, slow: float = 1.0, fast: float = 32.0, device=None):
+    """(inv_freq, factor) for rssm_rotary_append: base ** (-2 i / rot_dim), for
+    contexts `scale` times the trained one adjusted by `kind`:
+      linear  all frequencies divided by scale (positions squeezed);
+      base    the base raised so that the slowest pair is scale times slower and the
+              fastest keeps its frequency;
+      blend   pairs of at most `slow` turns in `trained` positions divided by scale,
+              those of at least `fast` turns kept, evenly in between, and the
+              factor 0.1 ln(scale) + 1 on queries and keys (1 for scale <= 1)."""
+    import math
+    import torch
+    if rot_dim < 2 or rot_dim % 2 != 0:
+        raise ValueError(f"rot_dim must be even and positive (got {rot_dim})")
+    if not base > 0 or not scale > 0 or not math.isfinite(base) or not math.isfinite(scale):
+        raise ValueError("base and scale must be positive and finite")
+    half, factor = rot_dim // 2, 1.0
+    if kind == "base" and rot_dim > 2:
+        base = base * scale ** (rot_dim / (rot_dim - 2))
+    f = torch.tensor(float(base), dtype=torch.float64) ** (-torch.arange(half, dtype=torch.float64) / half)
+    if kind == "linear":
+        f = f / scale
+    elif kind == "blend":
+        if trained < 1 or not 0 < slow < fast:
+            raise ValueError("blend needs the trained length and 0 < slow < fast")
+        keep = ((trained * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / scale)
+        factor = 0.1 * math.log(scale) + 1.0 if scale > 1 else 1.0
+    elif kind != "base":
+        raise ValueError(f"unknown kind {kind!r} (linear, base, blend)")
+    return f.float().to(device) if device is not None else f.float(), factor
+
+
+def _pages_rows(page_table, kv_len, page_ref, page_size: int):
+    """Descriptor and table fields of a page pool."""
+    import torch
+    i32 = torch.int32
+    dev = _device_index(page_table, "page_table")
+    if page_table.dim() != 2 or page_table.dtype != i32 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be int32 [rows, pages] on cuda:{dev} with dense rows")
+    if kv_len.dim() != 1 or page_ref.dim() != 1:
+        raise ValueError("kv_len must be [rows] and page_ref [pages]")
+    rows, most = page_table.shape
+    desc = RssmPagesDesc(num_rows=_scalar("rows", rows), max_pages=_scalar("page_table columns", most),
+                         num_pages=_scalar("pages", page_ref.shape[0]), page_size=_scalar("page_size", page_size),
+                         table_stride=page_table.stride(0) if rows > 1 else most)
+    tab = RssmPagesTables(page_table=page_table.data_ptr(), kv_len=_vec(kv_len, "kv_len", i32, rows, dev),
+                          page_ref=_vec(page_ref, "page_ref", i32, page_ref.shape[0], dev))
+    return desc, tab, dev
+
+
+def _pages_items(desc, tab, dev, dst, dst_name, **others) -> None:
+    import torch
+    if dst.dim() != 1:
+        raise ValueError(f"{dst_name} must be one-dimensional")
+    n = dst.shape[0]
+    desc.num_items = _scalar("items", n)
+    tab.dst = _vec(dst, dst_name, torch.int32, n, dev)
+    for name, (field, t) in others.items():
+        setattr(tab, field, _vec(t, name, torch.int32, n, dev))
+
+
+def _pages_caches(desc, tab, dev, cache_ptrs, page_bytes: int, page_stride, token_bytes: int = 0) -> None:
+    import torch
+    if cache_ptrs.dim() != 1:
+        raise ValueError("cache_ptrs must be [caches]")
+    desc.num_caches = _scalar("caches", cache_ptrs.shape[0])
+    tab.cache_ptrs = _vec(cache_ptrs, "cache_ptrs", torch.int64, cache_ptrs.shape[0], dev)
+    desc.page_bytes = int(page_bytes)
+    desc.page_stride = int(page_bytes if page_stride is None else page_stride)
+    desc.token_bytes = int(token_bytes)
+
+
+def _pages_workspace(desc, tab, given, dev, stream):
+    return _give_workspace(desc, tab, _lib.rssm_pages_workspace, given, dev, stream)
+
+
+def rssm_page_extend(page_table, kv_len, page_ref, rows, add, status, *, page_size: int, workspace=None,
+                     stream=None) -> None:
+    """Enqueue the growth of rows by add[i] tokens: the pages they lack are
+    taken from the free ones (page_ref 0), lowest first, in the items' order, and kv_len
+    is advanced.  page_table int32 [R, pages] (-1 where none), kv_len int32
+    [R], page_ref int32 [P]; rows, add and status int32 [n].  status[i]:
+    RSSM_PAGE_OK, or RSSM_PAGE_NONE (too few free pages), RSSM_PAGE_REFUSED (bad or repeated row, bad length)
+    or RSSM_PAGE_SHARED (the partly filled last page belongs to another row too), and the row is as it was.  workspace: uint8
+    tensor of rssm_pages_workspace's size; allocated when not given."""
+    if stream is None:
+        mod, device, current = _fast()
+        i = device()
+        if mod.page_extend(i, current(i), page_table, kv_len, page_ref, rows, add, status, page_size, workspace):
+            return
+    desc, tab, dev = _pages_rows(page_table, kv_len, page_ref, page_size)
+    _pages_items(desc, tab, dev, rows, "rows", add=("lengths", add), status=("status", status))
+    ws = _pages_workspace(desc, tab, workspace, dev, stream)  # noqa: F841
+    _launch(_lib.rssm_page_extend, desc, tab, dev, stream)
+
+
+def rssm_page_fork(cache_ptrs, page_table, kv_len, page_ref, src, dst, status, *, page_size: int, page_bytes: int,
+                   page_stride=None, token_bytes: int = 0, lengths=None, workspace=None, stream=None) -> None:
+    """Enqueue forks: the empty rows dst[i] become the first lengths[i] tokens
+    (default: all) of rows src[i].  Full pages are shared; of a last page that
+    is not full the tokens are copied, in every cache, to a page of the fork's
+    own.  cache_ptrs int64 [caches]: device addresses of page 0 (pointer_table);
+    page_bytes of each page, page_stride between them (default page_bytes),
+    token_bytes when a page holds its tokens one after another (copies the filled
+    ones alone).  Tables, status and workspace as rssm_page_extend."""
+    if stream is None:
+        mod, device, current = _fast()
+        i = device()
+        if mod.page_fork(i, current(i), cache_ptrs, page_table, kv_len, page_ref, src, dst, status, page_size, page_bytes,
+                         page_bytes if page_stride is None else page_stride, token_bytes, lengths, workspace):
+            return
+    desc, tab, dev = _pages_rows(page_table, kv_len, page_ref, page_size)
+    _pages_items(desc, tab, dev, dst, "dst", src=("src", src), lengths=("lengths", lengths), status=("status", status))
+    _pages_caches(desc, tab, dev, cache_ptrs, page_bytes, page_stride, token_bytes)
+    ws = _pages_workspace(desc, tab, workspace, dev, stream)  # noqa: F841
+    _launch(_lib.rssm_page_fork, desc, tab, dev, stream)
+
+
+def rssm_page_release(page_table, kv_len, page_ref, rows, *, page_size: int, lengths=None, stream=None) -> None:
+    """Enqueue the release of rows: they keep their first lengths[i] tokens
+    (default: none), pages past them are given back."""
+    if stream is None:
+        mod, device, current = _fast()
+        i = device()
+        if mod.page_release(i, current(i), page_table, kv_len, page_ref, rows, page_size, lengths):
+            return
+    desc, tab, dev = _pages_rows(page_table, kv_len, page_ref, page_size)
+    _pages_items(desc, tab, dev, rows, "rows", lengths=("lengths", lengths))
+    _launch(_lib.rssm_page_release, desc, tab, dev, stream)
+
+
+def rssm_page_compact(cache_ptrs, page_table, kv_len, page_ref, live, *, page_size: int, page_bytes: int,
+                      page_stride=None, workspace=None, stream=None) -> None:
+    """Enqueue the packing of the pool: pages in use move to the front in every
+    cache, page_table and page_ref follow, live int32 [1] gets their number.
+    Other arguments as rssm_page_fork."""
+    if stream is None:
+        mod, device, current = _fast()
+        i = device()
+        if mod.page_compact(i, current(i), cache_ptrs, page_table, kv_len, page_ref, live, page_size, page_bytes,
+                            page_bytes if page_stride is None else page_stride, workspace):
+            return
+    import torch
+    desc, tab, dev = _pages_rows(page_table, kv_len, page_ref, page_size)
+    _pages_caches(desc, tab, dev, cache_ptrs, page_bytes, page_stride)
+    tab.live = _vec(live, "live", torch.int32, 1, dev)
+    ws = _pages_workspace(desc, tab, workspace, dev, stream)  # noqa: F841
+    _launch(_lib.rssm_page_compact, desc, tab, dev, stream)
+
+
+def rssm_page_copy(cache_ptrs, src, dst, *, num_pages: int, page_bytes: int, page_stride=None, stream=None) -> None:
+    """Enqueue copies of pages src[i] to pages dst[i] (int32 [n]) in every cache."""
+    dev = _device_index(dst, "dst")
+    desc, tab = RssmPagesDesc(num_pages=_scalar("num_pages", num_pages)), RssmPagesTables()
+    _pages_items(desc, tab, dev, dst, "dst", src=("src", src))
+    _pages_caches(desc, tab, dev, cache_ptrs, page_bytes, page_stride)
+    _launch(_lib.rssm_page_copy, desc, tab, dev, stream)
+
+
+def rssm_pages_workspace(*, num_items: int, num_rows: int, num_pages: int) -> int:
+    """Workspace bytes of rssm_page_extend, rssm_page_fork and rssm_page_compact (num_items 0)."""
+    desc = RssmPagesDesc(num_items=_scalar("num_items", num_items), num_rows=_scalar("num_rows", num_rows),
+                         num_pages=_scalar("num_pages", num_pages), max_pages=1, page_size=1, table_stride=1)
+    need = ctypes.c_int64()
+    _check(_lib.rssm_pages_workspace(desc, need))
+    return need.value
+
 
 
 def rssm_pool_alloc(nbytes: int):

@@ -32,7 +32,9 @@ SOURCES = ["rssm_inst_f32.hip", "rssm_inst_bf16.hip", "rssm_inst_f16.hip", "rssm
            "rssm_inst_linattn_f32.hip", "rssm_inst_linattn_bf16.hip", "rssm_inst_linattn_f16.hip",
            "rssm_inst_paged_f32.hip", "rssm_inst_paged_bf16.hip", "rssm_inst_paged_f16.hip",
            "rssm_inst_norm_f32.hip", "rssm_inst_norm_bf16.hip", "rssm_inst_norm_f16.hip",
-           "rssm_linear_attention.hip", "rssm_paged_attention.hip", "rssm_block_norm.hip"]
+           "rssm_inst_scan_f32.hip", "rssm_inst_scan_bf16.hip", "rssm_inst_scan_f16.hip",
+           "rssm_linear_attention.hip", "rssm_paged_attention.hip", "rssm_block_norm.hip", "rssm_causal_conv.hip",
+           "rssm_selective_scan.hip", "rssm_rotary.hip", "rssm_pages.hip"]
 POOL_SOURCES = ["rssm_pool.hip"]
 # the binding's marshalling extension (host code against torch's headers)
 FAST_SOURCE = "fast_calls.cpp"

@@ -20,8 +20,12 @@
 #include <initializer_list>
 
 #include "rssm_block_norm.h"
+#include "rssm_causal_conv.h"
 #include "rssm_linear_attention.h"
 #include "rssm_paged_attention.h"
+#include "rssm_pages.h"
+#include "rssm_rotary.h"
+#include "rssm_selective_scan.h"
 
 namespace {
 
@@ -286,11 +290,262 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (device, stream, step, x, weight, y, state, slots, seq_start, bias, load_state, silu, pad_slot_id)
+PyObject* causal_conv(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, [&] {
+    need(n == 13);
+    const int dev = i32(a[0]);
+    const bool step = a[2] == Py_True;
+    const at::Tensor &x = tensor(a[3], dev), &w = tensor(a[4], dev), &state = tensor(a[6], dev), &slots = tensor(a[7], dev);
+    need(x.dim() == 2 && w.dim() == 2 && state.dim() == 3 && slots.dim() == 1);
+    const int64_t N = x.size(0), C = x.size(1), W = w.size(0), S = state.size(0), R = slots.size(0);
+    const at::ScalarType it = x.scalar_type();
+    rssm_causal_conv_desc d{};
+    d.num_seqs = i32(R);
+    d.num_tokens = i32(N);
+    d.channels = i32(C);
+    d.width = i32(W);
+    d.num_slots = i32(S);
+    d.pad_slot_id = i32(a[12]);
+    d.dtype = code_of(it);
+    d.silu = PyObject_IsTrue(a[11]) == 1;
+    d.state_slot_stride = (W - 1) * C;
+    d.x_token_stride = d.y_token_stride = C;
+    rssm_causal_conv_tables t{};
+    t.x = x.data_ptr();
+    t.weight = static_cast<const float*>(addr(a[4], dev, at::kFloat, {W, C}));
+    t.bias = static_cast<const float*>(opt(a[9], dev, at::kFloat, {C}));
+    t.y = addr(a[5], dev, it, {N, C});
+    t.state = addr(a[6], dev, it, {S, W - 1, C});
+    t.slots = static_cast<const int32_t*>(addr(a[7], dev, at::kInt, {R}));
+    if (step) return rssm_causal_conv_step(&d, &t, stream(a[1])) == RSSM_OK;
+    t.seq_start = static_cast<const int32_t*>(addr(a[8], dev, at::kInt, {R + 1}));
+    t.load_state = static_cast<const int32_t*>(opt(a[10], dev, at::kInt, {R}));
+    return rssm_causal_conv(&d, &t, stream(a[1])) == RSSM_OK;
+  });
+}
+
+// (device, stream, step, state, A, x, B, C, dt, y, slots, seq_start, max_seq_len, load_state, D, dt_bias, z,
+//  dt_softplus, pad_slot_id, workspace)
+PyObject* selective_scan(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, [&] {
+    need(n == 20);
+    const int dev = i32(a[0]);
+    const bool step = a[2] == Py_True;
+    const at::Tensor &state = tensor(a[3], dev), &x = tensor(a[5], dev), &B = tensor(a[6], dev), &slots = tensor(a[10], dev);
+    need(state.dim() == 3 && x.dim() == 2 && B.dim() == 3 && slots.dim() == 1);
+    const int64_t S = state.size(0), Ch = state.size(1), ds = state.size(2), N = x.size(0), G = B.size(1), R = slots.size(0);
+    const at::ScalarType it = x.scalar_type();
+    rssm_selective_scan_desc d{};
+    d.num_seqs = i32(R);
+    d.num_tokens = i32(N);
+    d.channels = i32(Ch);
+    d.groups = i32(G);
+    d.dstate = i32(ds);
+    d.num_slots = i32(S);
+    d.pad_slot_id = i32(a[18]);
+    d.max_seq_len = i32(a[12]);
+    d.state_dtype = code_of(state.scalar_type());
+    d.input_dtype = code_of(it);
+    d.dt_softplus = PyObject_IsTrue(a[17]) == 1;
+    d.state_slot_stride = Ch * ds;
+    d.x_token_stride = d.dt_token_stride = d.z_token_stride = d.y_token_stride = Ch;
+    d.B_token_stride = d.C_token_stride = G * ds;
+    rssm_selective_scan_tables t{};
+    t.state = state.data_ptr();
+    t.A = static_cast<const float*>(addr(a[4], dev, at::kFloat, {Ch, ds}));
+    t.D = static_cast<const float*>(opt(a[14], dev, at::kFloat, {Ch}));
+    t.dt_bias = static_cast<const float*>(opt(a[15], dev, at::kFloat, {Ch}));
+    t.x = addr(a[5], dev, it, {N, Ch});
+    t.B = addr(a[6], dev, it, {N, G, ds});
+    t.C = addr(a[7], dev, it, {N, G, ds});
+    t.dt = addr(a[8], dev, it, {N, Ch});
+    t.y = addr(a[9], dev, it, {N, Ch});
+    t.z = opt(a[16], dev, it, {N, Ch});
+    t.slots = static_cast<const int32_t*>(addr(a[10], dev, at::kInt, {R}));
+    if (step) return rssm_selective_scan_step(&d, &t, stream(a[1])) == RSSM_OK;
+    t.seq_start = static_cast<const int32_t*>(addr(a[11], dev, at::kInt, {R + 1}));
+    t.load_state = static_cast<const int32_t*>(opt(a[13], dev, at::kInt, {R}));
+    int64_t bytes = 0;
+    need(rssm_selective_scan_workspace(&d, &bytes) == RSSM_OK);
+    const at::Tensor ws = workspace(a[19], bytes, dev);
+    if (ws.defined()) {
+      t.workspace = ws.data_ptr();
+      d.workspace_bytes = static_cast<int64_t>(ws.nbytes());
+    }
+    return rssm_selective_scan(&d, &t, stream(a[1])) == RSSM_OK;
+  });
+}
+
+// (device, stream, q, q_out, k_cache, v_cache, k_new, v_new, page_table, seq_start, kv_len, inv_freq, interleaved,
+//  factor, positions): queries, keys and values all there
+PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, [&] {
+    need(n == 15);
+    const int dev = i32(a[0]);
+    rssm_paged_attention_desc p{};
+    rssm_paged_attention_tables pt{};
+    at::ScalarType st;
+    caches(a[4], a[5], a[8], a[9], a[10], dev, &p, &pt, &st);
+    const at::Tensor &q = tensor(a[2], dev), &f = tensor(a[11], dev);
+    need(q.dim() == 3 && f.dim() == 1);
+    const int64_t N = q.size(0), Hq = q.size(1), D = p.head_dim, Hkv = p.num_kv_heads;
+    rssm_rotary_desc d{};
+    rssm_rotary_tables t{};
+    d.num_seqs = p.num_seqs;
+    d.num_tokens = i32(N);
+    d.num_q_heads = i32(Hq);
+    d.num_kv_heads = p.num_kv_heads;
+    d.head_dim = p.head_dim;
+    d.rot_dim = i32(2 * f.size(0));
+    d.interleaved = PyObject_IsTrue(a[12]) == 1;
+    d.page_size = p.page_size;
+    d.num_pages = p.num_pages;
+    d.max_pages = p.max_pages;
+    d.dtype = p.dtype;
+    d.factor = real(a[13]);
+    d.page_stride = p.page_stride;
+    d.row_stride = p.row_stride;
+    d.head_stride = p.head_stride;
+    d.q_token_stride = d.q_out_token_stride = Hq * D;
+    d.k_token_stride = d.v_token_stride = Hkv * D;
+    d.table_stride = p.table_stride;
+    t.q = addr(a[2], dev, st, {N, Hq, D});
+    t.q_out = addr(a[3], dev, st, {N, Hq, D});
+    t.k_new = addr(a[6], dev, st, {N, Hkv, D});
+    t.v_new = addr(a[7], dev, st, {N, Hkv, D});
+    t.k_cache = pt.k_cache;
+    t.v_cache = pt.v_cache;
+    t.page_table = pt.page_table;
+    t.seq_start = pt.seq_start;
+    t.kv_len = pt.kv_len;
+    t.positions = static_cast<const int32_t*>(opt(a[14], dev, at::kInt, {N}));
+    t.inv_freq = static_cast<const float*>(addr(a[11], dev, at::kFloat, {f.size(0)}));
+    return rssm_rotary_append(&d, &t, stream(a[1])) == RSSM_OK;
+  });
+}
+
+// The page pool's fields: page_table, kv_len, page_ref and page_size.
+void pool(PyObject* table, PyObject* kv_len, PyObject* ref, PyObject* page_size, int dev, rssm_pages_desc* d,
+          rssm_pages_tables* t) {
+  const at::Tensor &pt = tensor(table, dev), &pr = tensor(ref, dev);
+  need(pt.dim() == 2 && pt.scalar_type() == at::kInt && pr.dim() == 1 && pr.scalar_type() == at::kInt);
+  d->num_rows = i32(pt.size(0));
+  d->max_pages = i32(pt.size(1));
+  d->num_pages = i32(pr.size(0));
+  d->page_size = i32(page_size);
+  d->table_stride = pt.size(1);
+  t->page_table = static_cast<int32_t*>(pt.data_ptr());
+  t->kv_len = static_cast<int32_t*>(addr(kv_len, dev, at::kInt, {pt.size(0)}));
+  t->page_ref = static_cast<int32_t*>(pr.data_ptr());
+}
+
+int64_t items(PyObject* dst, int dev, rssm_pages_desc* d, rssm_pages_tables* t) {
+  const at::Tensor& r = tensor(dst, dev);
+  need(r.dim() == 1 && r.scalar_type() == at::kInt);
+  d->num_items = i32(r.size(0));
+  t->dst = static_cast<const int32_t*>(r.data_ptr());
+  return r.size(0);
+}
+
+int32_t* ints(PyObject* o, int dev, int64_t n) { return static_cast<int32_t*>(opt(o, dev, at::kInt, {n})); }
+
+void pool_caches(PyObject* ptrs, PyObject* page_bytes, PyObject* page_stride, int dev, rssm_pages_desc* d,
+                 rssm_pages_tables* t) {
+  const at::Tensor& p = tensor(ptrs, dev);
+  need(p.dim() == 1 && p.scalar_type() == at::kLong);
+  d->num_caches = i32(p.size(0));
+  d->page_bytes = integer(page_bytes);
+  d->page_stride = integer(page_stride);
+  t->cache_ptrs = p.data_ptr<int64_t>();
+}
+
+at::Tensor pool_workspace(PyObject* given, int dev, rssm_pages_desc* d, rssm_pages_tables* t) {
+  int64_t bytes = 0;
+  need(rssm_pages_workspace(d, &bytes) == RSSM_OK);
+  const at::Tensor ws = workspace(given, bytes, dev);
+  t->workspace = ws.data_ptr();
+  d->workspace_bytes = static_cast<int64_t>(ws.nbytes());
+  return ws;
+}
+
+// (device, stream, page_table, kv_len, page_ref, rows, add, status, page_size, workspace)
+PyObject* page_extend(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, [&] {
+    need(n == 10);
+    const int dev = i32(a[0]);
+    rssm_pages_desc d{};
+    rssm_pages_tables t{};
+    pool(a[2], a[3], a[4], a[8], dev, &d, &t);
+    const int64_t k = items(a[5], dev, &d, &t);
+    t.lengths = ints(a[6], dev, k);
+    t.status = ints(a[7], dev, k);
+    const at::Tensor ws = pool_workspace(a[9], dev, &d, &t);
+    return rssm_page_extend(&d, &t, stream(a[1])) == RSSM_OK;
+  });
+}
+
+// (device, stream, cache_ptrs, page_table, kv_len, page_ref, src, dst, status, page_size, page_bytes, page_stride,
+//  token_bytes, lengths, workspace)
+PyObject* page_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, [&] {
+    need(n == 15);
+    const int dev = i32(a[0]);
+    rssm_pages_desc d{};
+    rssm_pages_tables t{};
+    pool(a[3], a[4], a[5], a[9], dev, &d, &t);
+    const int64_t k = items(a[7], dev, &d, &t);
+    t.src = ints(a[6], dev, k);
+    t.status = ints(a[8], dev, k);
+    t.lengths = ints(a[13], dev, k);
+    pool_caches(a[2], a[10], a[11], dev, &d, &t);
+    d.token_bytes = integer(a[12]);
+    const at::Tensor ws = pool_workspace(a[14], dev, &d, &t);
+    return rssm_page_fork(&d, &t, stream(a[1])) == RSSM_OK;
+  });
+}
+
+// (device, stream, page_table, kv_len, page_ref, rows, page_size, lengths)
+PyObject* page_release(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, [&] {
+    need(n == 8);
+    const int dev = i32(a[0]);
+    rssm_pages_desc d{};
+    rssm_pages_tables t{};
+    pool(a[2], a[3], a[4], a[6], dev, &d, &t);
+    const int64_t k = items(a[5], dev, &d, &t);
+    t.lengths = ints(a[7], dev, k);
+    return rssm_page_release(&d, &t, stream(a[1])) == RSSM_OK;
+  });
+}
+
+// (device, stream, cache_ptrs, page_table, kv_len, page_ref, live, page_size, page_bytes, page_stride, workspace)
+PyObject* page_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(a, n, [&] {
+    need(n == 11);
+    const int dev = i32(a[0]);
+    rssm_pages_desc d{};
+    rssm_pages_tables t{};
+    pool(a[3], a[4], a[5], a[7], dev, &d, &t);
+    pool_caches(a[2], a[8], a[9], dev, &d, &t);
+    t.live = static_cast<int32_t*>(addr(a[6], dev, at::kInt, {1}));
+    const at::Tensor ws = pool_workspace(a[10], dev, &d, &t);
+    return rssm_page_compact(&d, &t, stream(a[1])) == RSSM_OK;
+  });
+}
+
 PyMethodDef methods[] = {
     {"linear_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(linear_attention)), METH_FASTCALL, nullptr},
     {"paged_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(paged_append)), METH_FASTCALL, nullptr},
     {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(paged_attention)), METH_FASTCALL, nullptr},
     {"block_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(block_norm)), METH_FASTCALL, nullptr},
+    {"causal_conv", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(causal_conv)), METH_FASTCALL, nullptr},
+    {"selective_scan", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(selective_scan)), METH_FASTCALL, nullptr},
+    {"rotary_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rotary_append)), METH_FASTCALL, nullptr},
+    {"page_extend", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(page_extend)), METH_FASTCALL, nullptr},
+    {"page_fork", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(page_fork)), METH_FASTCALL, nullptr},
+    {"page_release", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(page_release)), METH_FASTCALL, nullptr},
+    {"page_compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(page_compact)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

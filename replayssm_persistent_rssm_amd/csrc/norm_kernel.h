@@ -31,26 +31,6 @@ struct NormArgs {
 constexpr int kNormBlock = 256;
 constexpr int kNormMaxGroups = 256;
 
-template <int DT>
-__device__ __forceinline__ f32x8 load8(const char* p) {
-  if constexpr (DT == kF32) {
-    const f32x4 a = __builtin_bit_cast(f32x4, ld<false, u32x4>(p)), b = __builtin_bit_cast(f32x4, ld<false, u32x4>(p + 16));
-    return stack(a, b);
-  } else {
-    return from_frag<DT>(__builtin_bit_cast(typename Mma<DT>::frag, ld<false, u32x4>(p)));
-  }
-}
-
-template <int DT>
-__device__ __forceinline__ void store8(char* p, f32x8 v) {
-  if constexpr (DT == kF32) {
-    st<false>(p, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
-    st<false>(p + 16, __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]}));
-  } else {
-    st<false>(p, __builtin_bit_cast(u32x4, to_frag<DT>(v)));
-  }
-}
-
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);

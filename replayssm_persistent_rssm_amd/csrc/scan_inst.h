@@ -1,0 +1,34 @@
+// scan_inst.h -- instance selection of the selective-scan kernels for one input dtype.
+#pragma once
+
+#include "scan_kernel.h"
+
+namespace rssm {
+
+enum : int { kScanMain = 0, kScanFold = 1, kScanStepOne = 2, kScanStepFour = 3 };
+
+template <int IT, int N>
+const void* scan_fn(int which, int state_dtype) {
+  if (which == kScanMain) return reinterpret_cast<const void*>(&scan_kernel<IT, N, false>);
+  if (which == kScanFold) return reinterpret_cast<const void*>(&scan_kernel<IT, N, true>);
+  const bool four = which == kScanStepFour;
+  switch (state_dtype) {
+    case kF32:
+      return four ? reinterpret_cast<const void*>(&scan_step_kernel<IT, kF32, N, 4>)
+                  : reinterpret_cast<const void*>(&scan_step_kernel<IT, kF32, N, 1>);
+    case kBF16:
+      return four ? reinterpret_cast<const void*>(&scan_step_kernel<IT, kBF16, N, 4>)
+                  : reinterpret_cast<const void*>(&scan_step_kernel<IT, kBF16, N, 1>);
+    default:
+      return four ? reinterpret_cast<const void*>(&scan_step_kernel<IT, kF16, N, 4>)
+                  : reinterpret_cast<const void*>(&scan_step_kernel<IT, kF16, N, 1>);
+  }
+}
+
+template <int IT>
+const void* scan_pick(int which, int state_dtype, int dstate) {
+  return dstate == 16 ? scan_fn<IT, 16>(which, state_dtype)
+         : dstate == 32 ? scan_fn<IT, 32>(which, state_dtype) : scan_fn<IT, 64>(which, state_dtype);
+}
+
+}  // namespace rssm
