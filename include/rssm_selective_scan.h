@@ -38,7 +38,7 @@ extern "C" {
  *   input_dtype        x, dt, B, C, z and y: RSSM_F32 | RSSM_BF16 | RSSM_F16
  *   dt_softplus        1: d = softplus(dt + bias); 0: d = dt + bias
  *   state_slot_stride  elements between slots, >= channels * dstate
- *   *_token_stride     elements between rows of each tensor (at most 2^31); rows are dense
+ *   *_token_stride     elements between rows of each tensor (at most 2^24); rows are dense
  *                      inside, so that views of one packed projection pass
  *   workspace_bytes    bytes at tables->workspace
  * num_seqs * ceil(channels / 64) is below 2^24. */

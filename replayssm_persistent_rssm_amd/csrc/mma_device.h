@@ -253,41 +253,6 @@ __device__ __forceinline__ float silu(float v) {
   return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
 }
 
-// exp(x) from the hardware's exp2: the product x log2(e) is carried in two parts, so that
-// the result is within a few units of the last place at any x.
-__device__ __forceinline__ float exp_near(float x) {
-  const float y = x * 1.44269502f;                              // log2(e) = 1.44269502 + 1.92596e-8
-  const float r = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269502f, -y));
-  const float e = __builtin_amdgcn_exp2f(y);
-  return fabsf(y) < 150.0f ? fmaf(e, r * 0.693147181f, e) : e;   // far out: 0, infinity or NaN as it is
-}
-
-// softplus(raw + bias) = max(v, 0) + log(1 + t), t = exp(-|v|), with the sum's
-// rounding error (Knuth's TwoSum) carried to t.  log(1 + t) = 2 artanh(s), s = t / (2 + t)
-// <= 1/3, by its series up to s^15: small dt keep their relative accuracy.
-__device__ __forceinline__ float prompt_dt(float raw, float bias, int softplus) {
-  const float v = raw + bias;
-  if (!softplus) return v;
-  const float bb = v - raw;
-  // (an infinite v has no rounding error: softplus is 0 or infinity)
-  const float lo = fabsf(v) < __builtin_inff() ? (raw - (v - bb)) + (bias - bb) : 0.0f;
-  const float t0 = exp_near(-fabsf(v));
-  const float t = fmaf(t0, v > 0.0f ? -lo : lo, t0);
-  const float d = 2.0f + t;
-  float rc = __builtin_amdgcn_rcpf(d);
-  rc = fmaf(rc, fmaf(-d, rc, 1.0f), rc);
-  const float s = t * rc, q = s * s;
-  float p = 2.0f / 15.0f;
-  p = fmaf(p, q, 2.0f / 13.0f);
-  p = fmaf(p, q, 2.0f / 11.0f);
-  p = fmaf(p, q, 2.0f / 9.0f);
-  p = fmaf(p, q, 2.0f / 7.0f);
-  p = fmaf(p, q, 2.0f / 5.0f);
-  p = fmaf(p, q, 2.0f / 3.0f);
-  const float l = fmaf(s * q, p, 2.0f * s);
-  return v > 0.0f ? v + (lo + l) : l;
-}
-
 // Workgroup order that gives each of the 8 XCDs (workgroups are dealt to them in
 // turn) one contiguous range of items, so that neighbouring items, which
 // share inputs, meet in one L2.

@@ -66,7 +66,8 @@ rssm_status check_desc(const rssm_selective_scan_desc* d, bool step) {
   for (const T& t : strides) {
     if (t.v < t.least) return fail(RSSM_ERR_INVALID_ARGUMENT, "%s is below the dense row", t.n);
     if ((t.v * ib) % 16 != 0) return fail(RSSM_ERR_INVALID_ARGUMENT, "%s must be a multiple of 16 bytes", t.n);
-    if (t.v > (int64_t(1) << 31)) return fail(RSSM_ERR_INVALID_ARGUMENT, "%s exceeds 2^31 elements", t.n);
+    // 32-bit byte offsets inside a tile of 16 rows
+    if (t.v > (int64_t(1) << 24)) return fail(RSSM_ERR_INVALID_ARGUMENT, "%s exceeds 2^24 elements", t.n);
   }
   if (d->workspace_bytes < 0) return fail(RSSM_ERR_INVALID_ARGUMENT, "workspace_bytes must be >= 0");
   return RSSM_OK;
@@ -141,6 +142,7 @@ void fill_args(ScanArgs* a, const rssm_selective_scan_desc* d, const rssm_select
   a->num_seqs = d->num_seqs;
   a->num_tokens = d->num_tokens;
   a->channels = d->channels;
+  a->groups = d->groups;
   a->per_group = d->channels / d->groups;
   a->num_slots = d->num_slots;
   a->pad = d->pad_slot_id;

@@ -6,13 +6,15 @@
 // bound, and everything else is arranged so as not to add to it.
 //
 // scan_kernel: a wavefront owns 16 channels of a sequence and all their states in registers: lane 16 g + j
-// has states g N/4 .. (g + 1) N/4 - 1 of channel j.  It walks the tokens in tiles of 16.
-//  * Inputs of a tile come as lane 16 g + j = token j, channels 4g .. 4g + 3 (x, dt, z) and token j, states of
-//    group g (B, C): one load an input, each step size computed once.
+// has states 16 m + 4 g .. 16 m + 4 g + 3 of channel j.  It walks the tokens in tiles of 16.
+//  * Inputs of a tile come as lane 16 g + j = token j, channels 4g .. 4g + 3 (x, dt, z): one load an input, each step
+//    size computed once.  Rows past the end read as zeros by the size of their buffer.
 //  * Step sizes go to the channels' lanes through LDS (16 x 16 floats of the wavefront's own, no barrier).
-//  * B_t and C_t are the same for all 16 channels: the product's operand is broadcast from lane t of each row of 16
-//    by the instruction that uses it (row broadcast), at no cost.
-//  * The sums over the four groups of states are taken for four tokens at once by swapping halves and rows of lanes
+//  * d x B is an outer product of 16 channels and 16 states a token: a matrix instruction gives four tokens of it (four
+//    blocks of 16 x 16 with one product each, exact to one rounding), in the layout that the states are in.
+//  * C_t is the same for all 16 channels: it is broadcast from lane t of each row of 16 by the instruction that
+//    multiplies it (row broadcast), at no cost.
+//  * The sums over the four groups of lanes are taken for four tokens at once by swapping halves and rows of lanes
 //    (6 instructions for 4 tokens), and go back to the tile's layout through LDS for skip, gate and store.
 // When sequences and channels leave compute units empty, the token axis is split: scan_kernel<FOLD> gives
 // each stretch's own end state and the sum of its step sizes (a decay over the stretch is exp(A sum)), and
@@ -43,7 +45,7 @@ struct ScanArgs {
   float* ws_h;                // [num_seqs][nseg][channels][N] (nseg > 1)
   float* ws_d;                // [num_seqs][nseg][channels]
   int64_t state_stride, x_stride, dt_stride, B_stride, C_stride, z_stride, y_stride;   // elements
-  int32_t num_seqs, num_tokens, channels, per_group, num_slots, pad, max_seq_len, dt_softplus, state_dtype;
+  int32_t num_seqs, num_tokens, channels, groups, per_group, num_slots, pad, max_seq_len, dt_softplus, state_dtype;
   int32_t nseg, seg_len;      // stretches of the token axis and their length (a multiple of 16)
   int32_t blocks;             // channel blocks
 };
@@ -71,10 +73,6 @@ struct ScanRaw {
       }
     }
   }
-  __device__ __forceinline__ void keep(bool on) {
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) w[k] = on ? w[k] : 0u;
-  }
   __device__ __forceinline__ float get(int i) const {
     if constexpr (IT == kF32) return __uint_as_float(w[i]);
     else if constexpr (IT == kBF16) return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
@@ -86,12 +84,6 @@ struct ScanRaw {
 __device__ __forceinline__ void scan_wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
-}
-
-// v of lane T of the lane's row of 16.
-template <int T>
-__device__ __forceinline__ float row_bcast(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x150 + T, 0xf, 0xf, true));
 }
 
 // p plus (kFirst: instead of p) the sum of four products C_i h_i with C broadcast from lane T of each row.  The compiler
@@ -155,52 +147,147 @@ __device__ __forceinline__ void scan_state_store(char* base, int64_t at, int dty
 // A log2(e), with -infinity as the most negative number: a step of size 0 then decays by exp2(-0) = 1.
 __device__ __forceinline__ float scan_rate(float A) { return fmaxf(A * kLog2e, -3.40282347e38f); }
 
-template <int NS>
-struct ScanTile {
-  float dt[kScanTile], dx[kScanTile];   // of the lane's channel
-  float B[NS], C[NS];                   // of token lane % 16, the lane's group of states
+// softplus(v) = max(v, 0) + log(1 + t), t = exp(-|v|); log(1 + t) / t on [0, 1] is the polynomial through its values
+// at the ten Chebyshev points (off by 1.4e-8 of itself, 1.3e-7 with its roundings): small steps keep
+// their relative accuracy.
+__device__ __forceinline__ float scan_step_size(float raw, float bias, int softplus) {
+  const float v = raw + bias;
+  if (!softplus) return v;
+  const float t = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e);
+  float p = -0.0031760570127516985f;
+  p = fmaf(p, t, 0.019542526453733444f);
+  p = fmaf(p, t, -0.056373611092567444f);
+  p = fmaf(p, t, 0.10543623566627502f);
+  p = fmaf(p, t, -0.1526966691017151f);
+  p = fmaf(p, t, 0.1966327428817749f);
+  p = fmaf(p, t, -0.24951615929603577f);
+  p = fmaf(p, t, 0.33329710364341736f);
+  p = fmaf(p, t, -0.49999892711639404f);
+  p = fmaf(p, t, 1.0f);
+  return fmaf(p, t, fmaxf(v, 0.0f));
+}
+
+// A tensor's rows of one sequence, a tile of 16 at a time: a buffer that ends with the last row, so that loads past it
+// give 0 and stores past it are dropped.  Addresses advance in scalar registers.
+struct ScanRows {
+  const char* at;          // first row of the tile
+  uint32_t step, width;    // bytes between rows (at most 2^26) and in one
+  __device__ __forceinline__ void start(const char* base, int64_t row, int64_t stride, int width_bytes, int es) {
+    at = base + row * stride * es;
+    step = static_cast<uint32_t>(stride * es);
+    width = static_cast<uint32_t>(width_bytes);
+  }
+  __device__ __forceinline__ rsrc_t tile(int rows) const {
+    return make_rsrc(at, (static_cast<uint32_t>(rows < kScanTile ? rows : kScanTile) - 1) * step + width);
+  }
+  __device__ __forceinline__ void next() { at += static_cast<int64_t>(kScanTile) * step; }
 };
 
-// Tokens T .. of a tile: the states move on, p[t] is the lane's part of y_t.
-template <int NS, bool FOLD, int T>
-__device__ __forceinline__ float scan_token(const ScanTile<NS>& k, const float (&A)[NS], float (&h)[NS]) {
+// 4 elements in storage, at a byte offset of a buffer.
+template <int IT>
+struct ScanFour {
+  static constexpr int kWords = static_cast<int>(sizeof(typename Mma<IT>::elem));
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(rsrc_t r, uint32_t off) {
+    if constexpr (IT == kF32) {
+      const u32x4 v = bload16<false>(r, off, 0);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+      const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+      w[0] = v.x, w[1] = v.y;
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (IT == kF32) return __uint_as_float(w[i]);
+    else if constexpr (IT == kBF16) return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    else return f16_bits_to_float(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
+  }
+};
+
+template <int IT>
+__device__ __forceinline__ uint32_t scan_one_load(rsrc_t r, uint32_t off) {
+  if constexpr (IT == kF32) return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+  else return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+}
+template <int IT>
+__device__ __forceinline__ float scan_one(uint32_t w) {
+  if constexpr (IT == kF32) return __uint_as_float(w);
+  else return elem_to_float<IT>(static_cast<uint16_t>(w));
+}
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr uint32_t kScanNowhere = 0xfffffff0u;   // offset past every buffer
+
+// Sequence with the rank-th longest row range (ties: lower index first), for at most 64 sequences: the long ones start
+// first, so that they do not run alone at the end.
+__device__ __forceinline__ int scan_by_length(const ScanArgs& a, int rank, int lane) {
+  int len = -1;
+  if (lane < a.num_seqs) len = gload(a.seq_start + lane + 1) - gload(a.seq_start + lane);
+  int before = 0;
+  for (int i = 0; i < a.num_seqs; ++i) {
+    const int other = __builtin_amdgcn_readlane(len, i);
+    before += other > len || (other == len && i < lane) ? 1 : 0;
+  }
+  return __builtin_ctzll(__ballot(lane < a.num_seqs && before == rank));
+}
+
+template <int M>
+struct ScanState {
+  float A[4 * M], h[4 * M];
+};
+
+// Token T of a tile: the states move on; the lane's part of y_t.
+template <int M, bool FOLD, int T>
+__device__ __forceinline__ float scan_token(const float (&dt)[kScanTile], const float (&C)[4 * M], const f32x16 (&u)[M],
+                                            ScanState<M>& s) {
   float p = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const float e = __builtin_amdgcn_exp2f(k.dt[T] * A[i]);
-    h[i] = fmaf(e, h[i], row_bcast<T>(k.B[i]) * k.dx[T]);
-  }
-  if constexpr (!FOLD) {
-    p = scan_dot4<T, true>(p, k.C, h);
+  for (int m = 0; m < M; ++m) {
 #pragma unroll
-    for (int i = 4; i < NS; i += 4) p = scan_dot4<T, false>(p, k.C + i, h + i);
+    for (int i = 0; i < 4; ++i) {
+      const float e = __builtin_amdgcn_exp2f(dt[T] * s.A[4 * m + i]);
+      s.h[4 * m + i] = fmaf(e, s.h[4 * m + i], u[m][4 * (T & 3) + i]);
+    }
+    if constexpr (!FOLD) p = m == 0 ? scan_dot4<T, true>(p, C, s.h) : scan_dot4<T, false>(p, C + 4 * m, s.h + 4 * m);
   }
   return p;
 }
 
-template <int NS, bool FOLD, int Q>
-__device__ __forceinline__ float scan_four(const ScanTile<NS>& k, const float (&A)[NS], float (&h)[NS]) {
-  const float p0 = scan_token<NS, FOLD, 4 * Q>(k, A, h);
-  const float p1 = scan_token<NS, FOLD, 4 * Q + 1>(k, A, h);
-  const float p2 = scan_token<NS, FOLD, 4 * Q + 2>(k, A, h);
-  const float p3 = scan_token<NS, FOLD, 4 * Q + 3>(k, A, h);
+// Tokens 4 Q .. 4 Q + 3.  B: of token 4 Q + g, states 16 m + j; dx: of token 4 Q + g, channel j.
+template <int M, bool FOLD, int Q>
+__device__ __forceinline__ float scan_four(const float (&dt)[kScanTile], const float (&B)[4][M], const float (&dx)[4],
+                                           const float (&C)[4 * M], ScanState<M>& s) {
+  f32x16 u[M];
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const f32x16 zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    u[m] = __builtin_amdgcn_mfma_f32_16x16x1f32(B[Q][m], dx[Q], zero, 0, 0, 0);
+  }
+  const float p0 = scan_token<M, FOLD, 4 * Q>(dt, C, u, s);
+  const float p1 = scan_token<M, FOLD, 4 * Q + 1>(dt, C, u, s);
+  const float p2 = scan_token<M, FOLD, 4 * Q + 2>(dt, C, u, s);
+  const float p3 = scan_token<M, FOLD, 4 * Q + 3>(dt, C, u, s);
   if constexpr (FOLD) return 0.0f;
   return rows_sum(halves_sum(p0, p2), halves_sum(p1, p3));   // row g: token 4 Q + g
 }
 
 template <int IT, int N, bool FOLD>
-__global__ __launch_bounds__(kScanBlock) void scan_kernel(ScanArgs a) {
+__global__ __launch_bounds__(kScanBlock, 2) void scan_kernel(ScanArgs a) {
   constexpr int es = sizeof(typename Mma<IT>::elem);
-  constexpr int NS = N / 4;
+  constexpr int M = N / 16;
   __shared__ alignas(16) float lds[kScanBlock / 64][3][kScanTile * kScanPitch];
   const int tid = threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int u = blockIdx.x;
-  const int c0 = (u % a.blocks) * kScanChannels + wave * 16;
-  u /= a.blocks;
-  const int seg = u % a.nseg, s = u / a.nseg;
+  int b = blockIdx.x;
+  const int c0 = (b % a.blocks) * kScanChannels + wave * 16;
+  b /= a.blocks;
+  const int seg = b % a.nseg;
+  int s = b / a.nseg;
+  if (c0 >= a.channels) return;
+  if (a.num_seqs > 1 && a.num_seqs <= 64) s = scan_by_length(a, s, lane);
   const int slot = sload(a.slots + s);
-  if (slot == a.pad || slot < 0 || slot >= a.num_slots || c0 >= a.channels) return;
+  if (slot == a.pad || slot < 0 || slot >= a.num_slots) return;
   int start = sload(a.seq_start + s), end = sload(a.seq_start + s + 1);
   start = start < 0 ? 0 : (start > a.num_tokens ? a.num_tokens : start);
   end = end < start ? start : (end > a.num_tokens ? a.num_tokens : end);
@@ -212,24 +299,25 @@ __global__ __launch_bounds__(kScanBlock) void scan_kernel(ScanArgs a) {
 
   const int cj = c0 + j, cg = c0 + 4 * g;                     // the lane's channel, its first channel of a tile's inputs
   const bool has_j = cj < a.channels, has_g = cg < a.channels;
-  const int64_t st0 = slot * a.state_stride + static_cast<int64_t>(cj) * N + g * NS;
-  float A[NS], h[NS];
+  const int64_t st0 = slot * a.state_stride + static_cast<int64_t>(cj) * N + 4 * g;
+  ScanState<M> st;
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    A[i] = has_j ? scan_rate(gload(a.A + static_cast<int64_t>(cj) * N + g * NS + i)) : 0.0f;
-    h[i] = 0.0f;
+  for (int i = 0; i < 4 * M; ++i) {
+    const int n0 = 16 * (i / 4) + i % 4;                      // state of the lane's group
+    st.A[i] = has_j ? scan_rate(gload(a.A + static_cast<int64_t>(cj) * N + 4 * g + n0)) : 0.0f;
+    st.h[i] = 0.0f;
   }
   if (!FOLD && has_j) {
     if (a.load_state == nullptr || sload(a.load_state + s) != 0) {
 #pragma unroll
-      for (int i = 0; i < NS; ++i) h[i] = scan_state_load(a.state, st0 + i, a.state_dtype);
+      for (int i = 0; i < 4 * M; ++i) st.h[i] = scan_state_load(a.state, st0 + 16 * (i / 4) + i % 4, a.state_dtype);
     }
     for (int k = 0; k < seg; ++k) {
       const int64_t at = (static_cast<int64_t>(s) * a.nseg + k) * a.channels + cj;
       const float sum = gload(a.ws_d + at);
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
-        h[i] = fmaf(__builtin_amdgcn_exp2f(sum * A[i]), h[i], gload(a.ws_h + at * N + g * NS + i));
+      for (int i = 0; i < 4 * M; ++i)
+        st.h[i] = fmaf(__builtin_amdgcn_exp2f(sum * st.A[i]), st.h[i], gload(a.ws_h + at * N + 4 * g + 16 * (i / 4) + i % 4));
     }
   }
   float bias[4], D[4], dsum[4] = {0, 0, 0, 0};
@@ -238,69 +326,87 @@ __global__ __launch_bounds__(kScanBlock) void scan_kernel(ScanArgs a) {
     bias[r] = a.dt_bias != nullptr && has_g ? gload(a.dt_bias + cg + r) : 0.0f;
     D[r] = a.D != nullptr && has_g ? gload(a.D + cg + r) : 0.0f;
   }
-  // rows of the lane's token and of the first tile; channels past the end read channel block c0
-  const int col = has_g ? cg : c0;
-  const int64_t row = static_cast<int64_t>(c0 / a.per_group) * N + g * NS;
-  const char* xp = a.x + (tok * a.x_stride + col) * es;
-  const char* dp = a.dt + (tok * a.dt_stride + col) * es;
-  const char* zp = a.z != nullptr ? a.z + (tok * a.z_stride + col) * es : nullptr;
-  const char* Bp = a.B + (tok * a.B_stride + row) * es;
-  const char* Cp = a.C + (tok * a.C_stride + row) * es;
-  char* yp = a.y + (tok * a.y_stride + col) * es;
-  ScanRaw<IT, 4> rx, rd, rz;
-  ScanRaw<IT, NS> rB, rC;
-  rz.keep(false);
-  const auto fetch = [&](int t0) {
-    const int64_t t = t0 + j < n ? t0 + j : n - 1;
-    rx.load(xp + t * a.x_stride * es);
-    rd.load(dp + t * a.dt_stride * es);
-    rB.load(Bp + t * a.B_stride * es);
+  const int gN = a.groups * N;
+  ScanRows xr, dr, zr, Br, Cr, yr;
+  xr.start(a.x, tok, a.x_stride, a.channels * es, es);
+  dr.start(a.dt, tok, a.dt_stride, a.channels * es, es);
+  Br.start(a.B, tok, a.B_stride, gN * es, es);
+  const bool gated = a.z != nullptr;
+  if constexpr (!FOLD) {
+    Cr.start(a.C, tok, a.C_stride, gN * es, es);
+    yr.start(a.y, tok, a.y_stride, a.channels * es, es);
+    zr.start(gated ? a.z : a.x, tok, gated ? a.z_stride : a.x_stride, a.channels * es, es);
+  }
+  const uint32_t row = static_cast<uint32_t>(c0 / a.per_group) * N;
+  const uint32_t xo = has_g ? j * xr.step + cg * es : kScanNowhere, dto = has_g ? j * dr.step + cg * es : kScanNowhere;
+  const uint32_t Bo = g * Br.step + (row + j) * es;
+  uint32_t zo = 0, yo = 0, Co = 0;
+  if constexpr (!FOLD) {
+    zo = has_g ? j * zr.step + cg * es : kScanNowhere;
+    yo = has_g ? j * yr.step + cg * es : kScanNowhere;
+    Co = j * Cr.step + (row + 4 * g) * es;
+  }
+  ScanFour<IT> rx, rd, rz, rC[M];
+  uint32_t rB[4][M];
+  const auto fetch = [&](int rows) {
+    rx.load(xr.tile(rows), xo);
+    rd.load(dr.tile(rows), dto);
+    const rsrc_t rb = Br.tile(rows);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+#pragma unroll
+      for (int m = 0; m < M; ++m) rB[q][m] = scan_one_load<IT>(rb, Bo + 4 * q * Br.step + 16 * m * es);
+    }
+    xr.next();
+    dr.next();
+    Br.next();
     if constexpr (!FOLD) {
-      rC.load(Cp + t * a.C_stride * es);
-      if (zp != nullptr) rz.load(zp + t * a.z_stride * es);
+      const rsrc_t rc = Cr.tile(rows);
+#pragma unroll
+      for (int m = 0; m < M; ++m) rC[m].load(rc, Co + 16 * m * es);
+      rz.load(zr.tile(rows), zo);
+      Cr.next();
+      zr.next();
     }
   };
-  if (n > 0) fetch(0);
+  if (n > 0) fetch(n);
   float* const sd = lds[wave][0];
   float* const sx = lds[wave][1];
   float* const sy = lds[wave][2];
   for (int t0 = 0; t0 < n; t0 += kScanTile) {
     const bool on = t0 + j < n;
-    ScanTile<NS> k;
-    float x[4], z[4];
+    float x[4], z[4], B[4][M], C[4 * M];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      x[r] = on && has_g ? rx.get(r) : 0.0f;
-      z[r] = rz.get(r);
-      float d = prompt_dt(rd.get(r), bias[r], a.dt_softplus);
-      d = on && has_g ? d : 0.0f;
+      x[r] = rx.get(r);
+      z[r] = FOLD ? 0.0f : rz.get(r);
+      float d = scan_step_size(rd.get(r), bias[r], a.dt_softplus);
+      d = on ? d : 0.0f;
       if constexpr (FOLD) dsum[r] += d;
       sd[(4 * g + r) * kScanPitch + j] = d;
       sx[(4 * g + r) * kScanPitch + j] = d * x[r];
     }
-    rB.keep(on);
-    if constexpr (!FOLD) rC.keep(on);
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      k.B[i] = rB.get(i);
-      k.C[i] = FOLD ? 0.0f : rC.get(i);
+    for (int q = 0; q < 4; ++q) {
+#pragma unroll
+      for (int m = 0; m < M; ++m) B[q][m] = scan_one<IT>(rB[q][m]);
     }
-    if (t0 + kScanTile < n) fetch(t0 + kScanTile);
+#pragma unroll
+    for (int i = 0; i < 4 * M; ++i) C[i] = FOLD ? 0.0f : rC[i / 4].get(i % 4);
+    if (t0 + kScanTile < n) fetch(n - t0 - kScanTile);
     scan_wave_sync();
+    float dt[kScanTile], dx[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const f32x4 d = *reinterpret_cast<const f32x4*>(sd + j * kScanPitch + 4 * q);
-      const f32x4 v = *reinterpret_cast<const f32x4*>(sx + j * kScanPitch + 4 * q);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        k.dt[4 * q + e] = d[e];
-        k.dx[4 * q + e] = v[e];
-      }
+      for (int e = 0; e < 4; ++e) dt[4 * q + e] = d[e];
+      dx[q] = sx[j * kScanPitch + 4 * q + g];
     }
-    const float y0 = scan_four<NS, FOLD, 0>(k, A, h);
-    const float y1 = scan_four<NS, FOLD, 1>(k, A, h);
-    const float y2 = scan_four<NS, FOLD, 2>(k, A, h);
-    const float y3 = scan_four<NS, FOLD, 3>(k, A, h);
+    const float y0 = scan_four<M, FOLD, 0>(dt, B, dx, C, st);
+    const float y1 = scan_four<M, FOLD, 1>(dt, B, dx, C, st);
+    const float y2 = scan_four<M, FOLD, 2>(dt, B, dx, C, st);
+    const float y3 = scan_four<M, FOLD, 3>(dt, B, dx, C, st);
     if constexpr (!FOLD) {
       sy[g * kScanPitch + j] = y0;
       sy[(4 + g) * kScanPitch + j] = y1;
@@ -311,9 +417,20 @@ __global__ __launch_bounds__(kScanBlock) void scan_kernel(ScanArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         y[r] = fmaf(D[r], x[r], y[r]);
-        if (zp != nullptr) y[r] *= silu(z[r]);
+        if (gated) y[r] *= silu(z[r]);
       }
-      if (on && has_g) narrow4<IT>(reinterpret_cast<typename Mma<IT>::elem*>(yp + (t0 + j) * a.y_stride * es), y);
+      const rsrc_t ry = yr.tile(n - t0);
+      if constexpr (IT == kF32) {
+        bstore16<false>(ry, yo, 0, __builtin_bit_cast(u32x4, y));
+      } else {
+        typename Mma<IT>::elem out[4];
+        narrow4<IT>(out, y);
+        typedef decltype(__builtin_amdgcn_raw_buffer_load_b64(ry, 0u, 0u, 0)) two;
+        two v;
+        __builtin_memcpy(&v, out, 8);
+        __builtin_amdgcn_raw_buffer_store_b64(v, ry, yo, 0, 0);
+      }
+      yr.next();
     }
     scan_wave_sync();
   }
@@ -328,11 +445,11 @@ __global__ __launch_bounds__(kScanBlock) void scan_kernel(ScanArgs a) {
     }
     if (has_j) {
 #pragma unroll
-      for (int i = 0; i < NS; ++i) gstore(a.ws_h + (at + cj) * N + g * NS + i, h[i]);
+      for (int i = 0; i < 4 * M; ++i) gstore(a.ws_h + (at + cj) * N + 4 * g + 16 * (i / 4) + i % 4, st.h[i]);
     }
   } else if (seg == last && has_j) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) scan_state_store(a.state, st0 + i, a.state_dtype, h[i]);
+    for (int i = 0; i < 4 * M; ++i) scan_state_store(a.state, st0 + 16 * (i / 4) + i % 4, a.state_dtype, st.h[i]);
   }
 }
 
@@ -387,7 +504,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_step_kernel(ScanArgs a) {
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     if (sp[r] == nullptr) continue;        // the same for the whole wavefront
-    const float d = prompt_dt(elem_to_float<IT>(rd[r]), bias, a.dt_softplus);
+    const float d = scan_step_size(elem_to_float<IT>(rd[r]), bias, a.dt_softplus);
     const float x = elem_to_float<IT>(rx[r]), dx = d * x;
     float h[EV], p = 0.0f;
     if constexpr (ST == kF32) {
