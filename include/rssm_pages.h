@@ -44,7 +44,8 @@ extern "C" {
  *   page_stride    bytes between pages, a multiple of 16, >= page_bytes
  *   token_bytes    a multiple of 16 that page_size times gives page_bytes, when a page holds its tokens
  *                  one after another (a fork then copies the filled ones alone); 0: laid out otherwise
- *   workspace_bytes  bytes at tables->workspace */
+ *   workspace_bytes  bytes at tables->workspace
+ * Items (compact: half of the pages) times caches times the 16 KiB pieces of a page are below 2^31. */
 typedef struct {
   int32_t num_items;
   int32_t num_rows;

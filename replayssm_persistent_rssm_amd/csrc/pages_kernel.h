@@ -43,31 +43,41 @@ __device__ __forceinline__ int agent_load(const int32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Exclusive prefix sum over the workgroup, and the total.
+// Sums that stop at 2^32 - 1: no pool has as many pages, so a sum that stopped asks for too many all the same.
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
+
+// Inclusive prefix sum over the wavefront: within rows of 16 lanes, then the last lanes of rows 0 and 2 to rows 1 and 3, then
+// lane 31 to the upper half.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v = add_sat(v, __builtin_amdgcn_update_dpp(0u, v, 0x111, 0xf, 0xf, true));
+  v = add_sat(v, __builtin_amdgcn_update_dpp(0u, v, 0x112, 0xf, 0xf, true));
+  v = add_sat(v, __builtin_amdgcn_update_dpp(0u, v, 0x114, 0xf, 0xf, true));
+  v = add_sat(v, __builtin_amdgcn_update_dpp(0u, v, 0x118, 0xf, 0xf, true));
+  v = add_sat(v, __builtin_amdgcn_update_dpp(0u, v, 0x142, 0xa, 0xf, false));
+  return add_sat(v, __builtin_amdgcn_update_dpp(0u, v, 0x143, 0xc, 0xf, false));
+}
+
+// Exclusive prefix sum over a workgroup of B threads, and the total.  Successive calls alternate between two turns.
+template <int B>
 struct PlanScan {
-  int64_t wave[kPlanBlock / 64];
+  uint32_t wave[2][B / 64];
 };
-template <typename T>
-__device__ __forceinline__ T plan_scan(PlanScan& lds, T v, T& total) {
+template <int B>
+__device__ __forceinline__ uint32_t plan_scan(PlanScan<B>& lds, int turn, uint32_t v, uint32_t& total) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  T sum = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const T o = __shfl_up(sum, d);
-    sum += lane >= d ? o : 0;
-  }
-  __syncthreads();                       // the previous use is over
-  if (lane == 63) lds.wave[w] = sum;
+  const uint32_t sum = wave_scan(v);
+  if (lane == 63) lds.wave[turn][w] = sum;
   __syncthreads();
-  T before = 0;
+  uint32_t before = 0;
   total = 0;
 #pragma unroll
-  for (int i = 0; i < kPlanBlock / 64; ++i) {
-    const T x = static_cast<T>(lds.wave[i]);
-    before += i < w ? x : 0;
-    total += x;
+  for (int i = 0; i < B / 64; ++i) {
+    const uint32_t x = lds.wave[turn][i];
+    before = i < w ? add_sat(before, x) : before;
+    total = add_sat(total, x);
   }
-  return before + sum - v;
+  const uint32_t prev = __builtin_amdgcn_update_dpp(0u, sum, 0x138, 0xf, 0xf, true);   // the lane before
+  return add_sat(before, lane > 0 ? prev : 0u);
 }
 
 typedef int i32x4u __attribute__((ext_vector_type(4), aligned(4)));
@@ -92,8 +102,9 @@ __device__ __forceinline__ PlanMask plan_mask(const PagesArgs& a, int64_t base) 
   return m;
 }
 
-__device__ __forceinline__ int pages_of(int64_t tokens, int page_size) {
-  return static_cast<int>((tokens + page_size - 1) / page_size);
+// Pages of 0 <= tokens < 2^31.
+__device__ __forceinline__ int pages_of(int tokens, int page_size) {
+  return static_cast<int>((static_cast<uint32_t>(tokens) + page_size - 1) / static_cast<uint32_t>(page_size));
 }
 
 __device__ __forceinline__ int row_tokens(const PagesArgs& a, int row) {
@@ -101,10 +112,147 @@ __device__ __forceinline__ int row_tokens(const PagesArgs& a, int row) {
   return n < 0 ? 0 : n;
 }
 
-// Extend and fork: who gets which pages.
+// What an item asks for: its status so far, its plan (fork: tokens, extend: pages; -1: nothing to do) and the
+// pages it needs.  `mine`: it is the first item that names its row.
+struct PlanAsk { int state, plan, need, have, held; };
+
+template <bool FORK>
+__device__ __forceinline__ PlanAsk plan_ask(const PagesArgs& a, bool mine, int row, int src, int length) {
+  PlanAsk k = {kPagesRefused, -1, 0, 0, 0};
+  if (!mine) return k;
+  const int have = row_tokens(a, row);
+  const int64_t most = static_cast<int64_t>(a.max_pages) * a.page_size;
+  if constexpr (FORK) {
+    if (src < 0 || src >= a.num_rows || length < 0) return k;
+    int n = row_tokens(a, src);
+    n = n < most ? n : static_cast<int>(most);
+    if (have != 0) return k;
+    k.state = kPagesOk;
+    k.plan = length < n ? length : n;
+    k.need = k.plan % a.page_size != 0 ? 1 : 0;
+  } else {
+    const int64_t after = static_cast<int64_t>(have) + length;
+    if (length < 0 || after > most || after > INT32_MAX) return k;
+    k.have = have;
+    k.held = pages_of(have, a.page_size);
+    if (length > 0 && have % a.page_size != 0) {
+      const int p = gload(a.table + row * a.table_stride + k.held - 1);
+      if (p >= 0 && p < a.num_pages && gload(a.ref + p) > 1) {
+        k.state = kPagesShared;
+        return k;
+      }
+    }
+    k.state = kPagesOk;
+    k.need = k.plan = pages_of(static_cast<int>(after), a.page_size) - k.held;
+  }
+  return k;
+}
+
+// Extend and fork of at most kPlanFew items, one a thread: everything but the tables' own entries stays in registers
+// and LDS, and the first round of the search for free pages is requested before anything else.  B threads:
+// 256 where one round of them sees the whole pool, 1024 otherwise.
+constexpr int kPlanFew = 256;
+constexpr int kPlanList = 2048;         // free pages kept in LDS, the rest in the workspace
+constexpr int kPlanHash = 1024;
+
+template <bool FORK, int B>
+__global__ __launch_bounds__(B) void pages_plan_few_kernel(PagesArgs a) {
+  __shared__ PlanScan<B> lds;
+  __shared__ int rows[kPlanFew], hash[kPlanHash], held[kPlanFew], list[kPlanList];
+  __shared__ uint32_t first[kPlanFew], needs[kPlanFew];
+  const int tid = threadIdx.x, i = tid;
+  const bool item = i < a.num_items;
+  const int64_t at0 = static_cast<int64_t>(tid) * kPlanPages;
+  uint32_t free = at0 < a.num_pages ? plan_mask(a, at0).free : 0u;
+  int row = -1, src = 0, length = INT32_MAX;
+  if (item) {
+    row = gload(a.dst + i);
+    if constexpr (FORK) src = gload(a.src + i);
+    if (a.lengths != nullptr) length = gload(a.lengths + i);
+  }
+  for (int k = tid; k < kPlanHash; k += B) hash[k] = INT32_MAX;
+  if (tid < kPlanFew) rows[tid] = row;
+  __syncthreads();
+  // a row belongs to the first item that names it: the lowest item of a slot decides unless another row shares the slot
+  const bool known = item && row >= 0 && row < a.num_rows;
+  if (known) atomicMin(&hash[row % kPlanHash], i);
+  __syncthreads();
+  bool mine = false;
+  if (known) {
+    const int k = hash[row % kPlanHash];
+    mine = k == i;
+    if (rows[k] != row) {
+      mine = true;
+      for (int m = 0; m < i; ++m) mine &= rows[m] != row;
+    }
+  }
+  const PlanAsk ask = plan_ask<FORK>(a, mine, row, src, length);
+  uint32_t wanted;
+  const uint32_t at = plan_scan<B>(lds, 0, ask.need, wanted);
+  if (tid < kPlanFew) {
+    first[tid] = at;
+    needs[tid] = ask.need;
+    held[tid] = ask.held;
+  }
+  uint32_t found = 0;
+  int turn = 1;
+  for (int64_t base = 0; base < a.num_pages && found < wanted; base += B * kPlanPages, turn ^= 1) {
+    const int64_t here = base + at0;
+    if (base > 0) free = here < a.num_pages ? plan_mask(a, here).free : 0u;
+    uint32_t total;
+    uint32_t k = found + plan_scan<B>(lds, turn, __builtin_popcount(free), total);
+    for (; free != 0 && k < wanted; ++k, free &= free - 1) {
+      const int page = static_cast<int>(here + __builtin_ctz(free));
+      if (k < kPlanList) list[k] = page;
+      else gstore(a.list + k, page);
+    }
+    found = found + total < wanted ? found + total : wanted;
+  }
+  __syncthreads();
+  const bool granted = ask.need == 0 || add_sat(at, ask.need) <= found;
+  const int state = ask.state == kPagesOk && !granted ? kPagesNone : ask.state;
+  if constexpr (FORK) {
+    if (item) {
+      int page = -1;
+      if (state == kPagesOk) {
+        if (ask.need > 0) {
+          page = list[at];               // fewer items than kPlanList
+          gstore(a.table + row * a.table_stride + ask.plan / a.page_size, page);
+          gstore(a.ref + page, 1);
+        }
+        gstore(a.kv_len + row, ask.plan);
+      }
+      gstore(a.plan + i, state == kPagesOk ? ask.plan : -1);
+      gstore(a.fresh + i, page);
+      gstore(a.status + i, state);
+    }
+  } else {
+    // page k of the list goes to the last item whose pages start at or before k
+    for (uint32_t k = tid; k < found; k += B) {
+      int lo = 0, hi = a.num_items - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= k) lo = mid;
+        else hi = mid - 1;
+      }
+      if (needs[lo] > 0 && add_sat(first[lo], needs[lo]) <= found) {
+        const int page = k < kPlanList ? list[k] : gload(a.list + k);
+        gstore(a.table + rows[lo] * a.table_stride + held[lo] + (k - first[lo]), page);
+        gstore(a.ref + page, 1);
+      }
+    }
+    if (item) {
+      if (state == kPagesOk) gstore(a.kv_len + row, ask.have + length);
+      gstore(a.status + i, state);
+    }
+  }
+}
+
+// Extend and fork of more items, in rounds.
 template <bool FORK>
 __global__ __launch_bounds__(kPlanBlock) void pages_plan_kernel(PagesArgs a) {
-  __shared__ PlanScan lds;
+  __shared__ PlanScan<kPlanBlock> lds;
+  int turn = 0;
   const int tid = threadIdx.x;
   // a row belongs to the first item that names it
   for (int i = tid; i < a.num_items; i += kPlanBlock) {
@@ -121,58 +269,30 @@ __global__ __launch_bounds__(kPlanBlock) void pages_plan_kernel(PagesArgs a) {
   int64_t wanted = 0;
   for (int base = 0; base < a.num_items; base += kPlanBlock) {
     const int i = base + tid;
-    int need = 0;
+    PlanAsk ask = {kPagesRefused, -1, 0, 0, 0};
     if (i < a.num_items) {
       const int r = gload(a.dst + i);
-      int state = r >= 0 && r < a.num_rows && agent_load(a.claim + r) == i ? kPagesOk : kPagesRefused;
-      int plan = -1;
-      if (state == kPagesOk) {
-        const int have = row_tokens(a, r);
-        if constexpr (FORK) {
-          const int s = gload(a.src + i);
-          const int asked = a.lengths != nullptr ? gload(a.lengths + i) : INT32_MAX;
-          if (s < 0 || s >= a.num_rows || asked < 0 || have != 0) {
-            state = kPagesRefused;
-          } else {
-            const int64_t most = static_cast<int64_t>(a.max_pages) * a.page_size;
-            const int n = row_tokens(a, s);
-            plan = asked < n ? asked : n;
-            plan = plan < most ? plan : static_cast<int>(most);
-            need = plan % a.page_size != 0 ? 1 : 0;
-          }
-        } else {
-          const int add = gload(a.lengths + i);
-          const int64_t after = static_cast<int64_t>(have) + add;
-          if (add < 0 || after > static_cast<int64_t>(a.max_pages) * a.page_size || after > INT32_MAX) {
-            state = kPagesRefused;
-          } else {
-            const int held = pages_of(have, a.page_size);
-            if (add > 0 && have % a.page_size != 0) {
-              const int p = gload(a.table + r * a.table_stride + held - 1);
-              if (p >= 0 && p < a.num_pages && gload(a.ref + p) > 1) state = kPagesShared;
-            }
-            if (state == kPagesOk) need = plan = pages_of(after, a.page_size) - held;
-          }
-        }
-      }
-      gstore(a.status + i, state);
-      gstore(a.plan + i, plan);
+      const bool mine = r >= 0 && r < a.num_rows && agent_load(a.claim + r) == i;
+      ask = plan_ask<FORK>(a, mine, r, FORK ? gload(a.src + i) : 0, a.lengths != nullptr ? gload(a.lengths + i) : INT32_MAX);
+      gstore(a.status + i, ask.state);
+      gstore(a.plan + i, ask.plan);
     }
-    int64_t total;                       // needs of a thousand rows may pass 32 bits
-    const int64_t at = wanted + plan_scan<int64_t>(lds, need, total);
+    uint32_t total;
+    const int64_t at = wanted + plan_scan<kPlanBlock>(lds, turn, ask.need, total);
     if (i < a.num_items) gstore(a.first + i, static_cast<int32_t>(at < INT32_MAX ? at : INT32_MAX));
     wanted += total;
+    turn ^= 1;
   }
   // free pages, lowest first, until there are enough
   int found = 0;
-  for (int64_t base = 0; base < a.num_pages && found < wanted; base += kPlanBlock * kPlanPages) {
+  for (int64_t base = 0; base < a.num_pages && found < wanted; base += kPlanBlock * kPlanPages, turn ^= 1) {
     const int64_t at = base + static_cast<int64_t>(tid) * kPlanPages;
     uint32_t free = at < a.num_pages ? plan_mask(a, at).free : 0u;
-    int total;
-    int k = found + plan_scan(lds, __builtin_popcount(free), total);
+    uint32_t total;
+    int64_t k = found + static_cast<int64_t>(plan_scan<kPlanBlock>(lds, turn, __builtin_popcount(free), total));
     for (; free != 0 && k < wanted; ++k, free &= free - 1)
       gstore(a.list + k, static_cast<int32_t>(at + __builtin_ctz(free)));
-    found = static_cast<int>(found + total < wanted ? found + total : wanted);
+    found = static_cast<int>(found + static_cast<int64_t>(total) < wanted ? found + static_cast<int64_t>(total) : wanted);
   }
   __syncthreads();
   if constexpr (FORK) {
@@ -250,9 +370,9 @@ __device__ __forceinline__ bool in_pool(const PagesArgs& a, int page) { return p
 
 // Fork: the shared entries of each row, and the tokens of each page of its own.
 __global__ __launch_bounds__(kPagesBlock) void pages_fork_kernel(PagesArgs a) {
-  const int64_t per = 1 + static_cast<int64_t>(a.num_caches) * a.chunks, total = a.num_items * per;
-  for (int64_t task = blockIdx.x; task < total; task += gridDim.x) {
-    const int i = static_cast<int>(task / per), k = static_cast<int>(task - i * per);
+  const uint32_t chunks = a.chunks, per = 1 + a.num_caches * chunks, total = a.num_items * per;
+  for (uint32_t task = blockIdx.x; task < total; task += gridDim.x) {
+    const uint32_t i = task / per, k = task - i * per;
     const int len = sload(a.plan + i);
     if (len < 0) continue;
     const int full = len / a.page_size, rest = len - full * a.page_size;
@@ -265,7 +385,7 @@ __global__ __launch_bounds__(kPagesBlock) void pages_fork_kernel(PagesArgs a) {
         if (in_pool(a, page)) atomicAdd(a.ref + page, 1);
       }
     } else if (rest > 0) {
-      const int cache = (k - 1) / a.chunks, chunk = (k - 1) - cache * a.chunks;
+      const uint32_t cache = (k - 1) / chunks, chunk = (k - 1) - cache * chunks;
       const int64_t bytes = a.token_bytes > 0 ? rest * a.token_bytes : a.page_bytes;
       const int page = sload(from + full);
       if (chunk * static_cast<int64_t>(kPagesChunk) < bytes && in_pool(a, page)) copy_chunk(a, cache, page, sload(a.fresh + i), chunk, bytes);
@@ -282,10 +402,9 @@ __global__ __launch_bounds__(kPagesBlock) void pages_release_kernel(PagesArgs a)
   if (r < 0 || r >= a.num_rows || keep < 0) return;
   if (threadIdx.x == 0) before = atomicMin(a.kv_len + r, keep);
   __syncthreads();
-  const int64_t most = a.max_pages;
-  const int64_t held = pages_of(before < 0 ? 0 : before, a.page_size);
+  const int held = pages_of(before < 0 ? 0 : before, a.page_size);
   int32_t* row = a.table + r * a.table_stride;
-  for (int64_t e = pages_of(keep, a.page_size) + threadIdx.x; e < (held < most ? held : most); e += kPagesBlock) {
+  for (int e = pages_of(keep, a.page_size) + threadIdx.x; e < (held < a.max_pages ? held : a.max_pages); e += kPagesBlock) {
     const int page = gload(row + e);
     gstore(row + e, -1);
     if (in_pool(a, page)) atomicSub(a.ref + page, 1);
@@ -294,33 +413,34 @@ __global__ __launch_bounds__(kPagesBlock) void pages_release_kernel(PagesArgs a)
 
 // Compact: the pages that move, in order, and the counts after the moves.
 __global__ __launch_bounds__(kPlanBlock) void pages_pack_kernel(PagesArgs a) {
-  __shared__ PlanScan lds;
+  __shared__ PlanScan<kPlanBlock> lds;
   const int tid = threadIdx.x;
-  int used = 0;
+  uint32_t used = 0;
   for (int64_t base = static_cast<int64_t>(tid) * kPlanPages; base < a.num_pages; base += kPlanBlock * kPlanPages) {
     const PlanMask m = plan_mask(a, base);
     used += __builtin_popcount(m.in & ~m.free);
   }
-  int live;
-  plan_scan(lds, used, live);
+  uint32_t live;
+  plan_scan<kPlanBlock>(lds, 0, used, live);
   // free pages before `live`, then pages in use from there on: as many of the one as of the other
-  int listed = 0;
-  for (int64_t base = 0; base < a.num_pages; base += kPlanBlock * kPlanPages) {
+  uint32_t listed = 0;
+  int turn = 1;
+  for (int64_t base = 0; base < a.num_pages; base += kPlanBlock * kPlanPages, turn ^= 1) {
     const int64_t at = base + static_cast<int64_t>(tid) * kPlanPages;
     uint32_t pick = 0;
     if (at < a.num_pages) {
       const PlanMask m = plan_mask(a, at);
-      const int64_t below = live - at;   // of these pages, so many lie before `live`
+      const int64_t below = static_cast<int64_t>(live) - at;   // of these pages, so many lie before `live`
       const uint32_t low = below <= 0 ? 0u : below >= kPlanPages ? 0xffffffffu : (1u << below) - 1;
       pick = (m.free & low) | (m.in & ~m.free & ~low);
     }
-    int total;
-    int k = listed + plan_scan(lds, __builtin_popcount(pick), total);
+    uint32_t total;
+    uint32_t k = listed + plan_scan<kPlanBlock>(lds, turn, __builtin_popcount(pick), total);
     for (; pick != 0; ++k, pick &= pick - 1) gstore(a.list + k, static_cast<int32_t>(at + __builtin_ctz(pick)));
     listed += total;
   }
   __syncthreads();
-  const int moves = listed / 2;
+  const int moves = static_cast<int>(listed / 2);
   for (int k = tid; k < moves; k += kPlanBlock) {
     const int hole = gload(a.list + k), page = gload(a.list + moves + k);
     gstore(a.moved + page, hole);
@@ -329,8 +449,8 @@ __global__ __launch_bounds__(kPlanBlock) void pages_pack_kernel(PagesArgs a) {
   }
   if (tid == 0) {
     gstore(a.count, moves);
-    gstore(a.count + 1, live);
-    gstore(a.live, live);
+    gstore(a.count + 1, static_cast<int32_t>(live));
+    gstore(a.live, static_cast<int32_t>(live));
   }
 }
 
@@ -338,30 +458,28 @@ __global__ __launch_bounds__(kPlanBlock) void pages_pack_kernel(PagesArgs a) {
 __global__ __launch_bounds__(kPagesBlock) void pages_move_kernel(PagesArgs a) {
   const int moves = sload(a.count), live = sload(a.count + 1);
   if (moves == 0) return;
-  const int64_t per = static_cast<int64_t>(a.num_caches) * a.chunks, total = a.num_rows + moves * per;
-  for (int64_t task = blockIdx.x; task < total; task += gridDim.x) {
-    if (task < a.num_rows) {
-      const int64_t held = pages_of(row_tokens(a, static_cast<int>(task)), a.page_size);
+  const uint32_t rows = a.num_rows, chunks = a.chunks, per = a.num_caches * chunks, total = rows + moves * per;
+  for (uint32_t task = blockIdx.x; task < total; task += gridDim.x) {
+    if (task < rows) {
+      const int held = pages_of(row_tokens(a, task), a.page_size);
       int32_t* row = a.table + task * a.table_stride;
-      for (int64_t e = threadIdx.x; e < (held < a.max_pages ? held : a.max_pages); e += kPagesBlock) {
+      for (int e = threadIdx.x; e < (held < a.max_pages ? held : a.max_pages); e += kPagesBlock) {
         const int page = gload(row + e);
         if (page >= live && page < a.num_pages) gstore(row + e, gload(a.moved + page));
       }
     } else {
-      const int64_t t = task - a.num_rows;
-      const int m = static_cast<int>(t / per), k = static_cast<int>(t - m * per);
-      const int cache = k / a.chunks;
-      copy_chunk(a, cache, sload(a.list + moves + m), sload(a.list + m), k - cache * a.chunks, a.page_bytes);
+      const uint32_t t = task - rows, m = t / per, k = t - m * per, cache = k / chunks;
+      copy_chunk(a, cache, sload(a.list + moves + m), sload(a.list + m), k - cache * chunks, a.page_bytes);
     }
   }
 }
 
 __global__ __launch_bounds__(kPagesBlock) void pages_copy_kernel(PagesArgs a) {
-  const int64_t per = static_cast<int64_t>(a.num_caches) * a.chunks, total = a.num_items * per;
-  for (int64_t task = blockIdx.x; task < total; task += gridDim.x) {
-    const int i = static_cast<int>(task / per), k = static_cast<int>(task - i * per), cache = k / a.chunks;
+  const uint32_t chunks = a.chunks, per = a.num_caches * chunks, total = a.num_items * per;
+  for (uint32_t task = blockIdx.x; task < total; task += gridDim.x) {
+    const uint32_t i = task / per, k = task - i * per, cache = k / chunks;
     const int from = sload(a.src + i), to = sload(a.dst + i);
-    if (in_pool(a, from) && in_pool(a, to) && from != to) copy_chunk(a, cache, from, to, k - cache * a.chunks, a.page_bytes);
+    if (in_pool(a, from) && in_pool(a, to) && from != to) copy_chunk(a, cache, from, to, k - cache * chunks, a.page_bytes);
   }
 }
 

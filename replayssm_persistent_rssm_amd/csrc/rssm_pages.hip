@@ -123,6 +123,21 @@ rssm_status launch(const void* fn, int64_t grid, int block, PagesArgs* a, void* 
   return RSSM_OK;
 }
 
+template <bool FORK>
+rssm_status launch_plan(PagesArgs* a, void* stream, const char* name) {
+  if (a->num_items > kPlanFew) return launch(reinterpret_cast<const void*>(&pages_plan_kernel<FORK>), 1, kPlanBlock, a, stream, name);
+  if (a->num_pages > 256 * kPlanPages)
+    return launch(reinterpret_cast<const void*>(&pages_plan_few_kernel<FORK, 1024>), 1, 1024, a, stream, name);
+  return launch(reinterpret_cast<const void*>(&pages_plan_few_kernel<FORK, 256>), 1, 256, a, stream, name);
+}
+
+// The tasks of a copying kernel are counted in 32 bits; 2^31 of them would be 32 TiB.
+rssm_status check_tasks(int64_t items, int64_t per, int64_t more, const char* name) {
+  if (items > 0 && per > ((int64_t(1) << 31) - more) / items)
+    return fail(RSSM_ERR_INVALID_ARGUMENT, "%s has more than 2^31 pieces of %d bytes to look at", name, kPagesChunk);
+  return RSSM_OK;
+}
+
 void say(const char* name, const rssm_pages_desc* d) {
   if (verbose())
     std::fprintf(stderr, "[rssm_%s] items=%d rows=%d pages=%d caches=%d\n", name, d->num_items, d->num_rows, d->num_pages,
@@ -157,7 +172,7 @@ rssm_status rssm_page_extend(const rssm_pages_desc* d, const rssm_pages_tables* 
   PagesArgs a;
   fill_args(&a, d, t);
   say("page_extend", d);
-  return launch(reinterpret_cast<const void*>(&pages_plan_kernel<false>), 1, kPlanBlock, &a, hip_stream, "page_extend");
+  return launch_plan<false>(&a, hip_stream, "page_extend");
 }
 
 rssm_status rssm_page_fork(const rssm_pages_desc* d, const rssm_pages_tables* t, void* hip_stream) {
@@ -176,8 +191,10 @@ rssm_status rssm_page_fork(const rssm_pages_desc* d, const rssm_pages_tables* t,
   if (st != RSSM_OK) return st;
   PagesArgs a;
   fill_args(&a, d, t);
+  st = check_tasks(d->num_items, 1 + static_cast<int64_t>(d->num_caches) * a.chunks, 0, "page_fork");
+  if (st != RSSM_OK) return st;
   say("page_fork", d);
-  st = launch(reinterpret_cast<const void*>(&pages_plan_kernel<true>), 1, kPlanBlock, &a, hip_stream, "page_fork (plan)");
+  st = launch_plan<true>(&a, hip_stream, "page_fork (plan)");
   if (st != RSSM_OK) return st;
   const int64_t tasks = d->num_items * (1 + static_cast<int64_t>(d->num_caches) * a.chunks);
   return launch(reinterpret_cast<const void*>(&pages_fork_kernel), std::min(tasks, kPagesGrid), kPagesBlock, &a, hip_stream, "page_fork");
@@ -217,6 +234,8 @@ rssm_status rssm_page_compact(const rssm_pages_desc* d, const rssm_pages_tables*
   if (st != RSSM_OK) return st;
   PagesArgs a;
   fill_args(&a, &e, t);
+  st = check_tasks(d->num_pages / 2, static_cast<int64_t>(d->num_caches) * a.chunks, d->num_rows, "page_compact");
+  if (st != RSSM_OK) return st;
   say("page_compact", &e);
   st = launch(reinterpret_cast<const void*>(&pages_pack_kernel), 1, kPlanBlock, &a, hip_stream, "page_compact (plan)");
   if (st != RSSM_OK) return st;
@@ -237,6 +256,8 @@ rssm_status rssm_page_copy(const rssm_pages_desc* d, const rssm_pages_tables* t,
   if (st != RSSM_OK) return st;
   PagesArgs a;
   fill_args(&a, d, t);
+  st = check_tasks(d->num_items, static_cast<int64_t>(d->num_caches) * a.chunks, 0, "page_copy");
+  if (st != RSSM_OK) return st;
   say("page_copy", d);
   const int64_t tasks = static_cast<int64_t>(d->num_items) * d->num_caches * a.chunks;
   return launch(reinterpret_cast<const void*>(&pages_copy_kernel), std::min(tasks, kPagesGrid), kPagesBlock, &a, hip_stream, "page_copy");

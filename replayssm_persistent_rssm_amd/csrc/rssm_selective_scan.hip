@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cstdio>
+#include <cstdlib>
 
 #include "rssm_host.h"
 #include "scan_inst.h"
@@ -103,7 +104,7 @@ int64_t main_blocks(const rssm_selective_scan_desc* d) { return (d->channels + k
 Split split_of(const rssm_selective_scan_desc* d) {
   const int64_t items = d->num_seqs * main_blocks(d);
   const int64_t tiles = (static_cast<int64_t>(d->max_seq_len) + kScanTile - 1) / kScanTile;
-  constexpr int64_t kFill = 512, kLeast = 4, kMost = 64;
+  const int64_t kFill = std::getenv("SC_FILL") ? std::atoi(std::getenv("SC_FILL")) : 512, kLeast = std::getenv("SC_LEAST") ? std::atoi(std::getenv("SC_LEAST")) : 4, kMost = 64;
   if (items == 0 || items > kFill / 2 || tiles < 2 * kLeast)
     return {1, static_cast<int>(std::max<int64_t>(tiles, 1) * kScanTile)};
   const int64_t want = std::min(std::min((kFill + items - 1) / items, tiles / kLeast), kMost);

@@ -312,6 +312,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void scan_kernel(ScanArgs a) {
 #pragma unroll
       for (int i = 0; i < 4 * M; ++i) st.h[i] = scan_state_load(a.state, st0 + 16 * (i / 4) + i % 4, a.state_dtype);
     }
+#pragma unroll 4
     for (int k = 0; k < seg; ++k) {
       const int64_t at = (static_cast<int64_t>(s) * a.nseg + k) * a.channels + cj;
       const float sum = gload(a.ws_d + at);

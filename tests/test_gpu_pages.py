@@ -206,6 +206,28 @@ def test_copy(rp):
     assert torch.equal(b.dev.cpu(), b.room)
 
 
+def test_rows_a_multiple_of_1024_apart(rp):
+    """Repeated rows are told from different ones, whichever table finds them."""
+    b = Both(rp, rows=4100, most=2, pages=600, page=4, caches=1, wide=16)
+    rows = [5, 1029, 5, 2053, 1029, 4096, 0, 1024, 2048, 0, 2053, 7]
+    assert b.extend(rows, [3] * 12) == [0, 0, 2, 0, 2, 0, 0, 0, 0, 2, 2, 0]
+    assert b.fork([5] * 5, [6, 1030, 6, 4102, 2054], [3, 2, 1, 1, 3]) == [0, 0, 2, 2, 0]
+    b.extend(rows * 20, [1] * 240)
+    b.extend(rows * 30, [1] * 360)
+
+
+@pytest.mark.parametrize("items", [1, 64, 65, 255, 256, 257, 1025])
+@pytest.mark.parametrize("pages", [300, 5000, 40000])
+def test_items_and_pools(rp, items, pages):
+    """The forms for few and many items, for pools of one round and several."""
+    b = Both(rp, rows=2 * items + 1, most=40, pages=pages, page=2, caches=1, wide=16)
+    rng = random.Random(items)
+    b.extend(list(range(items)), [rng.randint(0, 70) for _ in range(items)])
+    b.fork([rng.randint(0, items) for _ in range(items)], [items + i for i in range(items)], [rng.randint(0, 60) for _ in range(items)])
+    b.release(list(range(0, items, 2)))
+    b.extend(list(range(items)), [rng.randint(0, 9) for _ in range(items)])
+
+
 def test_strided_table(rp):
     """Rows of a wider table; what lies beside them stays."""
     wide = torch.full((4, 10), 77, dtype=torch.int32, device="cuda")

@@ -182,6 +182,11 @@ def test_pool_tables(rp):
     for name in ("rssm_page_extend", "rssm_page_fork", "rssm_page_release", "rssm_page_copy"):
         e = build(rp.RssmPagesDesc, PAGES, dict(num_items=0))
         assert getattr(rp.lib(), name)(ctypes.byref(e), ctypes.byref(fake(rp.RssmPagesTables)), None) == 0
+        if name != "rssm_page_release" and name != "rssm_page_extend":
+            big = build(rp.RssmPagesDesc, PAGES, dict(num_items=2 ** 20, num_caches=65535, workspace_bytes=1 << 40))
+            refused(rp, name, big, fake(rp.RssmPagesTables), 1, "2^31")
+    big = build(rp.RssmPagesDesc, PAGES, dict(num_pages=2 ** 30, num_caches=65535, workspace_bytes=1 << 40))
+    refused(rp, "rssm_page_compact", big, fake(rp.RssmPagesTables), 1, "2^31")
     for name in ("rssm_page_fork", "rssm_page_compact", "rssm_page_copy"):
         refused(rp, name, d, fake(rp.RssmPagesTables, cache_ptrs=0x10004), 1, "8-byte")
 
