@@ -118,47 +118,42 @@ __global__ __launch_bounds__(kConvBlock) void conv_prompt_kernel(ConvArgs a) {
   const int64_t t0 = start + static_cast<int64_t>(tile - (start / T + s)) * T;
   if (t0 < start || slot == a.pad || slot < 0 || slot >= a.num_slots || c >= a.channels) return;
   if (t0 > start && t0 >= end) return;
+  const ConvWeights<DT, W> w(a, c);
   const char* xp = a.x + c * es;
   const int64_t xs = a.x_stride * es;
-  Raw8<DT> hist[W - 1];                // the W - 1 inputs before t0, oldest first
-  if (t0 == start) {
+  const int n = static_cast<int>(end - t0 < T ? end - t0 : T);
+  Raw8<DT> hist[W - 1], tail[W - 1];   // the W - 1 inputs before t0 and the sequence's last ones, oldest first
+  char* const sp = a.state + (slot * a.state_stride + c) * es;
+  const int64_t srow = static_cast<int64_t>(a.channels) * es;
+  const bool opens = t0 == start;
+  if (opens) {
     const bool load = a.load_state == nullptr || sload(a.load_state + s) != 0;
-    char* sp = a.state + (slot * a.state_stride + c) * es;
-    const int64_t row = static_cast<int64_t>(a.channels) * es;
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) hist[k] = load ? raw_load<DT>(sp + k * row) : raw_zero<DT>();
-    // the last W - 1 inputs: rows of x, and of the old state where the sequence is shorter
-    const int len = end - start;
+    for (int k = 0; k < W - 1; ++k) hist[k] = load ? raw_load<DT>(sp + k * srow) : raw_zero<DT>();
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
-      Raw8<DT> v = raw_zero<DT>();
-      const int p = len - (W - 1) + k;       // place in the sequence; below 0: hist[p + W - 1]
-      if (p >= 0) {
-        v = raw_load<DT>(xp + (start + static_cast<int64_t>(p)) * xs);
-      } else {
-#pragma unroll
-        for (int m = 0; m < W - 1; ++m)
-          if (m == p + W - 1) v = hist[m];
-      }
-      raw_store<DT>(sp + k * row, v);
+      const int p = end - start - (W - 1) + k;   // place in the sequence; below 0: hist[p + W - 1]
+      tail[k] = raw_zero<DT>();
+      if (p >= 0) tail[k] = raw_load<DT>(xp + (start + static_cast<int64_t>(p)) * xs);
     }
   } else {
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) hist[k] = raw_load<DT>(xp + (t0 - (W - 1) + k) * xs);
   }
-  const int n = static_cast<int>(end - t0 < T ? end - t0 : T);
-  if (n <= 0) return;
-  const ConvWeights<DT, W> w(a, c);
-  f32x8 h[W - 1];
-#pragma unroll
-  for (int k = 0; k < W - 1; ++k) h[k] = raw_float<DT>(hist[k]);
   xp += t0 * xs;
   char* yp = a.y + t0 * a.y_stride * es + c * es;
   const int64_t ys = a.y_stride * es;
-  for (int t = 0; t < n; t += kAhead) {
-    Raw8<DT> in[kAhead];
+  Raw8<DT> in[kAhead];
+  const auto fetch = [&](int t) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) in[i] = raw_load<DT>(xp + (t + i < n ? t + i : n - 1) * xs);
+  };
+  if (n > 0) fetch(0);
+  f32x8 h[W - 1];
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) h[k] = raw_float<DT>(hist[k]);
+  for (int t = 0; t < n; t += kAhead) {
+    if (t > 0) fetch(t);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (t + i < n) {
@@ -176,6 +171,18 @@ __global__ __launch_bounds__(kConvBlock) void conv_prompt_kernel(ConvArgs a) {
         h[W - 2] = v;
         store8<DT>(yp + (t + i) * ys, conv_act(o, a.silu));
       }
+    }
+  }
+  if (opens) {   // of a sequence shorter than W - 1, old rows move up
+    const int len = end - start;
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+      Raw8<DT> v = tail[k];
+#pragma unroll
+      for (int m = k + 1; m < W - 1; ++m)
+        if (m == len + k) v = hist[m];
+      if (len == 0) v = hist[k];
+      raw_store<DT>(sp + k * srow, v);
     }
   }
 }

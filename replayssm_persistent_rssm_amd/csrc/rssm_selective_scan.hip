@@ -3,8 +3,8 @@
 #include "rssm_selective_scan.h"
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
-#include <cstdlib>
 
 #include "rssm_host.h"
 #include "scan_inst.h"
@@ -101,13 +101,21 @@ struct Split { int nseg, seg_len; };
 
 int64_t main_blocks(const rssm_selective_scan_desc* d) { return (d->channels + kScanChannels - 1) / kScanChannels; }
 
+// Stretches of the token axis.  All but the last are folded once more than they are computed (70 % of a
+// stretch's time), so the axis is split only when the sequences' channel blocks (of 64) leave compute units without a
+// workgroup (one prompt of 8,000 tokens, 8,192 channels, 128 blocks: 401 us, 573 with two stretches; three of
+// them, 384 blocks: 1,016 us whole, 1,090 in four).  Then as many stretches as give each unit six
+// workgroups (one of 16,384 tokens, 4,096 channels: 413 us, 453 with two a unit), of at least two tiles, at most
+// sqrt(8 tiles) of them because each reads the ends of those before it (2,048 tokens, 1,024 channels: 27 us with 32, 35
+// with 64; 300 tokens, 256 channels: 15 us with 9, 19 with 4, 29 whole), and none below 8 tiles, where
+// the second launch costs as much as it saves (97 tokens, 1,024 channels: 13.3 us whole, 14.1 in three).
 Split split_of(const rssm_selective_scan_desc* d) {
   const int64_t items = d->num_seqs * main_blocks(d);
   const int64_t tiles = (static_cast<int64_t>(d->max_seq_len) + kScanTile - 1) / kScanTile;
-  const int64_t kFill = std::getenv("SC_FILL") ? std::atoi(std::getenv("SC_FILL")) : 512, kLeast = std::getenv("SC_LEAST") ? std::atoi(std::getenv("SC_LEAST")) : 4, kMost = 64;
-  if (items == 0 || items > kFill / 2 || tiles < 2 * kLeast)
-    return {1, static_cast<int>(std::max<int64_t>(tiles, 1) * kScanTile)};
-  const int64_t want = std::min(std::min((kFill + items - 1) / items, tiles / kLeast), kMost);
+  constexpr int64_t kSplit = 256, kFill = 1536, kMost = 64;
+  if (items == 0 || items > kSplit || tiles < 8) return {1, static_cast<int>(std::max<int64_t>(tiles, 1) * kScanTile)};
+  const int64_t reads = static_cast<int64_t>(std::sqrt(8.0 * static_cast<double>(tiles)));
+  const int64_t want = std::min(std::min(kFill / items, tiles / 2), std::min(reads, kMost));
   const int64_t per = (tiles + want - 1) / want;
   return {static_cast<int>((tiles + per - 1) / per), static_cast<int>(per * kScanTile)};
 }
