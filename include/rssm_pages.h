@@ -29,8 +29,8 @@ extern "C" {
 #define RSSM_PAGE_NONE 1     /* too few free pages: the row is as it was */
 #define RSSM_PAGE_REFUSED 2  /* a row outside the table, named twice, of negative or too great length, or (fork)
                                 a destination that holds tokens: the row is as it was */
-#define RSSM_PAGE_SHARED 3   /* (extend) the row's last page is not full and other rows hold it too: fork the row
-                                first; the row is as it was */
+#define RSSM_PAGE_SHARED 3   /* (extend) the row's last page is not full and counted more than once (another row
+                                holds it too): fork the row first; the row is as it was */
 
 /* Host-side scalars (each entry point reads those it names).
  *   num_items      rows or pages that the call works on >= 0, at most 2^20
@@ -69,7 +69,7 @@ typedef struct {
  *   status       [num_items] int32, written (extend, fork): RSSM_PAGE_OK, _NONE, _REFUSED or _SHARED
  *   live         [1] int32, written (compact): pages in use, which are the pages 0 .. live - 1 afterwards
  *   workspace    device memory of workspace_bytes (extend, fork, compact)
- * Contract: the tables agree with one another (a pool starts with page_table -1, kv_len 0 and page_ref 0
+ * Contract: calls on one pool are ordered (one stream, or events); the tables agree with one another (a pool starts with page_table -1, kv_len 0 and page_ref 0
  * and is changed by these calls alone, apart from page counts that the caller takes or gives back for
  * itself).  As a guard against faults, pages outside the pool are neither read nor written.
  * Alignment: workspace 16 bytes, cache_ptrs 8, the others 4. */
@@ -96,7 +96,8 @@ rssm_status rssm_page_extend(const rssm_pages_desc *desc, const rssm_pages_table
 
 /* Rows dst[i], which are empty, become the first min(lengths[i], kv_len[src[i]]) tokens of rows src[i]: full pages are
  * shared (counted once more), the tokens of a last page that is not full are copied to a page of the fork's
- * own, in every cache.  Several items may have one source.  Of rows named twice as a destination the first item counts.  A
+ * own, in every cache.  Several items may have one source; sources are
+ * taken as they were when the call began.  Of rows named twice as a destination the first item counts.  A
  * shared page is never written to again: rows grow on pages of their own. */
 rssm_status rssm_page_fork(const rssm_pages_desc *desc, const rssm_pages_tables *tables, void *hip_stream);
 

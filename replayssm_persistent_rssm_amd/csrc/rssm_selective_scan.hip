@@ -101,19 +101,27 @@ struct Split { int nseg, seg_len; };
 
 int64_t main_blocks(const rssm_selective_scan_desc* d) { return (d->channels + kScanChannels - 1) / kScanChannels; }
 
+// Few channels and short sequences go to scan_short_kernel: up to 4,096 wavefronts of it (four a SIMD) and 512 tokens
+// (us with it and without: 12 prompts of 200, 1,024 channels: 24.4, 33.6; one of 200, 8,192 channels: 17.5, 21.6; of 400,
+// 4,096 channels: 19.2, 21.6; of 1,000: 41.3, 43.7 and with 8,192 channels 67.4, 63.6), 320 tokens where stretches would have
+// most of the device to themselves (1,024 channels: 14.3, 14.9 for 300 tokens, 17.9, 15.2 for 400).
+bool is_short(const rssm_selective_scan_desc* d) {
+  const int64_t waves = static_cast<int64_t>(d->num_seqs) * ((d->channels + 3) / 4);
+  return waves <= 4096 && d->max_seq_len <= (waves <= 512 ? 320 : 512);
+}
+
 // Stretches of the token axis.  All but the last are folded once more than they are computed (70 % of a
 // stretch's time), so the axis is split only when the sequences' channel blocks (of 64) leave compute units without a
 // workgroup (one prompt of 8,000 tokens, 8,192 channels, 128 blocks: 401 us, 573 with two stretches; three of
 // them, 384 blocks: 1,016 us whole, 1,090 in four).  Then as many stretches as give each unit six
 // workgroups (one of 16,384 tokens, 4,096 channels: 413 us, 453 with two a unit), of at least two tiles, at most
 // sqrt(8 tiles) of them because each reads the ends of those before it (2,048 tokens, 1,024 channels: 27 us with 32, 35
-// with 64; 300 tokens, 256 channels: 15 us with 9, 19 with 4, 29 whole), and none below 8 tiles, where
-// the second launch costs as much as it saves (97 tokens, 1,024 channels: 13.3 us whole, 14.1 in three).
+// with 64), and none below 8 tiles, where the second launch costs as much as it saves.
 Split split_of(const rssm_selective_scan_desc* d) {
   const int64_t items = d->num_seqs * main_blocks(d);
   const int64_t tiles = (static_cast<int64_t>(d->max_seq_len) + kScanTile - 1) / kScanTile;
   constexpr int64_t kSplit = 256, kFill = 1536, kMost = 64;
-  if (items == 0 || items > kSplit || tiles < 8) return {1, static_cast<int>(std::max<int64_t>(tiles, 1) * kScanTile)};
+  if (items == 0 || items > kSplit || tiles < 8 || is_short(d)) return {1, static_cast<int>(std::max<int64_t>(tiles, 1) * kScanTile)};
   const int64_t reads = static_cast<int64_t>(std::sqrt(8.0 * static_cast<double>(tiles)));
   const int64_t want = std::min(std::min(kFill / items, tiles / 2), std::min(reads, kMost));
   const int64_t per = (tiles + want - 1) / want;
@@ -208,6 +216,10 @@ rssm_status rssm_selective_scan(const rssm_selective_scan_desc* d, const rssm_se
   if (verbose())
     std::fprintf(stderr, "[rssm_selective_scan] %s/%s seqs=%d channels=%d dstate=%d stretches=%d of %d\n",
                  dtype_name(d->state_dtype), dtype_name(d->input_dtype), d->num_seqs, d->channels, d->dstate, sp.nseg, sp.seg_len);
+  if (is_short(d)) {
+    a.blocks = (d->channels + kScanShortChannels - 1) / kScanShortChannels;
+    return launch(kernel_for(kScanShort, d), static_cast<int64_t>(d->num_seqs) * a.blocks, &a, hip_stream, "selective_scan_short");
+  }
   const int64_t grid = static_cast<int64_t>(d->num_seqs) * sp.nseg * a.blocks;
   if (sp.nseg > 1) {
     a.ws_h = static_cast<float*>(t->workspace);

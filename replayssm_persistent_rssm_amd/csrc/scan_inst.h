@@ -5,12 +5,13 @@
 
 namespace rssm {
 
-enum : int { kScanMain = 0, kScanFold = 1, kScanStepOne = 2, kScanStepFour = 3 };
+enum : int { kScanMain = 0, kScanFold = 1, kScanStepOne = 2, kScanStepFour = 3, kScanShort = 4 };
 
 template <int IT, int N>
 const void* scan_fn(int which, int state_dtype) {
   if (which == kScanMain) return reinterpret_cast<const void*>(&scan_kernel<IT, N, false>);
   if (which == kScanFold) return reinterpret_cast<const void*>(&scan_kernel<IT, N, true>);
+  if (which == kScanShort) return reinterpret_cast<const void*>(&scan_short_kernel<IT, N>);
   const bool four = which == kScanStepFour;
   switch (state_dtype) {
     case kF32:

@@ -52,6 +52,7 @@ struct ScanArgs {
 
 constexpr int kScanBlock = 256;
 constexpr int kScanChannels = 64;    // a workgroup of scan_kernel, 16 a wavefront
+constexpr int kScanShortChannels = 16;   // a workgroup of scan_short_kernel, 4 a wavefront
 constexpr int kScanTile = 16;        // tokens
 constexpr int kScanPitch = 20;       // floats between rows of an LDS tile: 16-byte pieces of 16 rows on different banks
 constexpr float kLog2e = 1.44269504088896341f;
@@ -144,8 +145,11 @@ __device__ __forceinline__ void scan_state_store(char* base, int64_t at, int dty
   }
 }
 
-// A log2(e), with -infinity as the most negative number: a step of size 0 then decays by exp2(-0) = 1.
-__device__ __forceinline__ float scan_rate(float A) { return fmaxf(A * kLog2e, -3.40282347e38f); }
+// A log2(e), with -infinity as the most negative number: a step of size 0 then decays by exp2(-0) = 1.  (A NaN stays.)
+__device__ __forceinline__ float scan_rate(float A) {
+  const float v = A * kLog2e;
+  return v < -3.40282347e38f ? -3.40282347e38f : v;
+}
 
 // softplus(v) = max(v, 0) + log(1 + t), t = exp(-|v|); log(1 + t) / t on [0, 1] is the polynomial through its values
 // at the ten Chebyshev points (off by 1.4e-8 of itself, 1.3e-7 with its roundings): small steps keep
@@ -452,6 +456,176 @@ __global__ __launch_bounds__(kScanBlock, 2) void scan_kernel(ScanArgs a) {
 #pragma unroll
     for (int i = 0; i < 4 * M; ++i) scan_state_store(a.state, st0 + 16 * (i / 4) + i % 4, a.state_dtype, st.h[i]);
   }
+}
+
+// v of lane T of the lane's row of 16.
+template <int T>
+__device__ __forceinline__ float row_bcast(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x150 + T, 0xf, 0xf, true));
+}
+
+// Pairs of v[t] and v[t + n]: in the lanes of `banks` (groups of 4 in each row of 16) the second, otherwise the first, added
+// to its partner lane's (row_ror:8: 8 lanes on; row_half_mirror: 7 - lane of 8).  The leading wait is the broadcast's
+// after a vector write.
+#define RSSM_PAIR(ctrl, banks)                                                                        \
+  asm("s_nop 1\n\tv_add_f32_dpp %0, %1, %1 " ctrl " row_mask:0xf bank_mask:0xf\n\t"                   \
+      "v_add_f32_dpp %0, %2, %2 " ctrl " row_mask:0xf bank_mask:" banks                               \
+      : "=&v"(o) : "v"(a), "v"(b))
+__device__ __forceinline__ float pair_eight(float a, float b) {
+  float o;
+  RSSM_PAIR("row_ror:8", "0xc");
+  return o;
+}
+__device__ __forceinline__ float pair_four(float a, float b) {
+  float o;
+  RSSM_PAIR("row_half_mirror", "0xa");
+  return o;
+}
+#undef RSSM_PAIR
+
+template <int CTRL>
+__device__ __forceinline__ float quad_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+// Lane j of each row of 16: v[j] summed over the row.
+__device__ __forceinline__ float row_sums(const float (&v)[16], int j) {
+  float w[8], x[4];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) w[t] = pair_eight(v[t], v[t + 8]);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) x[t] = pair_four(w[t], w[t + 4]);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) x[t] = quad_add<0xB1>(x[t]);   // lane ^ 1; all lanes take part before any is chosen
+  const float a = quad_add<0x4E>(j & 1 ? x[1] : x[0]);       // lane ^ 2
+  const float b = quad_add<0x4E>(j & 1 ? x[3] : x[2]);
+  return j & 2 ? b : a;
+}
+
+template <int M, int Q, int T>
+__device__ __forceinline__ float scan_short_token(float d, float dx, const f32x4 (&B)[M], const f32x4 (&C)[M],
+                                                  const float (&A)[M], float (&h)[M]) {
+  float y = 0.0f;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const float e = __builtin_amdgcn_exp2f(row_bcast<4 * Q + T>(d) * A[m]);
+    h[m] = fmaf(e, h[m], row_bcast<4 * Q + T>(dx) * B[m][T]);
+    y = m == 0 ? h[0] * C[0][T] : fmaf(h[m], C[m][T], y);
+  }
+  return y;
+}
+
+template <int M, int Q>
+__device__ __forceinline__ void scan_short_four(float d, float dx, const float* sB, const float* sC, const float (&A)[M],
+                                                float (&h)[M], float (&v)[16]) {
+  f32x4 B[M], C[M];
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    B[m] = *reinterpret_cast<const f32x4*>(sB + 16 * m * kScanPitch + 4 * Q);
+    C[m] = *reinterpret_cast<const f32x4*>(sC + 16 * m * kScanPitch + 4 * Q);
+  }
+  v[4 * Q] = scan_short_token<M, Q, 0>(d, dx, B, C, A, h);
+  v[4 * Q + 1] = scan_short_token<M, Q, 1>(d, dx, B, C, A, h);
+  v[4 * Q + 2] = scan_short_token<M, Q, 2>(d, dx, B, C, A, h);
+  v[4 * Q + 3] = scan_short_token<M, Q, 3>(d, dx, B, C, A, h);
+}
+
+// For few channels and short sequences, where a tile's latency is the time: a wavefront owns 4 channels, lane 16 q + j the
+// states j, 16 + j, .. of channel q, a quarter of scan_kernel's work in one lane.  Step sizes and inputs are broadcast from
+// the lane of their token; B and C go through LDS to the lanes of their states.  97 tokens of 1,024 channels: 7.0 us, 13.3 by
+// scan_kernel; it takes 1.8 times the instructions for each token and channel, which is why the long and wide ones go there.
+template <int IT, int N>
+__global__ __launch_bounds__(kScanBlock) void scan_short_kernel(ScanArgs a) {
+  constexpr int es = sizeof(typename Mma<IT>::elem);
+  constexpr int M = N / 16;
+  __shared__ alignas(16) float lds[kScanBlock / 64][2][N * kScanPitch];
+  const int tid = threadIdx.x, lane = tid & 63, j = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int s = blockIdx.x / a.blocks, c0 = (blockIdx.x - s * a.blocks) * kScanShortChannels + 4 * wave;
+  if (c0 >= a.channels) return;
+  const int slot = sload(a.slots + s);
+  if (slot == a.pad || slot < 0 || slot >= a.num_slots) return;
+  int start = sload(a.seq_start + s), end = sload(a.seq_start + s + 1);
+  start = start < 0 ? 0 : (start > a.num_tokens ? a.num_tokens : start);
+  end = end < start ? start : (end > a.num_tokens ? a.num_tokens : end);
+  const int n = end - start < a.max_seq_len ? end - start : a.max_seq_len;
+  const int c = c0 + q;                                       // channels come in eights: all four are there
+  const int gN = a.groups * N;
+  ScanRows xr, dr, zr, Br, Cr, yr;
+  xr.start(a.x, start, a.x_stride, a.channels * es, es);
+  dr.start(a.dt, start, a.dt_stride, a.channels * es, es);
+  Br.start(a.B, start, a.B_stride, gN * es, es);
+  Cr.start(a.C, start, a.C_stride, gN * es, es);
+  yr.start(a.y, start, a.y_stride, a.channels * es, es);
+  const bool gated = a.z != nullptr;
+  zr.start(gated ? a.z : a.x, start, gated ? a.z_stride : a.x_stride, a.channels * es, es);
+  const uint32_t row = static_cast<uint32_t>(c0 / a.per_group) * N;
+  const uint32_t xo = j * xr.step + c * es, dto = j * dr.step + c * es, zo = j * zr.step + c * es, yo = j * yr.step + c * es;
+  const uint32_t Bo = j * Br.step + (row + 4 * q) * es, Co = j * Cr.step + (row + 4 * q) * es;
+  uint32_t rx = 0, rd = 0, rz = 0;
+  ScanFour<IT> rB[M], rC[M];
+  const auto fetch = [&](int rows) {
+    rx = scan_one_load<IT>(xr.tile(rows), xo);
+    rd = scan_one_load<IT>(dr.tile(rows), dto);
+    rz = scan_one_load<IT>(zr.tile(rows), zo);
+    const rsrc_t rb = Br.tile(rows), rc = Cr.tile(rows);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      rB[m].load(rb, Bo + 16 * m * es);
+      rC[m].load(rc, Co + 16 * m * es);
+    }
+    xr.next();
+    dr.next();
+    zr.next();
+    Br.next();
+    Cr.next();
+  };
+  if (n > 0) fetch(n);
+  const int64_t st0 = slot * a.state_stride + static_cast<int64_t>(c) * N + j;
+  float A[M], h[M];
+  const bool load = a.load_state == nullptr || sload(a.load_state + s) != 0;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    A[m] = scan_rate(gload(a.A + static_cast<int64_t>(c) * N + j + 16 * m));
+    h[m] = load ? scan_state_load(a.state, st0 + 16 * m, a.state_dtype) : 0.0f;
+  }
+  const float bias = a.dt_bias != nullptr ? gload(a.dt_bias + c) : 0.0f;
+  const float D = a.D != nullptr ? gload(a.D + c) : 0.0f;
+  float* const wB = lds[wave][0] + 4 * q * kScanPitch + j;    // token j, states 16 m + 4 q ..
+  float* const wC = lds[wave][1] + 4 * q * kScanPitch + j;
+  const float* const sB = lds[wave][0] + j * kScanPitch;      // states 16 m + j
+  const float* const sC = lds[wave][1] + j * kScanPitch;
+  for (int t0 = 0; t0 < n; t0 += kScanTile) {
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        wB[(16 * m + r) * kScanPitch] = rB[m].get(r);
+        wC[(16 * m + r) * kScanPitch] = rC[m].get(r);
+      }
+    }
+    const float x = scan_one<IT>(rx), z = scan_one<IT>(rz);
+    float d = scan_step_size(scan_one<IT>(rd), bias, a.dt_softplus);
+    d = t0 + j < n ? d : 0.0f;
+    const float dx = d * x;
+    if (t0 + kScanTile < n) fetch(n - t0 - kScanTile);
+    scan_wave_sync();
+    float v[16];
+    scan_short_four<M, 0>(d, dx, sB, sC, A, h, v);
+    scan_short_four<M, 1>(d, dx, sB, sC, A, h, v);
+    scan_short_four<M, 2>(d, dx, sB, sC, A, h, v);
+    scan_short_four<M, 3>(d, dx, sB, sC, A, h, v);
+    float y = fmaf(D, x, row_sums(v, j));
+    if (gated) y *= silu(z);
+    const rsrc_t ry = yr.tile(n - t0);
+    if constexpr (IT == kF32) bstore_f32(ry, yo, 0, y);
+    else if constexpr (IT == kBF16) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<__bf16>(y)), ry, yo, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<_Float16>(y)), ry, yo, 0, 0);
+    yr.next();
+    scan_wave_sync();
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m) scan_state_store(a.state, st0 + 16 * m, a.state_dtype, h[m]);
 }
 
 // v summed over LPC neighbouring lanes (2 to 16), the same sum in each.

@@ -87,6 +87,19 @@ def test_stretches(rp, it, st, n):
     check(rp, p)
 
 
+@pytest.mark.parametrize("it", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("st,n,G", [("f32", 16, 1), ("bf16", 32, 4), ("f16", 64, 2)])
+def test_wide_batches(rp, it, st, n, G):
+    """Enough channels for the form with 16 of them a wavefront, no stretches; with and without all inputs."""
+    p = inputs([17, 0, 1, 48, 15, 16, 33, 2, 31], 2048, n, G, it, st, seed=n)
+    check(rp, p)
+    check(rp, p, use=("bias",))
+
+
+def test_more_sequences_than_are_sorted(rp):
+    check(rp, inputs([(7 * i) % 23 for i in range(70)], 512, seed=3))
+
+
 def test_channels_fill_the_device(rp):
     check(rp, inputs([70, 3, 40], 64 * 100, seed=4))
 
@@ -193,17 +206,29 @@ def test_extreme_rates_and_steps(rp):
 
 
 @pytest.mark.parametrize("it", ["bf16", "f32"])
-def test_a_bad_value_reaches_later_tokens_of_its_channel_only(rp, it):
-    p = inputs([50, 9], 64, it=it, seed=14)
+@pytest.mark.parametrize("Ch", [64, 8448])
+def test_a_bad_value_reaches_later_tokens_of_its_channel_only(rp, it, Ch):
+    p = inputs([50, 9], Ch, it=it, seed=14)
     p["x"][21, 5] = math.inf
     p["z"][30, 6] = math.nan
     p["dt"][40, 7] = math.nan
-    y = torch.empty(59, 64, dtype=DT[it], device="cuda")
+    y = torch.empty(59, Ch, dtype=DT[it], device="cuda")
     call(rp, p, on_device(p), y, p["state"].cuda())
     odd = ~torch.isfinite(y.float().cpu())
-    seen = torch.zeros(59, 64, dtype=torch.bool)
+    seen = torch.zeros(59, Ch, dtype=torch.bool)
     seen[21:50, 5] = seen[30, 6] = seen[40:50, 7] = True
     assert not (odd & ~seen).any() and odd[21:50, 5].all()
+
+
+@pytest.mark.parametrize("lens,Ch", [([20, 9], 64), ([700], 64), ([20] * 9, 2048)])
+def test_a_rate_that_is_not_a_number(rp, lens, Ch):
+    """In each of the forms it reaches its channel, and that one alone."""
+    p = inputs(lens, Ch, seed=18)
+    p["A"][5, 7] = math.nan
+    y = torch.empty(sum(lens), Ch, dtype=torch.bfloat16, device="cuda")
+    call(rp, p, on_device(p), y, p["state"].cuda())
+    odd = ~torch.isfinite(y.float())
+    assert odd[:, 5].all() and int(odd.sum()) == sum(lens)
 
 
 def test_bad_values_of_other_sequences_rows(rp):
