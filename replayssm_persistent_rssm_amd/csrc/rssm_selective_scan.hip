@@ -241,13 +241,14 @@ rssm_status rssm_selective_scan_step(const rssm_selective_scan_desc* d, const rs
   if (st != RSSM_OK) return st;
   ScanArgs a;
   fill_args(&a, d, t);
-  const int lanes = d->dstate * (d->state_dtype == RSSM_F32 ? 4 : 2) / 16, per = kScanBlock / lanes;   // lanes a channel
+  const int lanes = d->dstate * (d->state_dtype == RSSM_F32 ? 4 : 2) / 16;   // a channel
+  const int per = kScanBlock / lanes * (lanes < 4 ? 2 : 4);                  // channels a workgroup
   a.blocks = (d->channels + per - 1) / per;
-  const int R = static_cast<int64_t>(d->num_seqs) * a.blocks >= 4096 ? 4 : 1;
+  const int Q = static_cast<int64_t>(d->num_seqs) * a.blocks >= 2048 ? 2 : 1;
   if (verbose())
     std::fprintf(stderr, "[rssm_selective_scan_step] %s/%s requests=%d channels=%d dstate=%d\n", dtype_name(d->state_dtype),
                  dtype_name(d->input_dtype), d->num_seqs, d->channels, d->dstate);
-  return launch(kernel_for(R == 4 ? kScanStepFour : kScanStepOne, d), (d->num_seqs + static_cast<int64_t>(R) - 1) / R * a.blocks,
+  return launch(kernel_for(Q == 2 ? kScanStepTwo : kScanStepOne, d), (d->num_seqs + static_cast<int64_t>(Q) - 1) / Q * a.blocks,
                 &a, hip_stream, "selective_scan_step");
 }
 

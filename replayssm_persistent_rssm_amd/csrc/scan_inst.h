@@ -5,23 +5,23 @@
 
 namespace rssm {
 
-enum : int { kScanMain = 0, kScanFold = 1, kScanStepOne = 2, kScanStepFour = 3, kScanShort = 4 };
+enum : int { kScanMain = 0, kScanFold = 1, kScanStepOne = 2, kScanStepTwo = 3, kScanShort = 4 };
 
 template <int IT, int N>
 const void* scan_fn(int which, int state_dtype) {
   if (which == kScanMain) return reinterpret_cast<const void*>(&scan_kernel<IT, N, false>);
   if (which == kScanFold) return reinterpret_cast<const void*>(&scan_kernel<IT, N, true>);
   if (which == kScanShort) return reinterpret_cast<const void*>(&scan_short_kernel<IT, N>);
-  const bool four = which == kScanStepFour;
+  const bool two = which == kScanStepTwo;
   switch (state_dtype) {
     case kF32:
-      return four ? reinterpret_cast<const void*>(&scan_step_kernel<IT, kF32, N, 4>)
+      return two ? reinterpret_cast<const void*>(&scan_step_kernel<IT, kF32, N, 2>)
                   : reinterpret_cast<const void*>(&scan_step_kernel<IT, kF32, N, 1>);
     case kBF16:
-      return four ? reinterpret_cast<const void*>(&scan_step_kernel<IT, kBF16, N, 4>)
+      return two ? reinterpret_cast<const void*>(&scan_step_kernel<IT, kBF16, N, 2>)
                   : reinterpret_cast<const void*>(&scan_step_kernel<IT, kBF16, N, 1>);
     default:
-      return four ? reinterpret_cast<const void*>(&scan_step_kernel<IT, kF16, N, 4>)
+      return two ? reinterpret_cast<const void*>(&scan_step_kernel<IT, kF16, N, 2>)
                   : reinterpret_cast<const void*>(&scan_step_kernel<IT, kF16, N, 1>);
   }
 }

@@ -119,7 +119,8 @@ def test_step_sizes_as_they_are(rp):
 
 @pytest.mark.parametrize("it", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("st", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("S,Ch,n,G", [(1, 8, 16, 1), (5, 104, 16, 1), (67, 96, 32, 2), (9, 128, 64, 2), (260, 64 * 20, 16, 1)])
+@pytest.mark.parametrize("S,Ch,n,G", [(1, 8, 16, 1), (5, 104, 16, 1), (67, 96, 32, 2), (9, 128, 64, 2), (260, 64 * 20, 16, 1),
+                                       (3, 96, 16, 6), (6, 240, 32, 5), (130, 16 * 66, 16, 66)])
 def test_step(rp, it, st, S, Ch, n, G):
     check(rp, inputs([1] * S, Ch, n, G, it, st, seed=S + n), step=True)
 
