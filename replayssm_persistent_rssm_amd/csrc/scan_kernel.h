@@ -276,8 +276,10 @@ __device__ __forceinline__ float scan_four(const float (&dt)[kScanTile], const f
   return rows_sum(halves_sum(p0, p2), halves_sum(p1, p3));   // row g: token 4 Q + g
 }
 
+// Two wavefronts a SIMD keep the results of the matrix instructions out of the accumulation registers; the widest instance, which
+// comes within a few registers of spilling at that, may take one.
 template <int IT, int N, bool FOLD>
-__global__ __launch_bounds__(kScanBlock, 2) void scan_kernel(ScanArgs a) {
+__global__ __launch_bounds__(kScanBlock, IT == kF32 && N == 64 ? 1 : 2) void scan_kernel(ScanArgs a) {
   constexpr int es = sizeof(typename Mma<IT>::elem);
   constexpr int M = N / 16;
   __shared__ alignas(16) float lds[kScanBlock / 64][3][kScanTile * kScanPitch];
