@@ -49,6 +49,28 @@ void* addr(PyObject* o, int dev, at::ScalarType st, std::initializer_list<int64_
   return t.data_ptr();
 }
 
+// A tensor on the device, of any strides.
+const at::Tensor& look(PyObject* o, int dev) {
+  need(THPVariable_Check(o));
+  const at::Tensor& t = THPVariable_Unpack(o);
+  need(t.layout() == at::kStrided && t.is_cuda() && t.get_device() == dev);
+  return t;
+}
+
+// Address and row stride of a tensor of this dtype and shape whose rows are dense inside; the stride of a single row says
+// nothing.
+void* rows(PyObject* o, int dev, at::ScalarType st, std::initializer_list<int64_t> shape, int64_t* stride) {
+  const at::Tensor& t = look(o, dev);
+  need(t.scalar_type() == st && t.sizes() == at::IntArrayRef(shape));
+  int64_t dense = 1;
+  for (int64_t i = t.dim() - 1; i > 0; --i) {
+    need(t.size(i) == 1 || t.stride(i) == dense);
+    dense *= t.size(i);
+  }
+  *stride = t.size(0) > 1 ? t.stride(0) : dense;
+  return t.data_ptr();
+}
+
 void* opt(PyObject* o, int dev, at::ScalarType st, std::initializer_list<int64_t> shape) {
   return o == Py_None ? nullptr : addr(o, dev, st, shape);
 }
@@ -98,25 +120,25 @@ at::Tensor workspace(PyObject* given, int64_t bytes, int dev) {
   return at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(at::Device(at::kCUDA, dev)));
 }
 
-// Whether every tensor among the arguments is contiguous and on device a[0].  Asked first, so that views, the
+// Whether every tensor among the arguments is on device a[0], and contiguous unless views are taken.  Asked first, so that views, the
 // other ordinary case, do not pay for an exception (1 to 3 us) before the binding's Python code takes them.
-bool plain(PyObject* const* a, Py_ssize_t n) {
+bool plain(PyObject* const* a, Py_ssize_t n, bool views) {
   if (n < 2 || !PyLong_Check(a[0])) return false;
   int over = 0;
   const long dev = PyLong_AsLongAndOverflow(a[0], &over);
   for (Py_ssize_t i = 2; i < n; ++i) {
     if (!THPVariable_Check(a[i])) continue;
     const at::Tensor& t = THPVariable_Unpack(a[i]);
-    if (t.layout() != at::kStrided || !t.is_cuda() || t.get_device() != dev || !t.is_contiguous()) return false;
+    if (t.layout() != at::kStrided || !t.is_cuda() || t.get_device() != dev || (!views && !t.is_contiguous())) return false;
   }
   return true;
 }
 
 template <typename F>
-PyObject* guarded(PyObject* const* a, Py_ssize_t n, F f) {
+PyObject* guarded(PyObject* const* a, Py_ssize_t n, F f, bool views = false) {
   bool done = false;
   try {
-    done = plain(a, n) && f();
+    done = plain(a, n, views) && f();
   } catch (...) {
     if (PyErr_Occurred()) PyErr_Clear();
     done = false;
@@ -296,7 +318,7 @@ PyObject* causal_conv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(n == 13);
     const int dev = i32(a[0]);
     const bool step = a[2] == Py_True;
-    const at::Tensor &x = tensor(a[3], dev), &w = tensor(a[4], dev), &state = tensor(a[6], dev), &slots = tensor(a[7], dev);
+    const at::Tensor &x = look(a[3], dev), &w = tensor(a[4], dev), &state = look(a[6], dev), &slots = tensor(a[7], dev);
     need(x.dim() == 2 && w.dim() == 2 && state.dim() == 3 && slots.dim() == 1);
     const int64_t N = x.size(0), C = x.size(1), W = w.size(0), S = state.size(0), R = slots.size(0);
     const at::ScalarType it = x.scalar_type();
@@ -309,20 +331,18 @@ PyObject* causal_conv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.pad_slot_id = i32(a[12]);
     d.dtype = code_of(it);
     d.silu = PyObject_IsTrue(a[11]) == 1;
-    d.state_slot_stride = (W - 1) * C;
-    d.x_token_stride = d.y_token_stride = C;
     rssm_causal_conv_tables t{};
-    t.x = x.data_ptr();
+    t.x = rows(a[3], dev, it, {N, C}, &d.x_token_stride);
     t.weight = static_cast<const float*>(addr(a[4], dev, at::kFloat, {W, C}));
     t.bias = static_cast<const float*>(opt(a[9], dev, at::kFloat, {C}));
-    t.y = addr(a[5], dev, it, {N, C});
-    t.state = addr(a[6], dev, it, {S, W - 1, C});
+    t.y = rows(a[5], dev, it, {N, C}, &d.y_token_stride);
+    t.state = rows(a[6], dev, it, {S, W - 1, C}, &d.state_slot_stride);
     t.slots = static_cast<const int32_t*>(addr(a[7], dev, at::kInt, {R}));
     if (step) return rssm_causal_conv_step(&d, &t, stream(a[1])) == RSSM_OK;
     t.seq_start = static_cast<const int32_t*>(addr(a[8], dev, at::kInt, {R + 1}));
     t.load_state = static_cast<const int32_t*>(opt(a[10], dev, at::kInt, {R}));
     return rssm_causal_conv(&d, &t, stream(a[1])) == RSSM_OK;
-  });
+  }, true);
 }
 
 // (device, stream, step, state, A, x, B, C, dt, y, slots, seq_start, max_seq_len, load_state, D, dt_bias, z,
@@ -332,7 +352,7 @@ PyObject* selective_scan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(n == 20);
     const int dev = i32(a[0]);
     const bool step = a[2] == Py_True;
-    const at::Tensor &state = tensor(a[3], dev), &x = tensor(a[5], dev), &B = tensor(a[6], dev), &slots = tensor(a[10], dev);
+    const at::Tensor &state = look(a[3], dev), &x = look(a[5], dev), &B = look(a[6], dev), &slots = tensor(a[10], dev);
     need(state.dim() == 3 && x.dim() == 2 && B.dim() == 3 && slots.dim() == 1);
     const int64_t S = state.size(0), Ch = state.size(1), ds = state.size(2), N = x.size(0), G = B.size(1), R = slots.size(0);
     const at::ScalarType it = x.scalar_type();
@@ -348,20 +368,18 @@ PyObject* selective_scan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.state_dtype = code_of(state.scalar_type());
     d.input_dtype = code_of(it);
     d.dt_softplus = PyObject_IsTrue(a[17]) == 1;
-    d.state_slot_stride = Ch * ds;
-    d.x_token_stride = d.dt_token_stride = d.z_token_stride = d.y_token_stride = Ch;
-    d.B_token_stride = d.C_token_stride = G * ds;
     rssm_selective_scan_tables t{};
-    t.state = state.data_ptr();
+    t.state = rows(a[3], dev, state.scalar_type(), {S, Ch, ds}, &d.state_slot_stride);
     t.A = static_cast<const float*>(addr(a[4], dev, at::kFloat, {Ch, ds}));
     t.D = static_cast<const float*>(opt(a[14], dev, at::kFloat, {Ch}));
     t.dt_bias = static_cast<const float*>(opt(a[15], dev, at::kFloat, {Ch}));
-    t.x = addr(a[5], dev, it, {N, Ch});
-    t.B = addr(a[6], dev, it, {N, G, ds});
-    t.C = addr(a[7], dev, it, {N, G, ds});
-    t.dt = addr(a[8], dev, it, {N, Ch});
-    t.y = addr(a[9], dev, it, {N, Ch});
-    t.z = opt(a[16], dev, it, {N, Ch});
+    t.x = rows(a[5], dev, it, {N, Ch}, &d.x_token_stride);
+    t.B = rows(a[6], dev, it, {N, G, ds}, &d.B_token_stride);
+    t.C = rows(a[7], dev, it, {N, G, ds}, &d.C_token_stride);
+    t.dt = rows(a[8], dev, it, {N, Ch}, &d.dt_token_stride);
+    t.y = rows(a[9], dev, it, {N, Ch}, &d.y_token_stride);
+    d.z_token_stride = d.x_token_stride;
+    if (a[16] != Py_None) t.z = rows(a[16], dev, it, {N, Ch}, &d.z_token_stride);
     t.slots = static_cast<const int32_t*>(addr(a[10], dev, at::kInt, {R}));
     if (step) return rssm_selective_scan_step(&d, &t, stream(a[1])) == RSSM_OK;
     t.seq_start = static_cast<const int32_t*>(addr(a[11], dev, at::kInt, {R + 1}));
@@ -374,7 +392,7 @@ PyObject* selective_scan(PyObject*, PyObject* const* a, Py_ssize_t n) {
       d.workspace_bytes = static_cast<int64_t>(ws.nbytes());
     }
     return rssm_selective_scan(&d, &t, stream(a[1])) == RSSM_OK;
-  });
+  }, true);
 }
 
 // (device, stream, q, q_out, k_cache, v_cache, k_new, v_new, page_table, seq_start, kv_len, inv_freq, interleaved,
@@ -387,7 +405,7 @@ PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     rssm_paged_attention_tables pt{};
     at::ScalarType st;
     caches(a[4], a[5], a[8], a[9], a[10], dev, &p, &pt, &st);
-    const at::Tensor &q = tensor(a[2], dev), &f = tensor(a[11], dev);
+    const at::Tensor &q = look(a[2], dev), &f = tensor(a[11], dev);
     need(q.dim() == 3 && f.dim() == 1);
     const int64_t N = q.size(0), Hq = q.size(1), D = p.head_dim, Hkv = p.num_kv_heads;
     rssm_rotary_desc d{};
@@ -407,13 +425,11 @@ PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.page_stride = p.page_stride;
     d.row_stride = p.row_stride;
     d.head_stride = p.head_stride;
-    d.q_token_stride = d.q_out_token_stride = Hq * D;
-    d.k_token_stride = d.v_token_stride = Hkv * D;
     d.table_stride = p.table_stride;
-    t.q = addr(a[2], dev, st, {N, Hq, D});
-    t.q_out = addr(a[3], dev, st, {N, Hq, D});
-    t.k_new = addr(a[6], dev, st, {N, Hkv, D});
-    t.v_new = addr(a[7], dev, st, {N, Hkv, D});
+    t.q = rows(a[2], dev, st, {N, Hq, D}, &d.q_token_stride);
+    t.q_out = rows(a[3], dev, st, {N, Hq, D}, &d.q_out_token_stride);
+    t.k_new = rows(a[6], dev, st, {N, Hkv, D}, &d.k_token_stride);
+    t.v_new = rows(a[7], dev, st, {N, Hkv, D}, &d.v_token_stride);
     t.k_cache = pt.k_cache;
     t.v_cache = pt.v_cache;
     t.page_table = pt.page_table;
@@ -422,7 +438,7 @@ PyObject* rotary_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     t.positions = static_cast<const int32_t*>(opt(a[14], dev, at::kInt, {N}));
     t.inv_freq = static_cast<const float*>(addr(a[11], dev, at::kFloat, {f.size(0)}));
     return rssm_rotary_append(&d, &t, stream(a[1])) == RSSM_OK;
-  });
+  }, true);
 }
 
 // The page pool's fields: page_table, kv_len, page_ref and page_size.
