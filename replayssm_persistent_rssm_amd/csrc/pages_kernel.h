@@ -3,8 +3,9 @@
 //
 // The bookkeeping of a call is integers that depend on one another through prefix sums (an item's pages follow those of
 // the items before it, a free page is found by its rank), so one workgroup of 1024 threads does it and leaves a plan in the
-// workspace; the second kernel carries the plan out with the whole device.  Bytes move in tasks of 16 KiB that the
-// workgroups take in turn: bound by memory where there is much to copy, by the two launches otherwise.
+// workspace (3.3 us for 4 items, 5 to 6 for 128); the second kernel carries the plan out with the whole device.  Bytes move
+// in tasks of 16 KiB that the workgroups take in turn: bound by memory where there is much to copy (128 forks in 32
+// caches of 32 KiB pages, 67 MB in and out: 20 us), by the two launches otherwise.
 #pragma once
 
 #include "mma_device.h"

@@ -87,8 +87,8 @@ const void* instance(bool step, int size) {
   if (step)
     return size > 1 ? reinterpret_cast<const void*>(&conv_step_kernel<DT, W, 4>)
                     : reinterpret_cast<const void*>(&conv_step_kernel<DT, W, 1>);
-  return size > 8 ? reinterpret_cast<const void*>(&conv_prompt_kernel<DT, W, 32>)
-                  : reinterpret_cast<const void*>(&conv_prompt_kernel<DT, W, 8>);
+  return size > 4 ? reinterpret_cast<const void*>(&conv_prompt_kernel<DT, W, 8>)
+                  : reinterpret_cast<const void*>(&conv_prompt_kernel<DT, W, 4>);
 }
 
 template <int DT>
@@ -133,8 +133,12 @@ rssm_status rssm_causal_conv(const rssm_causal_conv_desc* d, const rssm_causal_c
   if (st != RSSM_OK) return st;
   ConvArgs a;
   fill_args(&a, d, t);
-  const int64_t tiles32 = d->num_tokens / 32 + static_cast<int64_t>(d->num_seqs) + 1;
-  const int size = tiles32 * a.blocks >= 4096 ? 32 : 8;
+  // tiles of 8 tokens; of 4 where those would be at most 8,192 wavefronts and a tile's latency counts (us with 4 and 8: 97 tokens,
+  // 1,024 channels 3.6, 4.5; 300 tokens, 18,432 channels 7.0, 8.2; 1,000 tokens 14.7, 15.4; 4,000 tokens, 18,000
+  // wavefronts, 66, 60).  Longer tiles read fewer rows twice and gain nothing by it (16,384 tokens, 18,432 channels: 221 with 8,
+  // 226 with 16, 228 with 32, 243 with 64)
+  const int64_t tiles = d->num_tokens / 8 + static_cast<int64_t>(d->num_seqs);
+  const int size = tiles * a.blocks > 8192 ? 8 : 4;
   return launch(&a, d, false, size, d->num_tokens / size + static_cast<int64_t>(d->num_seqs), hip_stream);
 }
 

@@ -19,6 +19,9 @@
 // When sequences and channels leave compute units empty, the token axis is split: scan_kernel<FOLD> gives
 // each stretch's own end state and the sum of its step sizes (a decay over the stretch is exp(A sum)), and
 // the main kernel starts each stretch from those of the stretches before it.
+// 12 ragged prompts up to 2,011 tokens, 8,192 bf16 channels of 16 states: 417 us, the vector ALUs busy throughout (416
+// instructions a tile, 256 of them the four an element); one of 16,384 tokens, 4,096 channels: 414 us in 24
+// stretches, 147 us of vector work in the fold and 218 in the main kernel.
 // scan_step_kernel: a lane has 16 bytes of a channel's states; bound by reading and writing the state.
 #pragma once
 

@@ -61,9 +61,15 @@ def test_lengths(rp, lens):
     check(rp, inputs(lens, 64, 4, "bf16", seed=len(lens)))
 
 
-def test_many_tokens_take_longer_tiles(rp):
-    """Enough work for tiles of 32 tokens: sequence ends inside and at their borders."""
+def test_many_channels(rp):
+    """More than a launch of the small cases: sequence ends inside tiles and at their borders."""
     check(rp, inputs([31, 1, 32, 33, 0, 64, 2, 95, 100], 512 * 300, 4, "bf16", seed=3))
+
+
+@pytest.mark.parametrize("it,W", [("bf16", 2), ("f16", 3), ("f32", 4), ("bf16", 4)])
+def test_longer_tiles(rp, it, W):
+    """Over 8,192 wavefronts' work: tiles of 8 tokens, ends inside and at their borders."""
+    check(rp, inputs([7, 8, 9, 0, 1, 2, 16, 41, 3, 0], 512 * 420, W, it, seed=W))
 
 
 def test_more_sequences_than_a_wavefront(rp):
