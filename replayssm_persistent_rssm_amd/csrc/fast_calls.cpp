@@ -3,12 +3,14 @@
 //
 // At their smallest these operators are a few microseconds of GPU work, as long as
 // Python needs to read the attributes of their tensors.  Each function here
-// takes the binding's arguments, checks that every tensor is contiguous, on the
+// takes the binding's arguments, checks that every tensor is contiguous (the convolution, selective scan and
+// rotary calls also take rows of wider ones, as a packed projection gives them), on the
 // given device and of the expected dtype and shape, and makes the C call.  It returns True when the
 // call was enqueued; on anything else (strided views, wrong arguments, a library error) it returns
 // False, and the binding's Python code handles the call or names the error.  Nothing has been enqueued
 // then, unless a later launch of a call that has several failed: the binding's call then starts over, and only
-// the last launch of each writes what the caller sees.
+// the last launch of each writes what the caller sees.  (A page fork and a compaction change the tables with their
+// first launch: a launch that fails raises here and is not repeated.)
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -30,6 +32,7 @@
 namespace {
 
 struct NotCommon {};   // leaves a function towards `return False`
+struct Failed {};      // leaves a function towards an exception with the library's error
 
 void need(bool ok) {
   if (!ok) throw NotCommon();
@@ -139,6 +142,9 @@ PyObject* guarded(PyObject* const* a, Py_ssize_t n, F f, bool views = false) {
   bool done = false;
   try {
     done = plain(a, n, views) && f();
+  } catch (const Failed&) {
+    PyErr_SetString(PyExc_RuntimeError, rssm_last_error());
+    return nullptr;
   } catch (...) {
     if (PyErr_Occurred()) PyErr_Clear();
     done = false;
@@ -485,6 +491,12 @@ at::Tensor pool_workspace(PyObject* given, int dev, rssm_pages_desc* d, rssm_pag
   return ws;
 }
 
+// Whether a call of two launches, the first of which changes the tables, was enqueued.
+bool enqueued(rssm_status st) {
+  if (st == RSSM_ERR_HIP) throw Failed();
+  return st == RSSM_OK;
+}
+
 // (device, stream, page_table, kv_len, page_ref, rows, add, status, page_size, workspace)
 PyObject* page_extend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(a, n, [&] {
@@ -517,7 +529,7 @@ PyObject* page_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     pool_caches(a[2], a[10], a[11], dev, &d, &t);
     d.token_bytes = integer(a[12]);
     const at::Tensor ws = pool_workspace(a[14], dev, &d, &t);
-    return rssm_page_fork(&d, &t, stream(a[1])) == RSSM_OK;
+    return enqueued(rssm_page_fork(&d, &t, stream(a[1])));
   });
 }
 
@@ -546,7 +558,7 @@ PyObject* page_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     pool_caches(a[2], a[8], a[9], dev, &d, &t);
     t.live = static_cast<int32_t*>(addr(a[6], dev, at::kInt, {1}));
     const at::Tensor ws = pool_workspace(a[10], dev, &d, &t);
-    return rssm_page_compact(&d, &t, stream(a[1])) == RSSM_OK;
+    return enqueued(rssm_page_compact(&d, &t, stream(a[1])));
   });
 }
 
