@@ -104,10 +104,14 @@ int64_t main_blocks(const rssm_selective_scan_desc* d) { return (d->channels + k
 // Few channels and short sequences go to scan_short_kernel: up to 4,096 wavefronts of it (four a SIMD) and 512 tokens
 // (us with it and without: 12 prompts of 200, 1,024 channels: 24.4, 33.6; one of 200, 8,192 channels: 17.5, 21.6; of 400,
 // 4,096 channels: 19.2, 21.6; of 1,000: 41.3, 43.7 and with 8,192 channels 67.4, 63.6), 320 tokens where stretches would have
-// most of the device to themselves (1,024 channels: 14.3, 14.9 for 300 tokens, 17.9, 15.2 for 400).
+// most of the device to themselves (1,024 channels: 14.3, 14.9 for 300 tokens, 17.9, 15.2 for 400).  More states a channel
+// make the other form's tiles longer and this one's sums cheaper: with 32 and 64 of them up to 2,048 tokens while there are at
+// most 2,048 wavefronts (2,000 tokens, 4,096 channels: 107, 113 and 174, 206; 8,192: 179, 195 and 327, 367; 8 of 1,000,
+// 2,048 channels, 4,096 wavefronts: 190, 184).
 bool is_short(const rssm_selective_scan_desc* d) {
   const int64_t waves = static_cast<int64_t>(d->num_seqs) * ((d->channels + 3) / 4);
-  return waves <= 4096 && d->max_seq_len <= (waves <= 512 ? 320 : 512);
+  const int longest = waves <= 512 ? 320 : d->dstate > 16 && waves <= 2048 ? 2048 : 512;
+  return waves <= 4096 && d->max_seq_len <= longest;
 }
 
 // Stretches of the token axis.  All but the last are folded once more than they are computed (70 % of a

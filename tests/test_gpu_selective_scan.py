@@ -96,6 +96,12 @@ def test_wide_batches(rp, it, st, n, G):
     check(rp, p, use=("bias",))
 
 
+@pytest.mark.parametrize("n,lens,Ch", [(32, [700], 2056), (64, [600, 3], 1040), (32, [700, 40], 4200)])
+def test_long_sequences_of_many_states(rp, n, lens, Ch):
+    """At either side of the choice between the forms."""
+    check(rp, inputs(lens, Ch, n, 1, "bf16", "f32", seed=n))
+
+
 def test_more_sequences_than_are_sorted(rp):
     check(rp, inputs([(7 * i) % 23 for i in range(70)], 512, seed=3))
 
