@@ -6,7 +6,7 @@
 // elements of a head that hold 8 whole pairs: vectors 2u and 2u + 1 when interleaved, vectors u and
 // u + rot_dim / 16 otherwise; units past rot_dim pass through.  Few tokens are shared out over up to 8 wavefronts each.  Bound
 // by memory: 18,900 ragged fp16 tokens of 32 + 2 x 8 heads of 128: 95 us, 4.9 TB/s, the rate of a large copy (past the caches
-// 138 us); a decoding batch of 64 tokens by the launch, 3.8 us.
+// 138 us); a decoding batch of 64 tokens by the launch, 4.1 us.
 #pragma once
 
 #include "mma_device.h"

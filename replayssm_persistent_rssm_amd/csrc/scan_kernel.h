@@ -25,8 +25,6 @@
 // scan_step_kernel: a lane has 16 bytes of a channel's states; bound by reading and writing the state.
 #pragma once
 
-#include <utility>
-
 #include "mma_device.h"
 
 namespace rssm {
