@@ -106,8 +106,9 @@ rssm_status rssm_selective_scan_workspace(const rssm_selective_scan_desc *desc, 
 
 /* Enqueue the prompt form on `hip_stream`.  fp32 arithmetic throughout, one rounding of each output.
  * Token t's output depends on tokens up to t only, non-finite inputs included.  With a split token axis
- * (workspace above 0) the state that enters a stretch is put together from the stretches before it; an
- * infinity that a whole stretch decays to nothing comes out as NaN there. */
+ * (workspace above 0) one launch reads the pool and the next one writes it, and the state that enters a
+ * stretch is put together from the stretches before it; an infinity that a whole stretch decays to nothing
+ * comes out as NaN there. */
 rssm_status rssm_selective_scan(const rssm_selective_scan_desc *desc, const rssm_selective_scan_tables *tables,
                                 void *hip_stream);
 

@@ -18,7 +18,8 @@
 //    (6 instructions for 4 tokens), and go back to the tile's layout through LDS for skip, gate and store.
 // When sequences and channels leave compute units empty, the token axis is split: scan_kernel<FOLD> gives
 // each stretch's own end state and the sum of its step sizes (a decay over the stretch is exp(A sum)), and
-// the main kernel starts each stretch from those of the stretches before it.
+// the main kernel starts each stretch from those of the stretches before it.  The state pool is read by one launch
+// and written by the other.
 // 12 ragged prompts up to 2,011 tokens, 8,192 bf16 channels of 16 states: 417 us, the vector ALUs busy throughout (416
 // instructions a tile, 256 of them the four an element); one of 16,384 tokens, 4,096 channels: 414 us in 24
 // stretches, 147 us of vector work in the fold and 218 in the main kernel.
@@ -43,7 +44,7 @@ struct ScanArgs {
   const int32_t* slots;
   const int32_t* seq_start;
   const int32_t* load_state;  // or null
-  float* ws_h;                // [num_seqs][nseg][channels][N] (nseg > 1)
+  float* ws_h;                // [num_seqs][nseg][channels][N] (nseg > 1): ends of stretches; of the last one the start of the first
   float* ws_d;                // [num_seqs][nseg][channels]
   int64_t state_stride, x_stride, dt_stride, B_stride, C_stride, z_stride, y_stride;   // elements
   int32_t num_seqs, num_tokens, channels, groups, per_group, num_slots, pad, max_seq_len, dt_softplus, state_dtype;
@@ -314,11 +315,25 @@ __global__ __launch_bounds__(kScanBlock, IT == kF32 && N == 64 ? 1 : 2) void sca
     st.A[i] = has_j ? scan_rate(gload(a.A + static_cast<int64_t>(cj) * N + 4 * g + n0)) : 0.0f;
     st.h[i] = 0.0f;
   }
-  if (!FOLD && has_j) {
-    if (a.load_state == nullptr || sload(a.load_state + s) != 0) {
+  // The pool is written by the last stretch, and nothing orders the workgroups of a launch: where there are several
+  // stretches the fold of the first one alone reads it, and leaves the state in the last one's workspace entry, which no fold
+  // fills.
+  const int64_t held = (static_cast<int64_t>(s) * a.nseg + last) * a.channels + cj;
+  if (has_j && (FOLD ? seg == 0 : last == 0) && (a.load_state == nullptr || sload(a.load_state + s) != 0)) {
 #pragma unroll
-      for (int i = 0; i < 4 * M; ++i) st.h[i] = scan_state_load(a.state, st0 + 16 * (i / 4) + i % 4, a.state_dtype);
+    for (int i = 0; i < 4 * M; ++i) st.h[i] = scan_state_load(a.state, st0 + 16 * (i / 4) + i % 4, a.state_dtype);
+  }
+  if constexpr (FOLD) {
+    if (seg == 0) {
+#pragma unroll
+      for (int i = 0; i < 4 * M; ++i) {
+        if (has_j) gstore(a.ws_h + held * N + 4 * g + 16 * (i / 4) + i % 4, st.h[i]);
+        st.h[i] = 0.0f;
+      }
     }
+  } else if (has_j && last > 0) {
+#pragma unroll
+    for (int i = 0; i < 4 * M; ++i) st.h[i] = gload(a.ws_h + held * N + 4 * g + 16 * (i / 4) + i % 4);
 #pragma unroll 4
     for (int k = 0; k < seg; ++k) {
       const int64_t at = (static_cast<int64_t>(s) * a.nseg + k) * a.channels + cj;
