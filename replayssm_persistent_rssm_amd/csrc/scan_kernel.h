@@ -339,8 +339,11 @@ __global__ __launch_bounds__(kScanBlock, IT == kF32 && N == 64 ? 1 : 2) void sca
       const int64_t at = (static_cast<int64_t>(s) * a.nseg + k) * a.channels + cj;
       const float sum = gload(a.ws_d + at);
 #pragma unroll
-      for (int i = 0; i < 4 * M; ++i)
-        st.h[i] = fmaf(__builtin_amdgcn_exp2f(sum * st.A[i]), st.h[i], gload(a.ws_h + at * N + 4 * g + 16 * (i / 4) + i % 4));
+      for (int i = 0; i < 4 * M; ++i) {
+        // from zero a stretch ends where its fold does, also where its steps together would grow a state past fp32
+        const float own = gload(a.ws_h + at * N + 4 * g + 16 * (i / 4) + i % 4);
+        st.h[i] = st.h[i] == 0.0f ? own : fmaf(__builtin_amdgcn_exp2f(sum * st.A[i]), st.h[i], own);
+      }
     }
   }
   float bias[4], D[4], dsum[4] = {0, 0, 0, 0};

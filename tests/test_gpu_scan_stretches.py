@@ -61,3 +61,17 @@ def test_the_start_goes_through_the_workspace(rp, it, st, n):
                                   z=p["z"], load=p["load"])
     ref.check(y, want, ref.scan_bound(want, m, y.dtype, ref.scan_chain(385, n)), "y")
     ref.check(pool, state, ref.scan_bound(state, sm, pool.dtype, ref.scan_chain(385, n)), "state")
+
+
+@pytest.mark.parametrize("n", [16, 32, 64])
+def test_nothing_grows_to_nothing(rp, n):
+    """States that start at zero and have not been written to yet stay zero, however far a stretch would have made them grow
+    (exp(96) here, past fp32)."""
+    p = scan.inputs([700, 690], 64, n, 1, "f32", "f32", seed=n)
+    d = scan.on_device(p)
+    assert workspace(rp, p, d, 700) > 0
+    p["A"][:, 3], p["A"][:, n - 1] = 1.0, 0.5
+    p["dt"][:] = 2.0
+    p["load"][:] = 0
+    p["x"][:690], p["x"][700:1380] = 0.0, 0.0
+    scan.check(rp, p, use=("D", "z", "load"), softplus=False)
