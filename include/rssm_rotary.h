@@ -88,7 +88,8 @@ typedef struct {
 } rssm_rotary_tables;
 
 /* Enqueue on `hip_stream`.  Angles are products and remainders in 64 bits (any int32 position), sines and
- * cosines and the rest fp32; each output is rounded once.  Values are the inputs' bytes. */
+ * cosines and the rest fp32; each output is rounded once.  Values, and the elements of a head past rot_dim, are the
+ * inputs' bytes. */
 rssm_status rssm_rotary_append(const rssm_rotary_desc *desc, const rssm_rotary_tables *tables, void *hip_stream);
 
 #ifdef __cplusplus

@@ -57,6 +57,33 @@ __device__ __forceinline__ void rotary_angle(int p, float f, float factor, float
   s *= factor;
 }
 
+// Eight elements in storage.
+template <int DT>
+struct Eight {
+  static constexpr int kParts = sizeof(typename Mma<DT>::elem) / 2;
+  u32x4 v[kParts];
+  __device__ __forceinline__ void load(const char* p) {
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) v[k] = ld<false, u32x4>(p + 16 * k);
+  }
+  __device__ __forceinline__ void store(char* p) const {
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) st<false>(p + 16 * k, v[k]);
+  }
+  __device__ __forceinline__ f32x8 get() const {
+    if constexpr (DT == kF32) return stack(__builtin_bit_cast(f32x4, v[0]), __builtin_bit_cast(f32x4, v[1]));
+    else return from_frag<DT>(__builtin_bit_cast(typename Mma<DT>::frag, v[0]));
+  }
+  __device__ __forceinline__ void set(f32x8 x) {
+    if constexpr (DT == kF32) {
+      v[0] = __builtin_bit_cast(u32x4, f32x4{x[0], x[1], x[2], x[3]});
+      v[1] = __builtin_bit_cast(u32x4, f32x4{x[4], x[5], x[6], x[7]});
+    } else {
+      v[0] = __builtin_bit_cast(u32x4, to_frag<DT>(x));
+    }
+  }
+};
+
 template <int DT, int D>
 __global__ __launch_bounds__(kRotaryBlock) void rotary_kernel(RotaryArgs a) {
   constexpr int es = sizeof(typename Mma<DT>::elem);
@@ -135,10 +162,17 @@ __global__ __launch_bounds__(kRotaryBlock) void rotary_kernel(RotaryArgs a) {
       src = (value ? a.v_new + token * a.v_stride * es : a.k_new + token * a.k_stride * es) + static_cast<int64_t>(kh) * D * es;
       dst = (value ? a.v : a.k) + (row + kh * a.head_stride) * es;
     }
-    f32x8 x = load8<DT>(src + v0 * 8 * es), y = load8<DT>(src + v1 * 8 * es);
-    if (turn && !value) turned(x, y);
-    store8<DT>(dst + v0 * 8 * es, x);
-    store8<DT>(dst + v1 * 8 * es, y);
+    Eight<DT> x, y;
+    x.load(src + v0 * 8 * es);
+    y.load(src + v1 * 8 * es);
+    if (turn && !value) {   // what is not turned keeps its bits (a conversion and back would make a signalling NaN a quiet one)
+      f32x8 p = x.get(), q = y.get();
+      turned(p, q);
+      x.set(p);
+      y.set(q);
+    }
+    x.store(dst + v0 * 8 * es);
+    y.store(dst + v1 * 8 * es);
   }
 }
 
