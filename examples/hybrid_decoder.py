@@ -92,12 +92,14 @@ class HybridDecoder:
         return cache["page"] * self.HKV * self.HD * self.embed.element_size()
 
     def fork(self, cache, src, dst):
-        """Sequences `dst`, which are empty, become copies of sequences `src`."""
+        """Sequences `dst`, which are empty, become copies of sequences `src`; all of them or, with an error, none."""
         i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=self.dev)                        # noqa: E731
         status = i32([0] * len(dst))
         rp.rssm_page_fork(cache["ptrs"], *self._pool(cache), i32(src), i32(dst), status, page_size=cache["page"],
                           page_bytes=self._page_bytes(cache), token_bytes=self._page_bytes(cache) // cache["page"])
         if status.any():
+            rp.rssm_page_release(*self._pool(cache), i32([d for d, s in zip(dst, status.tolist()) if s == rp.RSSM_PAGE_OK]),
+                                 page_size=cache["page"])
             raise RuntimeError(f"not forked: {status.tolist()}")
         for b, kept in zip(self.blocks, cache["layer"]):
             if b["kind"] != "attention":
@@ -122,9 +124,9 @@ class HybridDecoder:
             return live.item()
 
     def forward(self, cache, tokens):
-        """Logits after the last of each sequence's new tokens (a list of token lists, each possibly empty)."""
+        """Logits after the last of each sequence's new tokens (a list of token lists, each possibly empty).  Where a sequence does not
+        find its pages, an error, and the cache is as it was."""
         lens = [len(t) for t in tokens]
-        cache["length"] = [a + b for a, b in zip(cache["length"], lens)]
         starts = [0]
         for n in lens:
             starts.append(starts[-1] + n)
@@ -132,6 +134,10 @@ class HybridDecoder:
         i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=self.dev)                        # noqa: E731
         seq_start = i32(starts)
         rp.rssm_page_extend(*self._pool(cache), cache["rows"], i32(lens), cache["status"], page_size=cache["page"])
+        if cache["status"].any():        # appended all the same, these tokens would take the places of the row's last ones
+            rp.rssm_page_release(*self._pool(cache), cache["rows"], lengths=i32(cache["length"]), page_size=cache["page"])
+            raise RuntimeError(f"not extended: {cache['status'].tolist()}")
+        cache["length"] = [a + b for a, b in zip(cache["length"], lens)]
         x = self.embed[torch.tensor([t for s in tokens for t in s], device=self.dev)]
         residual, normed = torch.empty(N, self.D, device=self.dev), torch.empty_like(x)
         # the first norm: nothing but the embedding in the stream

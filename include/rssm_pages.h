@@ -66,7 +66,9 @@ typedef struct {
  *   src, dst     [num_items] int32: rows (fork), pages (copy); dst alone: rows (extend, release)
  *   lengths      [num_items] int32: tokens to add (extend), tokens of the fork (fork; NULL: all of the
  *                source's), tokens that stay (release; NULL: none)
- *   status       [num_items] int32, written (extend, fork): RSSM_PAGE_OK, _NONE, _REFUSED or _SHARED
+ *   status       [num_items] int32, written (extend, fork): RSSM_PAGE_OK, _NONE, _REFUSED or _SHARED.  A row whose
+ *                extend is not RSSM_PAGE_OK has its old kv_len: its new tokens must not be appended (their places, counted
+ *                back from kv_len, are those of its last tokens, on pages that other rows may hold too)
  *   live         [1] int32, written (compact): pages in use, which are the pages 0 .. live - 1 afterwards
  *   workspace    device memory of workspace_bytes (extend, fork, compact)
  * Contract: calls on one pool are ordered (one stream, or events); the tables agree with one another (a pool starts with page_table -1, kv_len 0 and page_ref 0
@@ -97,8 +99,8 @@ rssm_status rssm_page_extend(const rssm_pages_desc *desc, const rssm_pages_table
 /* Rows dst[i], which are empty, become the first min(lengths[i], kv_len[src[i]]) tokens of rows src[i]: full pages are
  * shared (counted once more), the tokens of a last page that is not full are copied to a page of the fork's
  * own, in every cache.  Several items may have one source; sources are
- * taken as they were when the call began.  Of rows named twice as a destination the first item counts.  A
- * shared page is never written to again: rows grow on pages of their own. */
+ * taken as they were when the call began.  Of rows named twice as a destination the first item counts.  These calls
+ * never write to a shared page again: rows grow on pages of their own. */
 rssm_status rssm_page_fork(const rssm_pages_desc *desc, const rssm_pages_tables *tables, void *hip_stream);
 
 /* Rows dst[i] keep their first lengths[i] tokens (none without lengths); pages past them are given back, those that

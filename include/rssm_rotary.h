@@ -71,7 +71,8 @@ typedef struct {
  *   inv_freq          [rot_dim / 2] fp32, finite
  * Without keys and with positions, seq_start and kv_len may be NULL.  Rows of no sequence are left
  * untouched (without seq_start all rows are turned).  Guards against faults: as in rssm_paged_append; a token
- * that the append skips (negative position, page outside the pool) still has its query turned.
+ * that the append skips (negative position, page outside the pool) still has its query turned.  kv_len counts the new
+ * tokens: rows that rssm_page_extend refused must have none here, or their new tokens overwrite their last ones.
  * Alignment: q, q_out, k_new, v_new and caches 16 bytes, their strides multiples of 16 bytes; the others 4 bytes. */
 typedef struct {
   const void *q;

@@ -1254,7 +1254,8 @@ def rssm_page_extend(page_table, kv_len, page_ref, rows, add, status, *, page_si
     is advanced.  page_table int32 [R, pages] (-1 where none), kv_len int32
     [R], page_ref int32 [P]; rows, add and status int32 [n].  status[i]:
     RSSM_PAGE_OK, or RSSM_PAGE_NONE (too few free pages), RSSM_PAGE_REFUSED (bad or repeated row, bad length)
-    or RSSM_PAGE_SHARED (the partly filled last page belongs to another row too), and the row is as it was.  workspace: uint8
+    or RSSM_PAGE_SHARED (the partly filled last page belongs to another row too), and the row is as it was: look at it before
+    the new tokens are appended, which would otherwise take the places of the row's last ones.  workspace: uint8
     tensor of rssm_pages_workspace's size; allocated when not given."""
     if stream is None:
         mod, device, current = _fast()
