@@ -606,7 +606,7 @@ _calls = None
 def _fast():
     """The marshalling extension (loaded on first use, after torch): each of its
     functions enqueues a call whose tensors are all contiguous and as expected, and
-    returns False otherwise."""
+    returns False otherwise (those of _enqueued may return a status)."""
     global _calls
     if _calls is None:
         import torch  # noqa: F401  (the extension needs its libraries)
@@ -620,6 +620,14 @@ def _fast():
         spec.loader.exec_module(mod)
         _calls = (mod, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
     return _calls
+
+
+def _enqueued(done) -> bool:
+    """What the extension returned for a call that may not be started over: whether it was enqueued, or the status of
+    a launch that failed, which is raised."""
+    if done is True or done is False:
+        return done
+    raise RssmError(done, rssm_last_error())
 
 
 def _code(dt) -> int:
@@ -1280,8 +1288,8 @@ def rssm_page_fork(cache_ptrs, page_table, kv_len, page_ref, src, dst, status, *
     if stream is None:
         mod, device, current = _fast()
         i = device()
-        if mod.page_fork(i, current(i), cache_ptrs, page_table, kv_len, page_ref, src, dst, status, page_size, page_bytes,
-                         page_bytes if page_stride is None else page_stride, token_bytes, lengths, workspace):
+        if _enqueued(mod.page_fork(i, current(i), cache_ptrs, page_table, kv_len, page_ref, src, dst, status, page_size, page_bytes,
+                                   page_bytes if page_stride is None else page_stride, token_bytes, lengths, workspace)):
             return
     desc, tab, dev = _pages_rows(page_table, kv_len, page_ref, page_size)
     _pages_items(desc, tab, dev, dst, "dst", src=("src", src), lengths=("lengths", lengths), status=("status", status))
@@ -1311,8 +1319,8 @@ def rssm_page_compact(cache_ptrs, page_table, kv_len, page_ref, live, *, page_si
     if stream is None:
         mod, device, current = _fast()
         i = device()
-        if mod.page_compact(i, current(i), cache_ptrs, page_table, kv_len, page_ref, live, page_size, page_bytes,
-                            page_bytes if page_stride is None else page_stride, workspace):
+        if _enqueued(mod.page_compact(i, current(i), cache_ptrs, page_table, kv_len, page_ref, live, page_size, page_bytes,
+                                      page_bytes if page_stride is None else page_stride, workspace)):
             return
     import torch
     desc, tab, dev = _pages_rows(page_table, kv_len, page_ref, page_size)

@@ -10,7 +10,7 @@
 // False, and the binding's Python code handles the call or names the error.  Nothing has been enqueued
 // then, unless a later launch of a call that has several failed: the binding's call then starts over, and only
 // the last launch of each writes what the caller sees.  (A page fork and a compaction change the tables with their
-// first launch: a launch that fails raises here and is not repeated.)
+// first launch: where one fails they return the library's status, which the binding raises, and are not repeated.)
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -32,7 +32,7 @@
 namespace {
 
 struct NotCommon {};   // leaves a function towards `return False`
-struct Failed {};      // leaves a function towards an exception with the library's error
+struct Failed { rssm_status status; };   // leaves a function towards `return status`
 
 void need(bool ok) {
   if (!ok) throw NotCommon();
@@ -142,9 +142,8 @@ PyObject* guarded(PyObject* const* a, Py_ssize_t n, F f, bool views = false) {
   bool done = false;
   try {
     done = plain(a, n, views) && f();
-  } catch (const Failed&) {
-    PyErr_SetString(PyExc_RuntimeError, rssm_last_error());
-    return nullptr;
+  } catch (const Failed& e) {
+    return PyLong_FromLong(e.status);
   } catch (...) {
     if (PyErr_Occurred()) PyErr_Clear();
     done = false;
@@ -493,7 +492,7 @@ at::Tensor pool_workspace(PyObject* given, int dev, rssm_pages_desc* d, rssm_pag
 
 // Whether a call of two launches, the first of which changes the tables, was enqueued.
 bool enqueued(rssm_status st) {
-  if (st == RSSM_ERR_HIP) throw Failed();
+  if (st == RSSM_ERR_HIP) throw Failed{st};
   return st == RSSM_OK;
 }
 
