@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import concurrent.futures
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -36,6 +37,8 @@ SOURCES = ["rssm_inst_f32.hip", "rssm_inst_bf16.hip", "rssm_inst_f16.hip", "rssm
            "rssm_linear_attention.hip", "rssm_paged_attention.hip", "rssm_block_norm.hip", "rssm_causal_conv.hip",
            "rssm_selective_scan.hip", "rssm_rotary.hip", "rssm_pages.hip"]
 POOL_SOURCES = ["rssm_pool.hip"]
+# Kernels that hold their states in registers: the build fails where the compiler spills one of them to scratch.
+NO_SCRATCH = ["rssm_inst_scan_f32.hip", "rssm_inst_scan_bf16.hip", "rssm_inst_scan_f16.hip"]
 # the binding's marshalling extension (host code against torch's headers)
 FAST_SOURCE = "fast_calls.cpp"
 FAST_PATH = os.path.join(PKG, "_fast_calls.so")
@@ -49,7 +52,8 @@ CFLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-Wall",
 
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [HIPCC] + CFLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
+    report = ["-Rpass-analysis=kernel-resource-usage"] if src in NO_SCRATCH else []
+    cmd = [HIPCC] + CFLAGS + report + ["-c", os.path.join(CSRC, src), "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -57,9 +61,23 @@ def _compile(src: str, verbose: bool) -> str:
     noise = [ln for ln in res.stderr.splitlines() if "packed-fp32-ops" not in ln and ln.strip()]
     if res.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n" + "\n".join(noise))
+    if report:
+        _check_scratch(src, res.stderr)
+        noise = [ln for ln in noise if "warning" in ln]
     if noise and verbose:
         print("\n".join(noise), file=sys.stderr)
     return obj
+
+
+def _check_scratch(src: str, report: str) -> None:
+    """Raise where the compiler's resource report of `src` has a kernel with scratch memory, or no kernel."""
+    kernels = re.findall(r"Function Name: (\S+)|ScratchSize \[bytes/lane\]: (\d+)", report)
+    names, sizes = [n for n, _ in kernels if n], [int(s) for _, s in kernels if s]
+    if not names or len(names) != len(sizes):
+        raise RuntimeError(f"no resource report of the kernels in {src}")
+    spilled = [f"{n} ({s} bytes a lane)" for n, s in zip(names, sizes) if s > 0]
+    if spilled:
+        raise RuntimeError(f"kernels of {src} use scratch memory: " + ", ".join(spilled))
 
 
 def _link(objs, path: str, verbose: bool) -> None:
