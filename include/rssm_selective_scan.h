@@ -67,7 +67,8 @@ typedef struct {
 
 /* Device tensors:
  *   state          [slots][channels][dstate] state dtype, read and written
- *   A              [channels][dstate] fp32 (-infinity: a state that keeps nothing of earlier tokens)
+ *   A              [channels][dstate] fp32 (-infinity: a state that keeps nothing of earlier tokens; steps below 2^-120
+ *                  count as ones of size 0 or little more there, and a step of size 0 leaves every state as it is)
  *   D, dt_bias     [channels] fp32 each, or NULL
  *   x, dt, z, y    [num_tokens][channels] input dtype (z may be NULL)
  *   B, C           [num_tokens][groups][dstate] input dtype

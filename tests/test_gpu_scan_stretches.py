@@ -37,6 +37,17 @@ def test_a_last_stretch_of_one_token(rp, lens, Ch, n, it, st):
         assert torch.equal(again, y) and torch.equal(st2, pool)
 
 
+@pytest.mark.parametrize("it", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("st", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,G", [(16, 1), (32, 4), (64, 2)])
+def test_every_type_and_number_of_states(rp, it, st, n, G):
+    """Resumed and new prompts, skipped slots, ends at, before and after the borders; all optional inputs and none."""
+    p = scan.inputs([385, 48, 49, 0, 47, 96, 330, 1], 192, n, G, it, st, seed=n, slots=[3, 0, 7, 5, 2, 9, -1, 8])
+    assert workspace(rp, p, scan.on_device(p), 385) > 0
+    scan.check(rp, p)
+    scan.check(rp, p, use=("load",))
+
+
 @pytest.mark.parametrize("it,st,n", [("bf16", "f32", 16), ("f16", "bf16", 32), ("f32", "f16", 64)])
 def test_the_start_goes_through_the_workspace(rp, it, st, n):
     """The first launch leaves it in the entry of the sequence's last stretch (of 9, 48 tokens each), zeros where
