@@ -182,6 +182,12 @@ def _load():
         raise ImportError(
             f"{LIB_PATH} is not built. Build it with `python replayssm_persistent_rssm_amd/build.py` "
             "(or __graft_entry__.build()); there is no fallback path.")
+    # torch brings a HIP runtime of its own.  Loaded first, it serves this library too; loaded second, there would be
+    # two, and a launch on a stream of the other one fails.
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        pass
     lib = ctypes.CDLL(LIB_PATH)
     lib.rssm_materialize.argtypes = [ctypes.POINTER(RssmDesc), ctypes.POINTER(RssmTables), ctypes.c_void_p]
     lib.rssm_materialize.restype = ctypes.c_int
