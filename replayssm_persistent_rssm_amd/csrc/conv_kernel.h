@@ -9,11 +9,12 @@
 //    first_tile(s) = floor(start_s / T) + s: at least ceil(length / T) of them whatever the lengths, without a
 //    prefix sum and without knowing the longest sequence.  The state is read and written by a sequence's first tile
 //    alone (tiles are longer than W - 1 tokens), so no other wavefront sees it change.  12 ragged prompts up to 2,011
-//    tokens, 18,432 bf16 channels: 192 us, 5.3 TB/s, above the rate of a large copy (4.9) on the same card; past
-//    the caches 3% faster alone, but then the kernel that reads y next finds none of it.
+//    tokens, 18,432 bf16 channels (a gigabyte): 192 us, 5.3 TB/s, above the rate of a large copy (4.9) on the same card; with loads
+//    and stores past the caches 3% faster alone, but then the kernel that reads y next finds none of it.
 //  * conv_step_kernel: a lane takes the same channels of several requests, so that the weights
 //    (4 W bytes a channel, as much as a request's own traffic) are read once for them.  256 requests of 18,432 bf16
-//    channels: 13.7 us, 5.5 TB/s (past the caches 17.2).
+//    channels: 13.8 us, 5.5 TB/s with the 47 MB of its tensors in the last cache, 22.0 over sets of them past it in turn (a plain
+//    copy of as many bytes: 11.3 and 16.2); loads and stores that go past the caches 17.2 in the first case.
 #pragma once
 
 #include "mma_device.h"

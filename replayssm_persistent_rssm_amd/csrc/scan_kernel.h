@@ -21,8 +21,9 @@
 // the main kernel starts each stretch from those of the stretches before it.  The state pool is read by one launch
 // and written by the other.
 // 12 ragged prompts up to 2,011 tokens, 8,192 bf16 channels of 16 states: 417 us, the vector ALUs busy throughout (416
-// instructions a tile, 256 of them the four an element); one of 16,384 tokens, 4,096 channels: 414 us in 24
-// stretches, 147 us of vector work in the fold and 218 in the main kernel.
+// instructions a tile, 256 of them the four an element); one of 16,384 tokens, 4,096 channels: 413 us in 24
+// stretches, 169 us in the fold and 243 in the main kernel (many calls in turn; 470 in the first few after a pause, at
+// lower clocks).
 // scan_step_kernel: a lane has 16 bytes of a channel's states; bound by reading and writing the state.
 #pragma once
 
@@ -694,7 +695,7 @@ __device__ __forceinline__ float scan_step_piece(u32x4& raw, float d, float dx, 
 // Q requests a wavefront, which share A, D and bias.  LPC lanes hold a channel's states, 16 bytes each; a wavefront takes R
 // pieces of 64 / LPC channels that follow one another.  The step sizes, inputs and outputs of piece r are those of the
 // lanes r modulo R: one load, one softplus and one gate a lane for R channels.  256 requests of 8,192 channels, fp16
-// with 16 fp32 states: 50.9 us, 5.6 TB/s (a kilobyte of each of four requests a wavefront instead of four of one: 57 us).
+// with 16 fp32 states: 52 us, 5.5 TB/s, also over pools past the caches in turn (a kilobyte of each of four requests a wavefront instead of four of one: 57 us).
 template <int IT, int ST, int N, int Q>
 __global__ __launch_bounds__(kScanBlock) void scan_step_kernel(ScanArgs a) {
   typedef typename Mma<IT>::elem elem;
