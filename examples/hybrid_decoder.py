@@ -131,6 +131,8 @@ class HybridDecoder:
         for n in lens:
             starts.append(starts[-1] + n)
         N, single = starts[-1], all(n == 1 for n in lens)
+        if N == 0:
+            return self.head.new_empty(0, self.VOCAB)
         i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=self.dev)                        # noqa: E731
         seq_start = i32(starts)
         rp.rssm_page_extend(*self._pool(cache), cache["rows"], i32(lens), cache["status"], page_size=cache["page"])
@@ -208,11 +210,14 @@ def prefill(model, cache, prompts, chunk):
             done[i] += len(p)
             if p:
                 logits[i] = next(out)
-    return torch.stack([row for row in logits if row is not None])
+    rows = [row for row in logits if row is not None]
+    return torch.stack(rows) if rows else model.head.new_empty(0, model.VOCAB)
 
 
 def generate(model, prompts, steps, chunk):
-    """Greedy tokens of each prompt, and the logits of every step."""
+    """Greedy tokens of each prompt (of a token or more), and the logits of every step."""
+    if not all(prompts):
+        raise ValueError("a prompt without tokens has nothing to go on from")
     cache = model.new_cache(len(prompts), max(len(p) for p in prompts) + steps)
     logits = [prefill(model, cache, prompts, chunk)]
     tokens = [[] for _ in prompts]

@@ -45,3 +45,15 @@ def test_a_refused_fork_beside_others(ex):  # noqa: F811
     out = m.forward(c, [[7], [8], [9], []])
     for got, text in zip(out, (base + [7], other + [8], base + [9])):
         close(got, ex.prefill(m, m.new_cache(1, 32), [text], 1000)[0])
+
+
+def test_nothing_to_do(ex):  # noqa: F811
+    """No tokens at all: no logits, nothing changed.  A prompt of none cannot be continued."""
+    m = ex.HybridDecoder(dtype="f32")
+    c = m.new_cache(2, 32)
+    assert ex.prefill(m, c, [[], []], 10).shape == (0, m.VOCAB)
+    ex.prefill(m, c, [tokens(ex, 5, 5), []], 10)
+    before = snapshot(m, c)
+    assert m.forward(c, [[], []]).shape == (0, m.VOCAB) and same(before, snapshot(m, c))
+    with pytest.raises(ValueError, match="without tokens"):
+        ex.generate(m, [[1, 2], []], 3, 10)
