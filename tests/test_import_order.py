@@ -20,7 +20,7 @@ PACKAGE = "replayssm_persistent_rssm_amd"
 
 
 def run(order, more=""):
-    subprocess.run([sys.executable, "-c", CODE.format(order=order, more=more)], cwd=ROOT, check=True, timeout=100)
+    subprocess.run([sys.executable, "-c", CODE.format(order=order, more=more)], cwd=ROOT, check=True, timeout=300)
 
 
 @pytest.mark.parametrize("order", [(PACKAGE, "torch"), ("torch", PACKAGE)])
